@@ -62,6 +62,16 @@ extern "C" {
                                  OIDN_E_UNSUPPORTED                                   */
 #define OIDN_TRANSFER_LOG  1  /* F(x) = ln(1 + x), F^-1(y) = exp(y) - 1 (reading)    */
 
+/* ---- activations of the dense operators ---------------------------------- */
+#define OIDN_ACT_NONE  0
+#define OIDN_ACT_RELU  1   /* max(z, 0), slope 0 at 0                          */
+#define OIDN_ACT_SILU  2   /* z / (1 + exp(-z))                                */
+#define OIDN_ACT_GELU  3   /* z (1 + erf(z / sqrt 2)) / 2                      */
+
+/* ---- flags of the dense operators ---------------------------------------- */
+#define OIDN_X_CKPT8  1u   /* x is a checkpoint (oidn_ckpt_pack), its pitch unused */
+#define OIDN_Z_CKPT8  2u   /* z is held in 8 bits                              */
+
 /* ---- limits ------------------------------------------------------------ */
 #define OIDN_MAX_SOURCE_CHANNELS 256   /* logical channels per conv source */
 #define OIDN_MAX_OUT_CHANNELS    128
@@ -359,6 +369,93 @@ int oidn_unet_forward_timed(const void* d_weights, int in_channels, const float*
                             int transfer, float input_scale, int max_tile, int overlap,
                             void* workspace, size_t ws_bytes, float* out_rgba, int dtype,
                             hipStream_t stream, void* const* events, int n_events);
+
+/* ========================================================================
+ * Dense operators over activation rows.  An NHWC activation of h x w pixels
+ * is a matrix of m = h * w rows of channels; its row pitch (`ld...`, in
+ * elements, >= the row's columns) is the stored channel count, so any run of
+ * channels of a wider tensor is a matrix too.  Weights are row-major with one
+ * row per output channel, in dtype; biases and their gradients are float32.
+ * Sums, activations and slopes are fp32; every output is rounded once, to
+ * nearest even, where it is stored.  fp16 outputs beyond 65504 become
+ * infinite.  Results do not depend on timing: a call with the same arguments
+ * gives the same bits.
+ *
+ * Any size and pitch works and any element-aligned base; bases and pitches
+ * that are multiples of 16 bytes are fastest.  m may be 0 (sums over no rows
+ * are 0, nothing else is written).  Outputs must not overlap inputs, except
+ * that `residual` may be y and `add` may be dx (same pitch).  Columns between
+ * a row's end and its pitch are neither read nor written.  Column counts
+ * above 2^24 and matrices above 2^38 elements: OIDN_E_UNSUPPORTED.
+ *
+ * The workspace (16-byte aligned, the size the matching *_workspace_bytes
+ * call gives) holds nothing between calls.
+ * ======================================================================== */
+
+/* 8-bit activation checkpoints: what a forward pass keeps for its backward
+ * pass, at half the bytes of a 16-bit type.  A row's columns go in blocks of
+ * 32 that share a scale:
+ *   s = bf16(max|x| / 127),  q = rint(x / s) in [-127, 127],  value = q s.
+ * Layout of an m x n checkpoint: m rows of int8 codes, padded to whole blocks
+ * (padding holds 0), then one bf16 scale per row and block.  Blocks with
+ * s < 2^-120 are stored as zeros; a block with an infinity or a NaN reads back
+ * as NaN.  The buffer is 16-byte aligned. */
+int oidn_ckpt_bytes(long m, long n, size_t* bytes);
+int oidn_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
+                   hipStream_t stream);
+int oidn_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ldy, int dtype,
+                     hipStream_t stream);
+
+/* Dense layer (a 1 x 1 convolution):
+ *   z = x w^T + bias,  y = act(z) + residual
+ * x: m x k, w: n x k, bias: n floats or NULL, residual: m x n or NULL, y: m x n.
+ * z, if not NULL, receives the pre-activation for the backward pass: m x n of
+ * dtype at pitch ldz or, with OIDN_Z_CKPT8, a checkpoint of it. */
+int oidn_linear_workspace_bytes(long m, int k, int n, int dtype, size_t* bytes);
+int oidn_linear(const void* x, long ldx, const void* w, long ldw, const float* bias,
+                const void* residual, long ldr, void* y, long ldy, void* z, long ldz, long m, int k,
+                int n, int act, int dtype, unsigned flags, void* workspace, size_t ws_bytes,
+                hipStream_t stream);
+
+/* Its gradients, from dy (m x n):
+ *   dz = dy act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum of dz's rows
+ * (the residual's gradient is dy itself; dz, and an x read from 8 bits, are
+ * rounded to dtype before the products).  dx, dw and dbias may each be NULL.
+ * z as saved by oidn_linear (unused with OIDN_ACT_NONE); x as given to it, or
+ * with OIDN_X_CKPT8 a checkpoint of it. */
+int oidn_linear_backward_workspace_bytes(long m, int k, int n, int act, int dtype, unsigned flags,
+                                         size_t* bytes);
+int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, const void* z, long ldz,
+                         const void* w, long ldw, void* dx, long lddx, void* dw, long lddw,
+                         float* dbias, long m, int k, int n, int act, int dtype, unsigned flags,
+                         void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Gated feed-forward block over rows of d channels with f hidden ones:
+ *   [a | b] = x w_in^T + b_in,  h = act(a) * b,  y = h w_out^T + b_out + residual
+ * w_in: 2f x d (the f gate rows, then the f up rows), w_out: d x f, both
+ * contiguous; b_in (2f), b_out (d) and residual (m x d) may be NULL.  h is
+ * rounded to dtype between the two products.  z, if not NULL, receives [a | b]
+ * for the backward pass: m x 2f of dtype, contiguous, or with OIDN_Z_CKPT8 two
+ * m x f checkpoints one after the other (a, then b; 2 oidn_ckpt_bytes(m, f)). */
+int oidn_ffn_workspace_bytes(long m, int d, int f, int dtype, size_t* bytes);
+int oidn_ffn(const void* x, long ldx, const void* w_in, const float* b_in, const void* w_out,
+             const float* b_out, const void* residual, long ldr, void* y, long ldy, void* z, long m,
+             int d, int f, int act, int dtype, unsigned flags, void* workspace, size_t ws_bytes,
+             hipStream_t stream);
+
+/* Its gradients, from dy (m x d):
+ *   dh = dy w_out,  da = dh b act'(a),  db = dh act(a),
+ *   dx = [da | db] w_in + add,  dw_in = [da | db]^T x,  dw_out = dy^T h,
+ *   db_in = sum of [da | db]'s rows,  db_out = sum of dy's rows
+ * add (m x d or NULL) is what else reaches x: dy where x is also the residual.
+ * da, db, h and an x read from 8 bits are rounded to dtype before the products
+ * that read them.  Any of dx, dw_in, db_in, dw_out, db_out may be NULL. */
+int oidn_ffn_backward_workspace_bytes(long m, int d, int f, int dtype, unsigned flags, size_t* bytes);
+int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const void* z,
+                      const void* w_in, const void* w_out, const void* add, long ldadd, void* dx,
+                      long lddx, void* dw_in, float* db_in, void* dw_out, float* db_out, long m, int d,
+                      int f, int act, int dtype, unsigned flags, void* workspace, size_t ws_bytes,
+                      hipStream_t stream);
 
 /* Measurement helper, not part of the denoise path: `blocks` workgroups of
  * 4 waves, each wave issuing iters x 8 independent 16x16x32 MFMAs (fp16, or

@@ -31,6 +31,14 @@ OIDN_POOL2X2 = 2
 OIDN_TRANSFER_PU = 0
 OIDN_TRANSFER_LOG = 1
 
+OIDN_ACT_NONE = 0
+OIDN_ACT_RELU = 1
+OIDN_ACT_SILU = 2
+OIDN_ACT_GELU = 3
+
+OIDN_X_CKPT8 = 1
+OIDN_Z_CKPT8 = 2
+
 OIDN_TILE_ALIGN = 16
 OIDN_DEFAULT_OVERLAP = 96
 OIDN_NOALLOC_SCRATCH_MB = 64
@@ -45,6 +53,9 @@ EXPORTS = (
     "oidn_unet_workspace_bytes", "oidn_unet_tile_batch", "oidn_unet_input_layout",
     "oidn_unet_forward",
     "oidn_unet_forward_timed", "oidn_unet_forward_noalloc", "oidn_unet_noalloc_scratch_bytes",
+    "oidn_ckpt_bytes", "oidn_ckpt_pack", "oidn_ckpt_unpack",
+    "oidn_linear_workspace_bytes", "oidn_linear", "oidn_linear_backward_workspace_bytes", "oidn_linear_backward",
+    "oidn_ffn_workspace_bytes", "oidn_ffn", "oidn_ffn_backward_workspace_bytes", "oidn_ffn_backward",
     "oidn_calibrate_mfma", "oidn_calibrate_read", "oidn_event_create", "oidn_event_destroy", "oidn_event_elapsed_ms",
 )
 
@@ -64,6 +75,7 @@ class oidn_tile(ctypes.Structure):
 
 
 _lib = None
+_l = ctypes.c_long
 _vp, _i, _u, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_float, ctypes.c_size_t
 _SIGS = {
     "oidn_last_error": ([], ctypes.c_char_p),
@@ -102,6 +114,21 @@ _SIGS = {
     "oidn_unet_forward_noalloc": ([_vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _i, _vp, _i,
                                    _vp], _i),
     "oidn_unet_noalloc_scratch_bytes": ([ctypes.POINTER(_sz)], _i),
+    "oidn_ckpt_bytes": ([_l, _l, ctypes.POINTER(_sz)], _i),
+    "oidn_ckpt_pack": ([_vp, _l, _l, _l, _vp, _i, _vp], _i),
+    "oidn_ckpt_unpack": ([_vp, _l, _l, _vp, _l, _i, _vp], _i),
+    "oidn_linear_workspace_bytes": ([_l, _i, _i, _i, ctypes.POINTER(_sz)], _i),
+    "oidn_linear": ([_vp, _l, _vp, _l, _vp, _vp, _l, _vp, _l, _vp, _l, _l, _i, _i, _i, _i, _u, _vp, _sz,
+                     _vp], _i),
+    "oidn_linear_backward_workspace_bytes": ([_l, _i, _i, _i, _i, _u, ctypes.POINTER(_sz)], _i),
+    "oidn_linear_backward": ([_vp, _l, _vp, _l, _vp, _l, _vp, _l, _vp, _l, _vp, _l, _vp, _l, _i, _i, _i, _i,
+                              _u, _vp, _sz, _vp], _i),
+    "oidn_ffn_workspace_bytes": ([_l, _i, _i, _i, ctypes.POINTER(_sz)], _i),
+    "oidn_ffn": ([_vp, _l, _vp, _vp, _vp, _vp, _vp, _l, _vp, _l, _vp, _l, _i, _i, _i, _i, _u, _vp, _sz,
+                  _vp], _i),
+    "oidn_ffn_backward_workspace_bytes": ([_l, _i, _i, _i, _u, ctypes.POINTER(_sz)], _i),
+    "oidn_ffn_backward": ([_vp, _l, _vp, _l, _vp, _vp, _vp, _vp, _l, _vp, _l, _vp, _vp, _vp, _vp, _l, _i, _i,
+                           _i, _i, _u, _vp, _sz, _vp], _i),
     "oidn_calibrate_mfma": ([_i, ctypes.c_long, _i, _vp, ctypes.POINTER(ctypes.c_longlong), _vp], _i),
     "oidn_calibrate_read": ([_vp, _sz, _vp, _vp], _i),
     "oidn_event_create": ([ctypes.POINTER(_vp)], _i),
@@ -392,6 +419,69 @@ def oidn_unet_noalloc_scratch_bytes() -> int:
     n = _sz()
     _check(lib().oidn_unet_noalloc_scratch_bytes(ctypes.byref(n)))
     return n.value
+
+
+# -------------------------------------------- dense operators over rows
+def _size(fn, *args) -> int:
+    n = _sz()
+    _check(fn(*args, ctypes.byref(n)))
+    return n.value
+
+
+def oidn_ckpt_bytes(m: int, n: int) -> int:
+    return _size(lib().oidn_ckpt_bytes, m, n)
+
+
+def oidn_ckpt_pack(x, ldx: int, m: int, n: int, ckpt, dtype: int, stream=None):
+    _check(lib().oidn_ckpt_pack(_p(x), ldx, m, n, _p(ckpt), dtype, _s(stream)))
+
+
+def oidn_ckpt_unpack(ckpt, m: int, n: int, y, ldy: int, dtype: int, stream=None):
+    _check(lib().oidn_ckpt_unpack(_p(ckpt), m, n, _p(y), ldy, dtype, _s(stream)))
+
+
+def oidn_linear_workspace_bytes(m: int, k: int, n: int, dtype: int) -> int:
+    return _size(lib().oidn_linear_workspace_bytes, m, k, n, dtype)
+
+
+def oidn_linear(x, ldx: int, w, ldw: int, bias, residual, ldr: int, y, ldy: int, z, ldz: int, m: int,
+                k: int, n: int, act: int, dtype: int, flags: int, workspace, ws_bytes: int, stream=None):
+    _check(lib().oidn_linear(_p(x), ldx, _p(w), ldw, _p(bias), _p(residual), ldr, _p(y), ldy, _p(z), ldz,
+                             m, k, n, act, dtype, flags, _p(workspace), ws_bytes, _s(stream)))
+
+
+def oidn_linear_backward_workspace_bytes(m: int, k: int, n: int, act: int, dtype: int, flags: int) -> int:
+    return _size(lib().oidn_linear_backward_workspace_bytes, m, k, n, act, dtype, flags)
+
+
+def oidn_linear_backward(dy, lddy: int, x, ldx: int, z, ldz: int, w, ldw: int, dx, lddx: int, dw, lddw: int,
+                         dbias, m: int, k: int, n: int, act: int, dtype: int, flags: int, workspace,
+                         ws_bytes: int, stream=None):
+    _check(lib().oidn_linear_backward(_p(dy), lddy, _p(x), ldx, _p(z), ldz, _p(w), ldw, _p(dx), lddx,
+                                      _p(dw), lddw, _p(dbias), m, k, n, act, dtype, flags, _p(workspace),
+                                      ws_bytes, _s(stream)))
+
+
+def oidn_ffn_workspace_bytes(m: int, d: int, f: int, dtype: int) -> int:
+    return _size(lib().oidn_ffn_workspace_bytes, m, d, f, dtype)
+
+
+def oidn_ffn(x, ldx: int, w_in, b_in, w_out, b_out, residual, ldr: int, y, ldy: int, z, m: int, d: int,
+             f: int, act: int, dtype: int, flags: int, workspace, ws_bytes: int, stream=None):
+    _check(lib().oidn_ffn(_p(x), ldx, _p(w_in), _p(b_in), _p(w_out), _p(b_out), _p(residual), ldr, _p(y),
+                          ldy, _p(z), m, d, f, act, dtype, flags, _p(workspace), ws_bytes, _s(stream)))
+
+
+def oidn_ffn_backward_workspace_bytes(m: int, d: int, f: int, dtype: int, flags: int) -> int:
+    return _size(lib().oidn_ffn_backward_workspace_bytes, m, d, f, dtype, flags)
+
+
+def oidn_ffn_backward(dy, lddy: int, x, ldx: int, z, w_in, w_out, add, ldadd: int, dx, lddx: int, dw_in,
+                      db_in, dw_out, db_out, m: int, d: int, f: int, act: int, dtype: int, flags: int,
+                      workspace, ws_bytes: int, stream=None):
+    _check(lib().oidn_ffn_backward(_p(dy), lddy, _p(x), ldx, _p(z), _p(w_in), _p(w_out), _p(add), ldadd,
+                                   _p(dx), lddx, _p(dw_in), _p(db_in), _p(dw_out), _p(db_out), m, d, f,
+                                   act, dtype, flags, _p(workspace), ws_bytes, _s(stream)))
 
 
 def oidn_calibrate_mfma(dtype: int, iters: int, blocks: int, sink, stream=None) -> int:

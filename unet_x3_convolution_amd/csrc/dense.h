@@ -1,0 +1,124 @@
+// Internal declarations of the dense operators over activation rows: matrix
+// products with fused epilogues, the gated feed-forward block, and 8-bit
+// activation checkpoints.
+#pragma once
+
+#include "internal.h"
+
+namespace oidn {
+
+// ---------------------------------------------------------------------------
+// 8-bit checkpoint of an m x n matrix: int8 codes, rows padded to whole blocks
+// of 32 columns, then one bf16 scale per row and block.
+// ---------------------------------------------------------------------------
+constexpr int kCkptBlock = 32;
+inline long ckpt_cols(long n) { return (n + kCkptBlock - 1) / kCkptBlock * kCkptBlock; }
+inline size_t ckpt_bytes(long m, long n) {
+  const size_t codes = (size_t)m * (size_t)ckpt_cols(n);
+  return align256(codes + codes / (kCkptBlock / 2));
+}
+
+// ---------------------------------------------------------------------------
+// Products C[i][j] = sum_l Q(i, l) P(j, l), i < rows, j < cols, l < len.
+// An operand is either stored with l fastest (element (i, l) at i * ld + l) or
+// "strided" (element (i, l) at l * ld + i):
+//   forward  y = x w^T:    Q = x, P = w            both l-fastest
+//   input    dx = dz w:    Q = dz, P = w           P strided
+//   weight   dw = dz^T x:  Q = dz, P = x           both strided
+// ---------------------------------------------------------------------------
+enum DenseLayout { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
+
+// What happens to the sums.
+enum DenseEpilogue {
+  kEpiLinear = 0,     // bias, saved z, activation, residual, store
+  kEpiPartial = 1,    // fp32 sums of one slice of l to the workspace
+  kEpiGated = 2,      // columns j and f + j of one product: h = act(a) * b
+  kEpiGatedBack = 3,  // dh with the saved z: h, da, db and column sums of da, db
+};
+
+// Bits of EpilogueArgs::vec: the tensor takes 16-byte accesses (base and row
+// pitch multiples of 16 bytes).
+enum DenseVec { kVecRes = 1, kVecY = 2, kVecZ = 4, kVecH = 8 };
+
+struct EpilogueArgs {
+  const float* bias;       // cols floats (kEpiGated: 2 * cols), may be null
+  const void* res;         // rows x cols, row pitch ldr, may be null
+  long ldr;
+  void* y;                 // rows x cols, row pitch ldy
+  long ldy;
+  void* z;                 // pre-activation, may be null: row pitch ldz, or checkpoint(s)
+  long ldz;
+  void* h;                 // kEpiGatedBack: rows x cols, contiguous
+  float* part;             // kEpiPartial: [slice][rows][cols]; kEpiGatedBack: column sums or null
+  int act;
+  unsigned vec;
+  int z8;                  // z is held in 8 bits
+  long rows;
+  int cols;
+};
+
+struct GemmArgs {
+  const void* q;
+  long ldq;
+  const void* p;
+  long ldp;
+  long len;                // summed length
+  int tiles_r, tiles_c;    // output tiles
+  int splits;              // slices of the summed length
+  long per_split;          // K tiles per slice
+  EpilogueArgs e;
+};
+
+// Tile shape and slices of a launch.
+struct GemmPlan {
+  int tile_r, tile_c;      // rows and columns of a workgroup's tile
+  int splits;
+  long per_split;
+};
+constexpr int kDenseK = 64;      // summed length of one staged 16-bit tile
+constexpr int kDenseKF32 = 32;   // the same in fp32
+GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int epi);
+// Row groups of kEpiGatedBack's column sums: one per wave row of every tile.
+long gated_back_groups(long rows, const GemmPlan& p);
+
+// 16-bit products, one entry for each layout.
+hipError_t launch_gemm16_forward(const GemmArgs& a, const GemmPlan& p, int epi, bool bf16, hipStream_t stream);
+hipError_t launch_gemm16_input(const GemmArgs& a, const GemmPlan& p, int epi, bool bf16, hipStream_t stream);
+hipError_t launch_gemm16_weight(const GemmArgs& a, const GemmPlan& p, int epi, bool bf16,
+                          hipStream_t stream);
+hipError_t launch_gemm_f32(const GemmArgs& a, const GemmPlan& p, int layout, int epi,
+                           hipStream_t stream);
+// Adds the slices of kEpiPartial and runs the epilogue (kEpiLinear).
+hipError_t launch_split_sum(const EpilogueArgs& e, const float* part, int splits, int dtype,
+                            hipStream_t stream);
+
+// dz = dy * act'(z) (dz may be null: column sums alone; act none: z unused)
+// and, with part, partial column sums of dz over `chunk` rows: part[r / chunk][n].
+struct SlopeArgs {
+  const void* dy;
+  long lddy;
+  const void* z;
+  long ldz;
+  int z8;
+  void* dz;                // contiguous rows x cols
+  float* part;
+  long rows;
+  int cols;
+  long chunk;
+  int act;
+  unsigned vec;            // bit 0: dy, bit 1: z, bit 2: dz take 16-byte accesses
+};
+long slope_chunk(long rows);
+hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream);
+// out[j] = sum over `groups` rows of part (fixed order); groups may be 0.
+hipError_t launch_column_sum(const float* part, long groups, int cols, float* out,
+                             hipStream_t stream);
+
+hipError_t launch_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
+                            hipStream_t stream);
+hipError_t launch_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ldy, int dtype,
+                              hipStream_t stream);
+// Zeros (a plain store kernel, so that a captured graph holds no memset node).
+hipError_t launch_zero(void* p, size_t bytes, hipStream_t stream);
+
+}  // namespace oidn

@@ -1,0 +1,552 @@
+// Host side of the dense operators' C ABI: argument checks, launch plans,
+// workspace layout and the launch sequences.  Nothing here allocates device
+// memory, waits for the device or throws.
+#include <cstdarg>
+#include <cstdio>
+
+#include "../../include/oidn_mi355x.h"
+#include "dense.h"
+
+using namespace oidn;
+
+namespace {
+
+int fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return set_error(code, buf);
+}
+int ran(hipError_t e, const char* what) {
+  return e == hipSuccess ? OIDN_OK : fail(OIDN_E_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+// Limits: columns index with 32-bit ints, and tiles and 8-column units of one
+// matrix have to fit a launch's grid.
+constexpr long kMaxColumns = 1L << 24;
+constexpr long kMaxRows = (1L << 31) - 1;
+constexpr long kMaxElements = 1L << 38;
+
+size_t esize(int dtype) { return dtype == OIDN_F32 ? 4 : 2; }
+size_t bytes_of(long rows, long cols, int dtype) {
+  return align256((size_t)rows * (size_t)cols * esize(dtype));
+}
+
+int check_type(int dtype) {
+  if (dtype == OIDN_F32 || dtype == OIDN_F16 || dtype == OIDN_BF16) return OIDN_OK;
+  return fail(OIDN_E_INVALID, "unknown dtype %d", dtype);
+}
+int check_size(const char* name, long rows, long cols) {
+  if (rows < 0 || cols < 1) return fail(OIDN_E_INVALID, "%s: %ld x %ld is not a size", name, rows, cols);
+  if (rows > kMaxRows || cols > kMaxColumns || rows > kMaxElements / cols)
+    return fail(OIDN_E_UNSUPPORTED, "%s: %ld x %ld is larger than the kernels index", name, rows, cols);
+  return OIDN_OK;
+}
+int check_act(int act) {
+  if (act >= OIDN_ACT_NONE && act <= OIDN_ACT_GELU) return OIDN_OK;
+  return fail(OIDN_E_INVALID, "unknown activation %d", act);
+}
+int check_flags(unsigned flags, unsigned known) {
+  if ((flags & ~known) == 0) return OIDN_OK;
+  return fail(OIDN_E_INVALID, "unknown flags 0x%x", flags & ~known);
+}
+int check_aligned(const char* name, const void* p, size_t to) {
+  if (reinterpret_cast<uintptr_t>(p) % to == 0) return OIDN_OK;
+  return fail(OIDN_E_INVALID, "%s must be aligned to %zu bytes", name, to);
+}
+// A matrix of `cols` columns at row pitch ld; may_be_null: absent is fine.
+int check_matrix(const char* name, const void* p, long ld, long cols, int dtype, bool may_be_null) {
+  if (!p) return may_be_null ? OIDN_OK : fail(OIDN_E_INVALID, "null pointer: %s", name);
+  if (ld < cols) return fail(OIDN_E_INVALID, "row pitch %ld of %s is less than its %ld columns", ld, name, cols);
+  if (ld > (1L << 32)) return fail(OIDN_E_UNSUPPORTED, "row pitch %ld of %s is above 2^32", ld, name);
+  return check_aligned(name, p, esize(dtype));
+}
+int check_blob(const char* name, const void* p) {
+  if (!p) return fail(OIDN_E_INVALID, "null pointer: %s", name);
+  return check_aligned(name, p, 16);
+}
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return OIDN_OK;
+  if (!ws) return fail(OIDN_E_INVALID, "null pointer: workspace");
+  const int rc = check_aligned("workspace", ws, 16);
+  if (rc) return rc;
+  if (have < need)
+    return fail(OIDN_E_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", have, need);
+  return OIDN_OK;
+}
+#define OIDN_TRY(expr)        \
+  do {                        \
+    const int rc_ = (expr);   \
+    if (rc_) return rc_;      \
+  } while (0)
+
+// Whether a tensor takes 16-byte accesses at every row and, with `step`, at
+// that many columns further.
+bool vec(const void* p, long ld, int dtype, long step = 0) {
+  const long e = (long)esize(dtype);
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * e % 16 == 0 && step * e % 16 == 0;
+}
+
+// One product: bytes of the workspace its slices take, and its launch.
+struct Product {
+  int layout, epi;
+  long rows, cols, len;
+  int dtype;
+  GemmPlan plan;
+};
+Product product(int layout, int epi, long rows, long cols, long len, int dtype) {
+  return {layout, epi, rows, cols, len, dtype, plan_gemm(rows, cols, len, dtype, epi)};
+}
+size_t product_bytes(const Product& p) {
+  return p.plan.splits > 1 ? align256((size_t)p.plan.splits * p.rows * p.cols * sizeof(float)) : 0;
+}
+int run_product(const Product& p, const void* q, long ldq, const void* pm, long ldp,
+                const EpilogueArgs& e, void* slices, hipStream_t stream) {
+  GemmArgs a{};
+  a.q = q;
+  a.ldq = ldq;
+  a.p = pm;
+  a.ldp = ldp;
+  a.len = p.len;
+  a.tiles_r = (int)((p.rows + p.plan.tile_r - 1) / p.plan.tile_r);
+  const long c = p.epi == kEpiGated ? p.plan.tile_c / 2 : p.plan.tile_c;
+  a.tiles_c = (int)((p.cols + c - 1) / c);
+  a.splits = p.plan.splits;
+  a.per_split = p.plan.per_split;
+  a.e = e;
+  a.e.rows = p.rows;
+  a.e.cols = (int)p.cols;
+  const bool split = p.plan.splits > 1;
+  const int epi = split ? kEpiPartial : p.epi;
+  if (split) a.e.part = static_cast<float*>(slices);
+  hipError_t r;
+  if (p.dtype == OIDN_F32) r = launch_gemm_f32(a, p.plan, p.layout, epi, stream);
+  else if (p.layout == kForward) r = launch_gemm16_forward(a, p.plan, epi, p.dtype == OIDN_BF16, stream);
+  else if (p.layout == kInputGrad) r = launch_gemm16_input(a, p.plan, epi, p.dtype == OIDN_BF16, stream);
+  else r = launch_gemm16_weight(a, p.plan, epi, p.dtype == OIDN_BF16, stream);
+  OIDN_TRY(ran(r, "matrix product launch"));
+  if (split)
+    OIDN_TRY(ran(launch_split_sum(a.e, a.e.part, p.plan.splits, p.dtype, stream), "slice sum launch"));
+  return OIDN_OK;
+}
+// The plain epilogue: store, with `add` (may be null) added.
+EpilogueArgs store_to(void* y, long ldy, const void* add, long ldadd, int dtype) {
+  EpilogueArgs e{};
+  e.y = y;
+  e.ldy = ldy;
+  e.res = add;
+  e.ldr = ldadd;
+  e.vec = (vec(y, ldy, dtype) ? kVecY : 0) | (add && vec(add, ldadd, dtype) ? kVecRes : 0);
+  return e;
+}
+
+// Workspace regions, handed out in order.
+struct Regions {
+  char* base;
+  size_t used;
+  void* take(size_t bytes) {
+    void* p = base ? base + used : nullptr;
+    used += bytes;
+    return p;
+  }
+};
+
+size_t most(size_t a, size_t b) { return a > b ? a : b; }
+
+// ---------------------------------------------------------------- linear
+struct LinearBack {
+  Product dx, dw;
+  long chunk, chunks;
+  void *dz, *x, *sums, *slices;
+  size_t bytes;
+};
+LinearBack linear_back(long m, int k, int n, int act, int dtype, unsigned flags, void* ws) {
+  LinearBack b{};
+  b.dx = product(kInputGrad, kEpiLinear, m, k, n, dtype);
+  b.dw = product(kWeightGrad, kEpiLinear, n, k, m, dtype);
+  b.chunk = slope_chunk(m);
+  b.chunks = (m + b.chunk - 1) / b.chunk;
+  Regions r{static_cast<char*>(ws), 0};
+  b.dz = act != OIDN_ACT_NONE ? r.take(bytes_of(m, n, dtype)) : nullptr;
+  b.x = flags & OIDN_X_CKPT8 ? r.take(bytes_of(m, k, dtype)) : nullptr;
+  b.sums = r.take(align256(b.chunks * (size_t)n * sizeof(float)));
+  b.slices = r.take(most(product_bytes(b.dx), product_bytes(b.dw)));
+  b.bytes = r.used;
+  return b;
+}
+
+int check_linear(long m, int k, int n, int dtype) {
+  OIDN_TRY(check_type(dtype));
+  OIDN_TRY(check_size("x", m, k));
+  OIDN_TRY(check_size("y", m, n));
+  return check_size("w", n, k);
+}
+
+// ------------------------------------------------------------------- ffn
+struct Ffn {
+  Product in, out;
+  void *h, *slices;
+  size_t bytes;
+};
+Ffn ffn_plan(long m, int d, int f, int dtype, void* ws) {
+  Ffn p{};
+  p.in = product(kForward, kEpiGated, m, f, d, dtype);
+  p.out = product(kForward, kEpiLinear, m, d, f, dtype);
+  Regions r{static_cast<char*>(ws), 0};
+  p.h = r.take(bytes_of(m, f, dtype));
+  p.slices = r.take(product_bytes(p.out));
+  p.bytes = r.used;
+  return p;
+}
+
+struct FfnBack {
+  Product dh, dx, dw_in, dw_out;
+  long groups, chunk, chunks;
+  void *h, *dz, *x, *in_sums, *out_sums, *slices;
+  size_t bytes;
+};
+FfnBack ffn_back(long m, int d, int f, int dtype, unsigned flags, void* ws) {
+  FfnBack b{};
+  b.dh = product(kInputGrad, kEpiGatedBack, m, f, d, dtype);
+  b.dx = product(kInputGrad, kEpiLinear, m, d, 2L * f, dtype);
+  b.dw_in = product(kWeightGrad, kEpiLinear, 2L * f, d, m, dtype);
+  b.dw_out = product(kWeightGrad, kEpiLinear, d, f, m, dtype);
+  b.groups = gated_back_groups(m, b.dh.plan);
+  b.chunk = slope_chunk(m);
+  b.chunks = (m + b.chunk - 1) / b.chunk;
+  Regions r{static_cast<char*>(ws), 0};
+  b.h = r.take(bytes_of(m, f, dtype));
+  b.dz = r.take(bytes_of(m, 2L * f, dtype));
+  b.x = flags & OIDN_X_CKPT8 ? r.take(bytes_of(m, d, dtype)) : nullptr;
+  b.in_sums = r.take(align256(b.groups * 2 * (size_t)f * sizeof(float)));
+  b.out_sums = r.take(align256(b.chunks * (size_t)d * sizeof(float)));
+  b.slices = r.take(most(product_bytes(b.dx), most(product_bytes(b.dw_in), product_bytes(b.dw_out))));
+  b.bytes = r.used;
+  return b;
+}
+
+int check_ffn(long m, int d, int f, int dtype) {
+  OIDN_TRY(check_type(dtype));
+  OIDN_TRY(check_size("x", m, d));
+  if (f < 1 || f > kMaxColumns / 2)
+    return fail(f < 1 ? OIDN_E_INVALID : OIDN_E_UNSUPPORTED, "hidden width %d is out of range", f);
+  OIDN_TRY(check_size("z", m, 2L * f));
+  return check_size("w_in", 2L * f, d);
+}
+
+// Column sums of dy (m x n) into out.
+int column_sums(const void* dy, long lddy, long m, int n, long chunk, long chunks, void* sums,
+                float* out, int dtype, hipStream_t stream) {
+  SlopeArgs s{};
+  s.dy = dy;
+  s.lddy = lddy;
+  s.part = static_cast<float*>(sums);
+  s.rows = m;
+  s.cols = n;
+  s.chunk = chunk;
+  s.act = OIDN_ACT_NONE;
+  s.vec = vec(dy, lddy, dtype) ? 1 : 0;
+  OIDN_TRY(ran(launch_slope(s, dtype, stream), "column sum launch"));
+  return ran(launch_column_sum(s.part, chunks, n, out, stream), "column sum launch");
+}
+
+}  // namespace
+
+namespace oidn {
+
+GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int epi) {
+  const long bk = dtype == OIDN_F32 ? kDenseKF32 : kDenseK;
+  const long kt = (len + bk - 1) / bk;
+  const long c128 = epi == kEpiGated ? 64 : 128;
+  const long big = ((rows + 127) / 128) * ((cols + c128 - 1) / c128);
+  GemmPlan p{128, 128, 1, kt};
+  // 128 x 128 tiles once they give every compute unit one; smaller ones until then
+  long tiles = big;
+  if (big < 256) {
+    p.tile_r = 64;
+    p.tile_c = epi == kEpiGated ? 128 : 64;
+    tiles = ((rows + 63) / 64) * ((cols + 63) / 64);
+  }
+  if (epi == kEpiLinear && tiles < 256 && kt >= 8) {
+    long s = (512 + tiles - 1) / tiles;
+    if (s > kt / 4) s = kt / 4;
+    if (s > 1) {
+      p.per_split = (kt + s - 1) / s;
+      p.splits = (int)((kt + p.per_split - 1) / p.per_split);
+    }
+  }
+  return p;
+}
+
+long gated_back_groups(long rows, const GemmPlan& p) {
+  return (rows + p.tile_r - 1) / p.tile_r * 2;
+}
+
+}  // namespace oidn
+
+extern "C" {
+
+// ------------------------------------------------------------ checkpoints
+int oidn_ckpt_bytes(long m, long n, size_t* bytes) {
+  if (!bytes) return fail(OIDN_E_INVALID, "null bytes pointer");
+  OIDN_TRY(check_size("checkpoint", m, n));
+  *bytes = ckpt_bytes(m, n);
+  return clear_error();
+}
+
+int oidn_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype, hipStream_t stream) {
+  OIDN_TRY(check_type(dtype));
+  OIDN_TRY(check_size("x", m, n));
+  if (m == 0) return clear_error();
+  OIDN_TRY(check_matrix("x", x, ldx, n, dtype, false));
+  OIDN_TRY(check_blob("checkpoint", ckpt));
+  OIDN_TRY(ran(launch_ckpt_pack(x, ldx, m, n, ckpt, dtype, stream), "checkpoint pack launch"));
+  return clear_error();
+}
+
+int oidn_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ldy, int dtype, hipStream_t stream) {
+  OIDN_TRY(check_type(dtype));
+  OIDN_TRY(check_size("y", m, n));
+  if (m == 0) return clear_error();
+  OIDN_TRY(check_matrix("y", y, ldy, n, dtype, false));
+  OIDN_TRY(check_blob("checkpoint", ckpt));
+  OIDN_TRY(ran(launch_ckpt_unpack(ckpt, m, n, y, ldy, dtype, stream), "checkpoint unpack launch"));
+  return clear_error();
+}
+
+// ----------------------------------------------------------------- linear
+int oidn_linear_workspace_bytes(long m, int k, int n, int dtype, size_t* bytes) {
+  if (!bytes) return fail(OIDN_E_INVALID, "null bytes pointer");
+  OIDN_TRY(check_linear(m, k, n, dtype));
+  *bytes = m ? product_bytes(product(kForward, kEpiLinear, m, n, k, dtype)) : 0;
+  return clear_error();
+}
+
+int oidn_linear(const void* x, long ldx, const void* w, long ldw, const float* bias,
+                const void* residual, long ldr, void* y, long ldy, void* z, long ldz, long m, int k,
+                int n, int act, int dtype, unsigned flags, void* workspace, size_t ws_bytes,
+                hipStream_t stream) {
+  OIDN_TRY(check_linear(m, k, n, dtype));
+  OIDN_TRY(check_act(act));
+  OIDN_TRY(check_flags(flags, OIDN_Z_CKPT8));
+  if (m == 0) return clear_error();
+  const bool z8 = flags & OIDN_Z_CKPT8;
+  OIDN_TRY(check_matrix("x", x, ldx, k, dtype, false));
+  OIDN_TRY(check_matrix("w", w, ldw, k, dtype, false));
+  OIDN_TRY(check_aligned("bias", bias, 4));
+  OIDN_TRY(check_matrix("residual", residual, ldr, n, dtype, true));
+  OIDN_TRY(check_matrix("y", y, ldy, n, dtype, false));
+  if (z8) OIDN_TRY(check_blob("z", z));
+  else OIDN_TRY(check_matrix("z", z, ldz, n, dtype, true));
+  const Product p = product(kForward, kEpiLinear, m, n, k, dtype);
+  OIDN_TRY(check_workspace(workspace, ws_bytes, product_bytes(p)));
+  EpilogueArgs e = store_to(y, ldy, residual, ldr, dtype);
+  e.bias = bias;
+  e.z = z;
+  e.ldz = ldz;
+  e.z8 = z8;
+  e.act = act;
+  if (z && !z8 && vec(z, ldz, dtype)) e.vec |= kVecZ;
+  OIDN_TRY(run_product(p, x, ldx, w, ldw, e, workspace, stream));
+  return clear_error();
+}
+
+int oidn_linear_backward_workspace_bytes(long m, int k, int n, int act, int dtype, unsigned flags,
+                                         size_t* bytes) {
+  if (!bytes) return fail(OIDN_E_INVALID, "null bytes pointer");
+  OIDN_TRY(check_linear(m, k, n, dtype));
+  OIDN_TRY(check_act(act));
+  OIDN_TRY(check_flags(flags, OIDN_X_CKPT8 | OIDN_Z_CKPT8));
+  *bytes = m ? linear_back(m, k, n, act, dtype, flags, nullptr).bytes : 0;
+  return clear_error();
+}
+
+int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, const void* z, long ldz,
+                         const void* w, long ldw, void* dx, long lddx, void* dw, long lddw,
+                         float* dbias, long m, int k, int n, int act, int dtype, unsigned flags,
+                         void* workspace, size_t ws_bytes, hipStream_t stream) {
+  OIDN_TRY(check_linear(m, k, n, dtype));
+  OIDN_TRY(check_act(act));
+  OIDN_TRY(check_flags(flags, OIDN_X_CKPT8 | OIDN_Z_CKPT8));
+  const bool x8 = flags & OIDN_X_CKPT8, z8 = flags & OIDN_Z_CKPT8, slope = act != OIDN_ACT_NONE;
+  OIDN_TRY(check_matrix("dw", dw, lddw, k, dtype, true));
+  OIDN_TRY(check_aligned("dbias", dbias, 4));
+  if (m == 0) {
+    // sums over no rows
+    for (long i = 0; dw && lddw != k && i < n; ++i)
+      OIDN_TRY(ran(launch_zero(static_cast<char*>(dw) + i * lddw * esize(dtype), k * esize(dtype), stream), "zero launch"));
+    if (dw && lddw == k) OIDN_TRY(ran(launch_zero(dw, (size_t)n * k * esize(dtype), stream), "zero launch"));
+    if (dbias) OIDN_TRY(ran(launch_zero(dbias, n * sizeof(float), stream), "zero launch"));
+    return clear_error();
+  }
+  OIDN_TRY(check_matrix("dy", dy, lddy, n, dtype, false));
+  if (dw) {
+    if (x8) OIDN_TRY(check_blob("x", x));
+    else OIDN_TRY(check_matrix("x", x, ldx, k, dtype, false));
+  }
+  if (slope) {
+    if (z8) OIDN_TRY(check_blob("z", z));
+    else OIDN_TRY(check_matrix("z", z, ldz, n, dtype, false));
+  }
+  if (dx) OIDN_TRY(check_matrix("w", w, ldw, k, dtype, false));
+  OIDN_TRY(check_matrix("dx", dx, lddx, k, dtype, true));
+  LinearBack b = linear_back(m, k, n, act, dtype, flags, workspace);
+  OIDN_TRY(check_workspace(workspace, ws_bytes, b.bytes));
+
+  if (slope || dbias) {
+    SlopeArgs s{};
+    s.dy = dy;
+    s.lddy = lddy;
+    s.z = z;
+    s.ldz = ldz;
+    s.z8 = z8;
+    s.dz = slope ? b.dz : nullptr;
+    s.part = dbias ? static_cast<float*>(b.sums) : nullptr;
+    s.rows = m;
+    s.cols = n;
+    s.chunk = b.chunk;
+    s.act = act;
+    s.vec = (vec(dy, lddy, dtype) ? 1 : 0) | (slope && !z8 && vec(z, ldz, dtype) ? 2 : 0) |
+            (slope && vec(b.dz, n, dtype) ? 4 : 0);
+    OIDN_TRY(ran(launch_slope(s, dtype, stream), "slope pass launch"));
+    if (dbias) OIDN_TRY(ran(launch_column_sum(s.part, b.chunks, n, dbias, stream), "column sum launch"));
+  }
+  const void* dz = slope ? b.dz : dy;
+  const long lddz = slope ? n : lddy;
+  if (dx) OIDN_TRY(run_product(b.dx, dz, lddz, w, ldw, store_to(dx, lddx, nullptr, 0, dtype), b.slices, stream));
+  if (dw) {
+    if (x8) {
+      OIDN_TRY(ran(launch_ckpt_unpack(x, m, k, b.x, k, dtype, stream), "checkpoint unpack launch"));
+      x = b.x;
+      ldx = k;
+    }
+    OIDN_TRY(run_product(b.dw, dz, lddz, x, ldx, store_to(dw, lddw, nullptr, 0, dtype), b.slices, stream));
+  }
+  return clear_error();
+}
+
+// -------------------------------------------------------------------- ffn
+int oidn_ffn_workspace_bytes(long m, int d, int f, int dtype, size_t* bytes) {
+  if (!bytes) return fail(OIDN_E_INVALID, "null bytes pointer");
+  OIDN_TRY(check_ffn(m, d, f, dtype));
+  *bytes = m ? ffn_plan(m, d, f, dtype, nullptr).bytes : 0;
+  return clear_error();
+}
+
+int oidn_ffn(const void* x, long ldx, const void* w_in, const float* b_in, const void* w_out,
+             const float* b_out, const void* residual, long ldr, void* y, long ldy, void* z, long m,
+             int d, int f, int act, int dtype, unsigned flags, void* workspace, size_t ws_bytes,
+             hipStream_t stream) {
+  OIDN_TRY(check_ffn(m, d, f, dtype));
+  OIDN_TRY(check_act(act));
+  OIDN_TRY(check_flags(flags, OIDN_Z_CKPT8));
+  if (m == 0) return clear_error();
+  const bool z8 = flags & OIDN_Z_CKPT8;
+  OIDN_TRY(check_matrix("x", x, ldx, d, dtype, false));
+  OIDN_TRY(check_matrix("w_in", w_in, d, d, dtype, false));
+  OIDN_TRY(check_matrix("w_out", w_out, f, f, dtype, false));
+  OIDN_TRY(check_aligned("b_in", b_in, 4));
+  OIDN_TRY(check_aligned("b_out", b_out, 4));
+  OIDN_TRY(check_matrix("residual", residual, ldr, d, dtype, true));
+  OIDN_TRY(check_matrix("y", y, ldy, d, dtype, false));
+  if (z8) OIDN_TRY(check_blob("z", z));
+  else OIDN_TRY(check_matrix("z", z, 2L * f, 2L * f, dtype, true));
+  const Ffn p = ffn_plan(m, d, f, dtype, workspace);
+  OIDN_TRY(check_workspace(workspace, ws_bytes, p.bytes));
+
+  EpilogueArgs e = store_to(p.h, f, nullptr, 0, dtype);
+  e.bias = b_in;
+  e.z = z;
+  e.ldz = 2L * f;
+  e.z8 = z8;
+  e.act = act;
+  if (z && !z8 && vec(z, 2L * f, dtype, f)) e.vec |= kVecZ;
+  OIDN_TRY(run_product(p.in, x, ldx, w_in, d, e, nullptr, stream));
+  EpilogueArgs o = store_to(y, ldy, residual, ldr, dtype);
+  o.bias = b_out;
+  OIDN_TRY(run_product(p.out, p.h, f, w_out, f, o, p.slices, stream));
+  return clear_error();
+}
+
+int oidn_ffn_backward_workspace_bytes(long m, int d, int f, int dtype, unsigned flags, size_t* bytes) {
+  if (!bytes) return fail(OIDN_E_INVALID, "null bytes pointer");
+  OIDN_TRY(check_ffn(m, d, f, dtype));
+  OIDN_TRY(check_flags(flags, OIDN_X_CKPT8 | OIDN_Z_CKPT8));
+  *bytes = m ? ffn_back(m, d, f, dtype, flags, nullptr).bytes : 0;
+  return clear_error();
+}
+
+int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const void* z,
+                      const void* w_in, const void* w_out, const void* add, long ldadd, void* dx,
+                      long lddx, void* dw_in, float* db_in, void* dw_out, float* db_out, long m, int d,
+                      int f, int act, int dtype, unsigned flags, void* workspace, size_t ws_bytes,
+                      hipStream_t stream) {
+  OIDN_TRY(check_ffn(m, d, f, dtype));
+  OIDN_TRY(check_act(act));
+  OIDN_TRY(check_flags(flags, OIDN_X_CKPT8 | OIDN_Z_CKPT8));
+  const bool x8 = flags & OIDN_X_CKPT8, z8 = flags & OIDN_Z_CKPT8;
+  const size_t es = esize(dtype);
+  OIDN_TRY(check_matrix("dw_in", dw_in, d, d, dtype, true));
+  OIDN_TRY(check_matrix("dw_out", dw_out, f, f, dtype, true));
+  OIDN_TRY(check_aligned("db_in", db_in, 4));
+  OIDN_TRY(check_aligned("db_out", db_out, 4));
+  if (m == 0) {
+    // sums over no rows
+    if (dw_in) OIDN_TRY(ran(launch_zero(dw_in, 2 * (size_t)f * d * es, stream), "zero launch"));
+    if (dw_out) OIDN_TRY(ran(launch_zero(dw_out, (size_t)f * d * es, stream), "zero launch"));
+    if (db_in) OIDN_TRY(ran(launch_zero(db_in, 2 * (size_t)f * sizeof(float), stream), "zero launch"));
+    if (db_out) OIDN_TRY(ran(launch_zero(db_out, d * sizeof(float), stream), "zero launch"));
+    return clear_error();
+  }
+  const bool inner = dx || dw_in || db_in || dw_out;     // what needs dh
+  OIDN_TRY(check_matrix("dy", dy, lddy, d, dtype, false));
+  if (dw_in) {
+    if (x8) OIDN_TRY(check_blob("x", x));
+    else OIDN_TRY(check_matrix("x", x, ldx, d, dtype, false));
+  }
+  if (inner) {
+    if (z8) OIDN_TRY(check_blob("z", z));
+    else OIDN_TRY(check_matrix("z", z, 2L * f, 2L * f, dtype, false));
+    OIDN_TRY(check_matrix("w_out", w_out, f, f, dtype, false));
+  }
+  if (dx) OIDN_TRY(check_matrix("w_in", w_in, d, d, dtype, false));
+  OIDN_TRY(check_matrix("dx", dx, lddx, d, dtype, true));
+  OIDN_TRY(check_matrix("add", add, ldadd, d, dtype, true));
+  const FfnBack b = ffn_back(m, d, f, dtype, flags, workspace);
+  OIDN_TRY(check_workspace(workspace, ws_bytes, b.bytes));
+
+  const long f2 = 2L * f;
+  if (inner) {
+    EpilogueArgs e{};
+    e.y = b.dz;
+    e.ldy = f2;
+    e.h = b.h;
+    e.z = const_cast<void*>(z);
+    e.ldz = f2;
+    e.z8 = z8;
+    e.act = act;
+    e.part = db_in ? static_cast<float*>(b.in_sums) : nullptr;
+    e.vec = (vec(b.dz, f2, dtype, f) ? kVecY : 0) | (vec(b.h, f, dtype) ? kVecH : 0) |
+            (!z8 && vec(z, f2, dtype, f) ? kVecZ : 0);
+    OIDN_TRY(run_product(b.dh, dy, lddy, w_out, f, e, nullptr, stream));
+    if (db_in) OIDN_TRY(ran(launch_column_sum(e.part, b.groups, (int)f2, db_in, stream), "column sum launch"));
+  }
+  if (db_out) OIDN_TRY(column_sums(dy, lddy, m, d, b.chunk, b.chunks, b.out_sums, db_out, dtype, stream));
+  if (dx)
+    OIDN_TRY(run_product(b.dx, b.dz, f2, w_in, d, store_to(dx, lddx, add, ldadd, dtype), b.slices, stream));
+  if (dw_in) {
+    if (x8) {
+      OIDN_TRY(ran(launch_ckpt_unpack(x, m, d, b.x, d, dtype, stream), "checkpoint unpack launch"));
+      x = b.x;
+      ldx = d;
+    }
+    OIDN_TRY(run_product(b.dw_in, b.dz, f2, x, ldx, store_to(dw_in, d, nullptr, 0, dtype), b.slices, stream));
+  }
+  if (dw_out)
+    OIDN_TRY(run_product(b.dw_out, dy, lddy, b.h, f, store_to(dw_out, f, nullptr, 0, dtype), b.slices, stream));
+  return clear_error();
+}
+
+}  // extern "C"

@@ -1,0 +1,205 @@
+// fp32 matrix products on the matrix cores (v_mfma_f32_16x16x4), the same
+// products, tiles of C and epilogues as the 16-bit form (dense_gemm16.h).
+//
+// 32 summed elements are staged at a time through registers into one of two
+// LDS buffers, as rows of 32 + 4 floats: the pad puts the 16 rows of a
+// fragment's 16-byte reads on distinct banks.  A lane's 16 bytes are elements
+// 4 g .. 4 g + 3 (g = lane / 16) of 16; MFMA e takes element e of every lane,
+// in both operands, so the order of the sum is permuted within 16 elements
+// and nothing is shuffled.  Strided operands are transposed by the LDS write:
+// eight neighbouring lanes read 128 contiguous bytes.
+#include "dense_epilogue.h"
+
+namespace oidn {
+namespace {
+
+constexpr int kPad32 = kDenseKF32 + 4;
+
+template <int T, bool STRIDED>
+struct Stage32 {
+  static constexpr int kUnits = T * kDenseKF32 / 4 / 256;
+  static constexpr int kFloats = T * kPad32;
+
+  static __device__ __forceinline__ float4 load4(const float* p, long n) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n >= 4) {
+      __builtin_memcpy(&v, p, 16);
+    } else {
+      if (n > 0) v.x = p[0];
+      if (n > 1) v.y = p[1];
+      if (n > 2) v.z = p[2];
+    }
+    return v;
+  }
+
+  static __device__ __forceinline__ void load(float4 (&u)[kUnits], const void* base, long ld, long i0,
+                                              long rows, long l0, long len, long half) {
+    const float* b = static_cast<const float*>(base);
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      if constexpr (!STRIDED) {
+        const int t = threadIdx.x + k * 256, r = t >> 3;
+        long i = i0 + (half ? r & (T / 2 - 1) : r);
+        i = (i < rows ? i : rows - 1) + (half && r >= T / 2 ? half : 0);
+        const long l = l0 + 4 * (t & 7);
+        u[k] = load4(b + i * ld + l, len - l);
+      } else {
+        const long l = l0 + (threadIdx.x >> 3), i = i0 + 32 * k + 4 * (threadIdx.x & 7);
+        u[k] = load4(b + l * ld + i, l < len ? rows - i : 0);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(const float4 (&u)[kUnits], float* lds) {
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      if constexpr (!STRIDED) {
+        const int t = threadIdx.x + k * 256;
+        *reinterpret_cast<float4*>(lds + (t >> 3) * kPad32 + 4 * (t & 7)) = u[k];
+      } else {
+        float* p = lds + (32 * k + 4 * (threadIdx.x & 7)) * kPad32 + (threadIdx.x >> 3);
+        p[0] = u[k].x;
+        p[kPad32] = u[k].y;
+        p[2 * kPad32] = u[k].z;
+        p[3 * kPad32] = u[k].w;
+      }
+    }
+  }
+  template <bool PAIR>
+  static __device__ __forceinline__ floatx4 fragment(const float* lds, int base, int q, int kk) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    const int row = base + (PAIR ? 8 * (r >> 2) + 4 * q + (r & 3) : 16 * q + r);
+    return *reinterpret_cast<const floatx4*>(lds + row * kPad32 + 16 * kk + 4 * g);
+  }
+};
+
+template <int LAYOUT, int EPI, int TR, int TC>
+__global__ __launch_bounds__(256, 2) void dense_gemm32(GemmArgs a) {
+  constexpr int DT = OIDN_F32;
+  constexpr bool PS = LAYOUT != kForward, QS = LAYOUT == kWeightGrad;
+  constexpr int FR = TR / 32, FC = TC / 32;
+  static_assert(EPI != kEpiGated || FC % 4 == 0, "a wave holds pairs of both projections");
+  typedef Stage32<TC, PS> P;
+  typedef Stage32<TR, QS> Q;
+  __shared__ __attribute__((aligned(16))) float lds[2][P::kFloats + Q::kFloats];
+
+  int tc, tr;
+  if (!tile_of_block(blockIdx.x, a.tiles_c, a.tiles_r, tc, tr)) return;
+  const long i0 = (long)tr * TR;
+  constexpr int C = EPI == kEpiGated ? TC / 2 : TC;
+  const long j0 = (long)tc * C;
+  const long half = EPI == kEpiGated ? a.e.cols : 0;
+  const int wave = threadIdx.x >> 6, wr = wave >> 1, wc = wave & 1;
+  const long t0 = (long)blockIdx.y * a.per_split;
+  const long nt = (a.len + kDenseKF32 - 1) / kDenseKF32;
+  const long t1 = t0 + a.per_split < nt ? t0 + a.per_split : nt;
+
+  floatx4 acc[FC][FR];
+#pragma unroll
+  for (int c = 0; c < FC; ++c)
+#pragma unroll
+    for (int r = 0; r < FR; ++r) acc[c][r] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  float4 up[P::kUnits], uq[Q::kUnits];
+  P::load(up, a.p, a.ldp, j0, a.e.cols, t0 * kDenseKF32, a.len, half);
+  Q::load(uq, a.q, a.ldq, i0, a.e.rows, t0 * kDenseKF32, a.len, 0);
+  for (long t = t0; t < t1; ++t) {
+    float* const lp = lds[(t - t0) & 1];
+    float* const lq = lp + P::kFloats;
+    P::store(up, lp);
+    Q::store(uq, lq);
+    __syncthreads();
+    if (t + 1 < t1) {
+      P::load(up, a.p, a.ldp, j0, a.e.cols, (t + 1) * kDenseKF32, a.len, half);
+      Q::load(uq, a.q, a.ldq, i0, a.e.rows, (t + 1) * kDenseKF32, a.len, 0);
+    }
+#pragma unroll
+    for (int kk = 0; kk < kDenseKF32 / 16; ++kk) {
+      floatx4 fp[FC], fq[FR];
+#pragma unroll
+      for (int c = 0; c < FC; ++c) {
+        const int pair = c / 2;
+        const int base = EPI == kEpiGated
+                             ? (pair < FC / 4 ? wc * (TC / 4) + 32 * pair
+                                              : TC / 2 + wc * (TC / 4) + 32 * (pair - FC / 4))
+                             : wc * (TC / 2) + 32 * pair;
+        fp[c] = P::template fragment<true>(lp, base, c & 1, kk);
+      }
+#pragma unroll
+      for (int r = 0; r < FR; ++r) fq[r] = Q::template fragment<false>(lq, wr * (TR / 2), r, kk);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int c = 0; c < FC; ++c)
+#pragma unroll
+          for (int r = 0; r < FR; ++r)
+            acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(fp[c][e], fq[r][e], acc[c][r], 0, 0, 0);
+    }
+  }
+
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  auto eight = [&](int pair, int r) {
+    Eight x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x.v[k] = acc[2 * pair][r][k];
+      x.v[4 + k] = acc[2 * pair + 1][r][k];
+    }
+    return x;
+  };
+  constexpr int PAIRS = EPI == kEpiGated ? FC / 4 : FC / 2;
+#pragma unroll
+  for (int pair = 0; pair < PAIRS; ++pair) {
+    const int j = (int)j0 + wc * (C / 2) + 32 * pair + 8 * g;
+    Eight sa{}, sb{};
+#pragma unroll
+    for (int r = 0; r < FR; ++r) {
+      const long i = i0 + wr * (TR / 2) + 16 * r + (lane & 15);
+      const bool row_ok = i < a.e.rows;
+      if constexpr (EPI == kEpiLinear)
+        epilogue_linear<DT, 16, 32>(a.e, i, j, eight(pair, r), row_ok);
+      else if constexpr (EPI == kEpiPartial)
+        epilogue_partial(a.e, blockIdx.y, i, j, eight(pair, r), row_ok);
+      else if constexpr (EPI == kEpiGated)
+        epilogue_gated<DT, 16, 32>(a.e, i, j, eight(pair, r), eight(pair + FC / 4, r), row_ok);
+      else
+        epilogue_gated_back<DT>(a.e, i, j, eight(pair, r), row_ok, sa, sb);
+    }
+    if constexpr (EPI == kEpiGatedBack) {
+      if (a.e.part) store_column_sums(a.e, (long)tr * 2 + wr, j, sa, sb);
+    }
+  }
+}
+
+template <int LAYOUT, int EPI, int TR, int TC>
+hipError_t launch(const GemmArgs& a, const GemmPlan& p, hipStream_t stream) {
+  const unsigned blocks = (unsigned)((a.tiles_r * (long)a.tiles_c + kXcds - 1) / kXcds * kXcds);
+  hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, TR, TC>), dim3(blocks, p.splits), dim3(256), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+
+template <int LAYOUT, int EPI>
+hipError_t launch_epi(const GemmArgs& a, const GemmPlan& p, hipStream_t stream) {
+  if (p.tile_r == 128) return launch<LAYOUT, EPI, 128, 128>(a, p, stream);
+  if constexpr (EPI == kEpiGated) return launch<LAYOUT, EPI, 64, 128>(a, p, stream);
+  else return launch<LAYOUT, EPI, 64, 64>(a, p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_f32(const GemmArgs& a, const GemmPlan& p, int layout, int epi,
+                           hipStream_t stream) {
+  switch (layout * 4 + epi) {
+    case kForward * 4 + kEpiLinear: return launch_epi<kForward, kEpiLinear>(a, p, stream);
+    case kForward * 4 + kEpiPartial: return launch_epi<kForward, kEpiPartial>(a, p, stream);
+    case kForward * 4 + kEpiGated: return launch_epi<kForward, kEpiGated>(a, p, stream);
+    case kInputGrad * 4 + kEpiLinear: return launch_epi<kInputGrad, kEpiLinear>(a, p, stream);
+    case kInputGrad * 4 + kEpiPartial: return launch_epi<kInputGrad, kEpiPartial>(a, p, stream);
+    case kInputGrad * 4 + kEpiGatedBack: return launch_epi<kInputGrad, kEpiGatedBack>(a, p, stream);
+    case kWeightGrad * 4 + kEpiLinear: return launch_epi<kWeightGrad, kEpiLinear>(a, p, stream);
+    case kWeightGrad * 4 + kEpiPartial: return launch_epi<kWeightGrad, kEpiPartial>(a, p, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace oidn

@@ -1,0 +1,209 @@
+// Memory-bound passes of the dense operators: the sum of a product's slices,
+// the slope pass dz = dy * act'(z) with column sums, column sums of partial
+// rows, 8-bit checkpoints of whole matrices, and zeros.
+#include "dense_epilogue.h"
+
+namespace oidn {
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// A thread sums eight columns of a row over the slices in order, so the result
+// does not depend on which workgroup finished when.  Four neighbouring lanes
+// hold a 32-column block.
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void split_sum(EpilogueArgs e, const float* __restrict__ part,
+                                                         int splits, long units, long total) {
+  const long t = (long)blockIdx.x * kRowThreads + threadIdx.x;
+  const long i = t / units;
+  const int j = (int)(t - i * units) * 8;
+  const int n = e.cols - j;
+  const bool ok = t < total && n > 0;
+  Eight x{};
+  if (ok) {
+    const bool vec = n >= 8 && (e.cols & 3) == 0;
+    const long step = e.rows * (long)e.cols;
+    const float* p = part + i * e.cols + j;
+    for (int s = 0; s < splits; ++s) {
+      const Eight v = load8<OIDN_F32>(p, s * step, vec, n);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x.v[k] += v.v[k];
+    }
+  }
+  epilogue_linear<DT, 1, 2>(e, i, j, x, t < total);
+}
+
+// A workgroup covers `chunk` rows by 8 << cs columns: 1 << cs units of eight
+// columns, the other threads are row lanes.
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, int cs) {
+  const int u = threadIdx.x & ((1 << cs) - 1), rl = threadIdx.x >> cs, rows_at_once = kRowThreads >> cs;
+  const int j = (int)((blockIdx.y << cs) + u) * 8;
+  const int n = a.cols - j;
+  const bool full = n >= 8;
+  const long r0 = blockIdx.x * a.chunk, r1 = r0 + a.chunk < a.rows ? r0 + a.chunk : a.rows;
+  Eight sum{};
+  if (n > 0) {
+    for (long i = r0 + rl; i < r1; i += rows_at_once) {
+      Eight d = load8<DT>(a.dy, i * a.lddy + j, full && (a.vec & 1), n);
+      if (a.act != OIDN_ACT_NONE) {
+        const Eight z = a.z8 ? ckpt_load8(ckpt_at(const_cast<void*>(a.z), a.rows, a.cols), i, j)
+                             : load8<DT>(a.z, i * a.ldz + j, full && (a.vec & 2), n);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float g, s;
+          activate_slope<DT>(a.act, z.v[k], g, s);
+          d.v[k] *= s;
+        }
+      }
+      if (a.dz) store8<DT>(a.dz, i * (long)a.cols + j, d, full && (a.vec & 4), n);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum.v[k] += d.v[k];
+    }
+  }
+  if (!a.part) return;
+  // row lanes are added in order through LDS
+  __shared__ float lds[kRowThreads][9];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) lds[threadIdx.x][k] = sum.v[k];
+  __syncthreads();
+  for (int c = threadIdx.x; c < (8 << cs); c += kRowThreads) {
+    float s = 0.f;
+    for (int r = 0; r < rows_at_once; ++r) s += lds[(r << cs) + c / 8][c % 8];
+    const int col = (int)(blockIdx.y << cs) * 8 + c;
+    if (col < a.cols) a.part[(long)blockIdx.x * a.cols + col] = s;
+  }
+}
+
+// 32 columns x 8 lanes over the groups.
+__global__ __launch_bounds__(kRowThreads) void column_sum(const float* __restrict__ part, long groups,
+                                                          int cols, float* __restrict__ out) {
+  const int c = threadIdx.x & 31, l = threadIdx.x >> 5, j = blockIdx.x * 32 + c;
+  float s = 0.f;
+  if (j < cols) {
+    for (long g = l; g < groups; g += 8) s += part[g * cols + j];
+  }
+  __shared__ float lds[8][32];
+  lds[l][c] = s;
+  __syncthreads();
+  if (l == 0 && j < cols) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += lds[k][c];
+    out[j] = s;
+  }
+}
+
+// A thread codes eight columns; four neighbouring lanes hold a block.
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void ckpt_pack(const void* __restrict__ x, long ldx, long m,
+                                                         long n, void* ckpt, long units, long total,
+                                                         int vec) {
+  const long t = (long)blockIdx.x * kRowThreads + threadIdx.x;
+  const long i = t / units, j = (t - i * units) * 8;
+  Eight v{};
+  const int left = n - j < 8 ? (int)(n - j) : 8;
+  if (t < total && left > 0) v = load8<DT>(x, i * ldx + j, vec && left == 8, left);
+  ckpt_store8<1, 2>(ckpt_at(ckpt, m, n), i, (int)j, v, t < total);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void ckpt_unpack(void* ckpt, long m, long n, void* __restrict__ y,
+                                                           long ldy, long units, long total, int vec) {
+  const long t = (long)blockIdx.x * kRowThreads + threadIdx.x;
+  const long i = t / units, j = (t - i * units) * 8;
+  const int left = n - j < 8 ? (int)(n - j) : 8;
+  if (t >= total || left <= 0) return;
+  store8<DT>(y, i * ldy + j, ckpt_load8(ckpt_at(ckpt, m, n), i, (int)j), vec && left == 8, left);
+}
+
+__global__ __launch_bounds__(kRowThreads) void zero_bytes(unsigned char* p, size_t n) {
+  const size_t step = (size_t)gridDim.x * kRowThreads;
+  for (size_t i = (size_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += step) p[i] = 0;
+}
+
+bool vec16(const void* p, long ld, int dtype) {
+  const long e = dtype == OIDN_F32 ? 4 : 2;
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * e % 16 == 0;
+}
+unsigned blocks_of(long n) { return (unsigned)((n + kRowThreads - 1) / kRowThreads); }
+
+}  // namespace
+
+hipError_t launch_split_sum(const EpilogueArgs& e, const float* part, int splits, int dtype,
+                            hipStream_t stream) {
+  const long units = ckpt_cols(e.cols) / 8, total = e.rows * units;
+  const dim3 grid(blocks_of(total)), block(kRowThreads);
+  if (dtype == OIDN_F32)
+    hipLaunchKernelGGL(split_sum<OIDN_F32>, grid, block, 0, stream, e, part, splits, units, total);
+  else if (dtype == OIDN_F16)
+    hipLaunchKernelGGL(split_sum<OIDN_F16>, grid, block, 0, stream, e, part, splits, units, total);
+  else
+    hipLaunchKernelGGL(split_sum<OIDN_BF16>, grid, block, 0, stream, e, part, splits, units, total);
+  return hipGetLastError();
+}
+
+long slope_chunk(long rows) {
+  // at most 256 chunks, so that the column sums stay a short second pass; at
+  // least 32 rows, so that a workgroup's lanes have work
+  const long c = (rows + 255) / 256;
+  return c < 32 ? 32 : c;
+}
+
+hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream) {
+  const int units = (a.cols + 7) / 8;
+  int cs = 0;
+  while (cs < 5 && (1 << cs) < units) ++cs;
+  const dim3 grid((unsigned)((a.rows + a.chunk - 1) / a.chunk), (unsigned)((units + (1 << cs) - 1) >> cs));
+  if (dtype == OIDN_F32)
+    hipLaunchKernelGGL(slope_pass<OIDN_F32>, grid, dim3(kRowThreads), 0, stream, a, cs);
+  else if (dtype == OIDN_F16)
+    hipLaunchKernelGGL(slope_pass<OIDN_F16>, grid, dim3(kRowThreads), 0, stream, a, cs);
+  else
+    hipLaunchKernelGGL(slope_pass<OIDN_BF16>, grid, dim3(kRowThreads), 0, stream, a, cs);
+  return hipGetLastError();
+}
+
+hipError_t launch_column_sum(const float* part, long groups, int cols, float* out,
+                             hipStream_t stream) {
+  hipLaunchKernelGGL(column_sum, dim3((unsigned)((cols + 31) / 32)), dim3(kRowThreads), 0, stream, part,
+                     groups, cols, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
+                            hipStream_t stream) {
+  const long units = ckpt_cols(n) / 8, total = m * units;
+  const int vec = vec16(x, ldx, dtype);
+  const dim3 grid(blocks_of(total)), block(kRowThreads);
+  if (dtype == OIDN_F32)
+    hipLaunchKernelGGL(ckpt_pack<OIDN_F32>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total, vec);
+  else if (dtype == OIDN_F16)
+    hipLaunchKernelGGL(ckpt_pack<OIDN_F16>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total, vec);
+  else
+    hipLaunchKernelGGL(ckpt_pack<OIDN_BF16>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total, vec);
+  return hipGetLastError();
+}
+
+hipError_t launch_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ldy, int dtype,
+                              hipStream_t stream) {
+  void* const c = const_cast<void*>(ckpt);
+  const long units = (n + 7) / 8, total = m * units;
+  const int vec = vec16(y, ldy, dtype);
+  const dim3 grid(blocks_of(total)), block(kRowThreads);
+  if (dtype == OIDN_F32)
+    hipLaunchKernelGGL(ckpt_unpack<OIDN_F32>, grid, block, 0, stream, c, m, n, y, ldy, units, total, vec);
+  else if (dtype == OIDN_F16)
+    hipLaunchKernelGGL(ckpt_unpack<OIDN_F16>, grid, block, 0, stream, c, m, n, y, ldy, units, total, vec);
+  else
+    hipLaunchKernelGGL(ckpt_unpack<OIDN_BF16>, grid, block, 0, stream, c, m, n, y, ldy, units, total, vec);
+  return hipGetLastError();
+}
+
+hipError_t launch_zero(void* p, size_t bytes, hipStream_t stream) {
+  const size_t b = (bytes + kRowThreads - 1) / kRowThreads;
+  hipLaunchKernelGGL(zero_bytes, dim3((unsigned)(b < 2048 ? b : 2048)), dim3(kRowThreads), 0, stream,
+                     static_cast<unsigned char*>(p), bytes);
+  return hipGetLastError();
+}
+
+}  // namespace oidn
