@@ -72,6 +72,7 @@ struct GemmArgs {
 // Tile shape and slices of a launch.
 struct GemmPlan {
   int tile_r, tile_c;      // rows and columns of a workgroup's tile
+  bool direct;             // 16-bit: operands go straight from memory to LDS
   int splits;
   long per_split;
 };
@@ -79,7 +80,8 @@ constexpr int kDenseK = 64;      // summed length of one staged 16-bit tile
 constexpr int kDenseKF32 = 32;   // the same in fp32
 GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int epi);
 // Row groups of kEpiGatedBack's column sums: one per wave row of every tile.
-long gated_back_groups(long rows, const GemmPlan& p);
+inline long gated_back_groups(long rows, int tile_r) { return (rows + tile_r - 1) / tile_r * 2; }
+constexpr int kMinTile = 64;
 
 // 16-bit products, one entry for each layout.
 hipError_t launch_gemm16_forward(const GemmArgs& a, const GemmPlan& p, int epi, bool bf16, hipStream_t stream);

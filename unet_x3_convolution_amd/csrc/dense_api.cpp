@@ -102,8 +102,22 @@ Product product(int layout, int epi, long rows, long cols, long len, int dtype) 
 size_t product_bytes(const Product& p) {
   return p.plan.splits > 1 ? align256((size_t)p.plan.splits * p.rows * p.cols * sizeof(float)) : 0;
 }
-int run_product(const Product& p, const void* q, long ldq, const void* pm, long ldp,
-                const EpilogueArgs& e, void* slices, hipStream_t stream) {
+// Whether a 16-bit operand can go straight to LDS in 16-byte units: `extent`
+// is what its rows hold of (the summed length, or the output's rows or columns
+// of a strided one), `span` the most rows that one tile's 32-bit offsets pass.
+bool direct_operand(const void* p, long ld, long extent, long span) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0 && extent % 8 == 0 &&
+         span * ld < (1L << 30);
+}
+int run_product(Product p, const void* q, long ldq, const void* pm, long ldp, const EpilogueArgs& e,
+                void* slices, hipStream_t stream, long* groups = nullptr) {
+  if (p.dtype != OIDN_F32) {
+    const bool ps = p.layout != kForward, qs = p.layout == kWeightGrad;
+    p.plan.direct = direct_operand(q, ldq, qs ? p.rows : p.len, 256) &&
+                    direct_operand(pm, ldp, ps ? p.cols : p.len, (p.epi == kEpiGated ? p.cols : 0) + 256);
+  }
+  if (!p.plan.direct && p.plan.tile_r > 128) p.plan.tile_r = p.plan.tile_c = 128;
+  if (groups) *groups = gated_back_groups(p.rows, p.plan.tile_r);
   GemmArgs a{};
   a.q = q;
   a.ldq = ldq;
@@ -213,7 +227,7 @@ FfnBack ffn_back(long m, int d, int f, int dtype, unsigned flags, void* ws) {
   b.dx = product(kInputGrad, kEpiLinear, m, d, 2L * f, dtype);
   b.dw_in = product(kWeightGrad, kEpiLinear, 2L * f, d, m, dtype);
   b.dw_out = product(kWeightGrad, kEpiLinear, d, f, m, dtype);
-  b.groups = gated_back_groups(m, b.dh.plan);
+  b.groups = gated_back_groups(m, kMinTile);
   b.chunk = slope_chunk(m);
   b.chunks = (m + b.chunk - 1) / b.chunk;
   Regions r{static_cast<char*>(ws), 0};
@@ -259,18 +273,17 @@ namespace oidn {
 GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int epi) {
   const long bk = dtype == OIDN_F32 ? kDenseKF32 : kDenseK;
   const long kt = (len + bk - 1) / bk;
-  const long c128 = epi == kEpiGated ? 64 : 128;
-  const long big = ((rows + 127) / 128) * ((cols + c128 - 1) / c128);
-  GemmPlan p{128, 128, 1, kt};
-  // 128 x 128 tiles once they give every compute unit one; smaller ones until then
-  long tiles = big;
-  if (big < 256) {
-    p.tile_r = 64;
-    p.tile_c = epi == kEpiGated ? 128 : 64;
-    tiles = ((rows + 63) / 64) * ((cols + 63) / 64);
-  }
-  if (epi == kEpiLinear && tiles < 256 && kt >= 8) {
-    long s = (512 + tiles - 1) / tiles;
+  auto tiles = [&](long t) {
+    const long c = epi == kEpiGated ? (t < 128 ? 64 : t / 2) : t;
+    return ((rows + t - 1) / t) * ((cols + c - 1) / c);
+  };
+  GemmPlan p{64, 64, false, 1, kt};
+  if (epi == kEpiGated) p.tile_c = 128;
+  // the largest tile that still gives every compute unit one
+  if (tiles(128) >= 256) p.tile_r = p.tile_c = 128;
+  if (dtype != OIDN_F32 && tiles(256) >= 256) p.tile_r = p.tile_c = 256;
+  if (epi == kEpiLinear && p.tile_r == 64 && tiles(64) < 256 && kt >= 8) {
+    long s = (512 + tiles(64) - 1) / tiles(64);
     if (s > kt / 4) s = kt / 4;
     if (s > 1) {
       p.per_split = (kt + s - 1) / s;
@@ -278,10 +291,6 @@ GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int epi) {
     }
   }
   return p;
-}
-
-long gated_back_groups(long rows, const GemmPlan& p) {
-  return (rows + p.tile_r - 1) / p.tile_r * 2;
 }
 
 }  // namespace oidn
@@ -530,8 +539,9 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
     e.part = db_in ? static_cast<float*>(b.in_sums) : nullptr;
     e.vec = (vec(b.dz, f2, dtype, f) ? kVecY : 0) | (vec(b.h, f, dtype) ? kVecH : 0) |
             (!z8 && vec(z, f2, dtype, f) ? kVecZ : 0);
-    OIDN_TRY(run_product(b.dh, dy, lddy, w_out, f, e, nullptr, stream));
-    if (db_in) OIDN_TRY(ran(launch_column_sum(e.part, b.groups, (int)f2, db_in, stream), "column sum launch"));
+    long groups = 0;
+    OIDN_TRY(run_product(b.dh, dy, lddy, w_out, f, e, nullptr, stream, &groups));
+    if (db_in) OIDN_TRY(ran(launch_column_sum(e.part, groups, (int)f2, db_in, stream), "column sum launch"));
   }
   if (db_out) OIDN_TRY(column_sums(dy, lddy, m, d, b.chunk, b.chunks, b.out_sums, db_out, dtype, stream));
   if (dx)

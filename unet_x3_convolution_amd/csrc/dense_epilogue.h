@@ -3,6 +3,8 @@
 // kernels and the slice sum run on eight neighbouring columns of one row.
 #pragma once
 
+#include <type_traits>
+
 #include "dense.h"
 #include "mfma_common.h"
 
@@ -214,137 +216,270 @@ __device__ __forceinline__ Eight ckpt_load8(const CkptAt& c, long i, int j) {
 }
 
 // ---------------------------------------------------------------- epilogues
-// Eight columns j .. j + 7 (j a multiple of 8) of row i; row_ok: the row
-// exists.  All lanes call them (the 8-bit stores exchange maxima between the
-// lanes XOR A and XOR B).
-__device__ __forceinline__ void add_bias(const float* bias, int j, int n, Eight& x) {
+// Eight columns j .. j + 7 (j a multiple of 8) of row i.  fetch() reads what
+// the epilogue needs from memory, finish() computes and stores; apart, so that
+// several rows' reads are in flight together.  All lanes call finish(): the
+// 8-bit stores exchange maxima between the lanes XOR A and XOR B.
+// WHOLE: all eight columns exist and every tensor takes 16-byte accesses
+// (whole_columns()), so no element is looked at by itself.
+__device__ __forceinline__ Eight bias8(const float* bias, int j, int n) {
+  Eight b{};
+  if (bias) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (k < n) x.v[k] += bias[j + k];
+    for (int k = 0; k < 8; ++k)
+      if (k < n) b.v[k] = bias[j + k];
+  }
+  return b;
+}
+__device__ __forceinline__ void add8(Eight& x, const Eight& b) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x.v[k] += b.v[k];
 }
 __device__ __forceinline__ void clear_tail(int n, Eight& x) {
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     if (k >= n) x.v[k] = 0.f;
 }
-
-template <int DT, int A, int B>
-__device__ __forceinline__ void epilogue_linear(const EpilogueArgs& e, long i, int j, Eight x,
-                                                bool row_ok) {
-  const int n = e.cols - j;                 // columns that exist from j on
-  const bool full = n >= 8;
-  if (e.bias) add_bias(e.bias, j, n, x);
-  if (e.z) {
-    if (e.z8) {
-      clear_tail(n, x);
-      ckpt_store8<A, B>(ckpt_at(e.z, e.rows, e.cols), i, j, x, row_ok);
-    } else if (row_ok && n > 0) {
-      store8<DT>(e.z, i * e.ldz + j, x, full && (e.vec & kVecZ), n);
-    }
-  }
-  if (!row_ok || n <= 0) return;
-  if (e.act != OIDN_ACT_NONE) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x.v[k] = activate<DT>(e.act, x.v[k]);
-  }
-  if (e.res) {
-    const Eight r = load8<DT>(e.res, i * e.ldr + j, full && (e.vec & kVecRes), n);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x.v[k] += r.v[k];
-  }
-  store8<DT>(e.y, i * e.ldy + j, x, full && (e.vec & kVecY), n);
-}
-
-// fp32 sums of one slice.
-__device__ __forceinline__ void epilogue_partial(const EpilogueArgs& e, int slice, long i, int j,
-                                                 const Eight& x, bool row_ok) {
-  const int n = e.cols - j;
-  if (!row_ok || n <= 0) return;
-  store8<OIDN_F32>(e.part, ((long)slice * e.rows + i) * e.cols + j, x,
-                   n >= 8 && (e.cols & 3) == 0, n);
-}
-
-// a, b: columns j of the gate and of the up projection.
-template <int DT, int A, int B>
-__device__ __forceinline__ void epilogue_gated(const EpilogueArgs& e, long i, int j, Eight a,
-                                               Eight b, bool row_ok) {
-  const int n = e.cols - j;
-  const bool full = n >= 8;
-  if (e.bias) {
-    add_bias(e.bias, j, n, a);
-    add_bias(e.bias + e.cols, j, n, b);
-  }
-  if (e.z) {
-    if (e.z8) {
-      clear_tail(n, a);
-      clear_tail(n, b);
-      ckpt_store8<A, B>(ckpt_at(e.z, e.rows, e.cols), i, j, a, row_ok);
-      ckpt_store8<A, B>(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols),
-                        i, j, b, row_ok);
-    } else if (row_ok && n > 0) {
-      store8<DT>(e.z, i * e.ldz + j, a, full && (e.vec & kVecZ), n);
-      store8<DT>(e.z, i * e.ldz + e.cols + j, b, full && (e.vec & kVecZ), n);
-    }
-  }
-  if (!row_ok || n <= 0) return;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) a.v[k] = activate<DT>(e.act, a.v[k]) * b.v[k];
-  store8<DT>(e.y, i * e.ldy + j, a, full && (e.vec & kVecY), n);
-}
-
-// dh: columns j of dy w_out.  Writes h and [da | db] and adds da, db to sa, sb
-// (0 where nothing exists).
+// The activation is the same for the whole launch: one branch for eight values.
 template <int DT>
-__device__ __forceinline__ void epilogue_gated_back(const EpilogueArgs& e, long i, int j, Eight dh,
-                                                    bool row_ok, Eight& sa, Eight& sb) {
-  const int n = e.cols - j;
-  const bool full = n >= 8;
-  if (!row_ok || n <= 0) return;
-  Eight a, b, h;
-  if (e.z8) {
-    void* z = e.z;
-    a = ckpt_load8(ckpt_at(z, e.rows, e.cols), i, j);
-    b = ckpt_load8(ckpt_at(static_cast<char*>(z) + ckpt_size(e.rows, e.cols), e.rows, e.cols), i, j);
-  } else {
-    a = load8<DT>(e.z, i * e.ldz + j, full && (e.vec & kVecZ), n);
-    b = load8<DT>(e.z, i * e.ldz + e.cols + j, full && (e.vec & kVecZ), n);
-  }
+__device__ __forceinline__ void activate8(int act, Eight& x) {
+  if (act == OIDN_ACT_RELU) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float g, s;
-    activate_slope<DT>(e.act, a.v[k], g, s);
-    h.v[k] = g * b.v[k];
-    a.v[k] = dh.v[k] * b.v[k] * s;
-    b.v[k] = dh.v[k] * g;
-    if (k < n) {
-      sa.v[k] += a.v[k];
-      sb.v[k] += b.v[k];
-    }
+    for (int k = 0; k < 8; ++k) x.v[k] = activate<DT>(OIDN_ACT_RELU, x.v[k]);
+  } else if (act == OIDN_ACT_SILU) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.v[k] = activate<DT>(OIDN_ACT_SILU, x.v[k]);
+  } else if (act == OIDN_ACT_GELU) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.v[k] = activate<DT>(OIDN_ACT_GELU, x.v[k]);
   }
-  store8<DT>(e.h, i * (long)e.cols + j, h, full && (e.vec & kVecH), n);
-  store8<DT>(e.y, i * e.ldy + j, a, full && (e.vec & kVecY), n);
-  store8<DT>(e.y, i * e.ldy + e.cols + j, b, full && (e.vec & kVecY), n);
 }
-
-// Column sums of a wave's rows: adds over the 16 lanes of a row fragment and
-// stores them as row `group` of the partial sums (2 * cols wide, da then db).
-__device__ __forceinline__ void store_column_sums(const EpilogueArgs& e, long group, int j,
-                                                  Eight sa, Eight sb) {
+// g = act(z), z becomes act'(z).
+template <int DT>
+__device__ __forceinline__ void activate_slope8(int act, Eight& z, Eight& g) {
+  if (act == OIDN_ACT_RELU) {
 #pragma unroll
-  for (int s = 1; s < 16; s *= 2)
+    for (int k = 0; k < 8; ++k) activate_slope<DT>(OIDN_ACT_RELU, z.v[k], g.v[k], z.v[k]);
+  } else if (act == OIDN_ACT_SILU) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) activate_slope<DT>(OIDN_ACT_SILU, z.v[k], g.v[k], z.v[k]);
+  } else if (act == OIDN_ACT_GELU) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) activate_slope<DT>(OIDN_ACT_GELU, z.v[k], g.v[k], z.v[k]);
+  } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      sa.v[k] += __shfl_xor(sa.v[k], s);
-      sb.v[k] += __shfl_xor(sb.v[k], s);
+      g.v[k] = z.v[k];
+      z.v[k] = 1.f;
     }
-  if (threadIdx.x & 15) return;
-  float* const row = e.part + group * 2 * e.cols;
+  }
+}
+
+struct Fetched { Eight a, b; };
+
+// Whether columns j0 .. j0 + width - 1 can be taken as WHOLE.
+template <int EPI>
+__device__ __forceinline__ bool whole_columns(const EpilogueArgs& e, int j0, int width) {
+  if (j0 + width > e.cols) return false;
+  if (EPI == kEpiPartial) return (e.cols & 3) == 0;
+  unsigned need = kVecY;
+  if (EPI == kEpiLinear && e.res) need |= kVecRes;
+  if (EPI == kEpiGatedBack) need |= kVecH;
+  if (e.z && !e.z8) need |= kVecZ;
+  return (e.vec & need) == need;
+}
+
+template <int DT, int EPI, bool WHOLE>
+__device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, Fetched& f) {
+  const int n = WHOLE ? 8 : e.cols - j;     // columns that exist from j on
+  if constexpr (EPI != kEpiLinear && EPI != kEpiGatedBack) return;
+  if constexpr (WHOLE) i = i < e.rows ? i : e.rows - 1;
+  else if (i >= e.rows || n <= 0) return;
+  const bool full = WHOLE || n >= 8;
+  if constexpr (EPI == kEpiLinear) {
+    if (e.res) f.a = load8<DT>(e.res, i * e.ldr + j, WHOLE || (full && (e.vec & kVecRes)), n);
+  }
+  if constexpr (EPI == kEpiGatedBack) {
+    if (e.z8) {
+      f.a = ckpt_load8(ckpt_at(e.z, e.rows, e.cols), i, j);
+      f.b = ckpt_load8(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols), i, j);
+    } else {
+      const bool vec = WHOLE || (full && (e.vec & kVecZ));
+      f.a = load8<DT>(e.z, i * e.ldz + j, vec, n);
+      f.b = load8<DT>(e.z, i * e.ldz + e.cols + j, vec, n);
+    }
+  }
+}
+
+// x: the sums (kEpiGated: the gate's, u the up projection's); bias: that of
+// the same columns, zeros if there is none.  kEpiGatedBack adds da and db to
+// sums.
+template <int DT, int EPI, int A, int B, bool WHOLE>
+__device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i, int j, Eight x, Eight u,
+                                       const Fetched& bias, Fetched& f, Fetched& sums) {
+  const int n = WHOLE ? 8 : e.cols - j;
+  const bool row_ok = i < e.rows, ok = row_ok && n > 0, full = n >= 8;
+  const bool vec_y = WHOLE || (full && (e.vec & kVecY)), vec_z = WHOLE || (full && (e.vec & kVecZ));
+  if constexpr (EPI == kEpiPartial) {       // fp32 sums of one slice
+    if (ok)
+      store8<OIDN_F32>(e.part, ((long)slice * e.rows + i) * e.cols + j, x,
+                       WHOLE || (full && (e.cols & 3) == 0), n);
+  } else if constexpr (EPI == kEpiLinear) {
+    add8(x, bias.a);
+    if (e.z) {
+      if (e.z8) {
+        if constexpr (!WHOLE) clear_tail(n, x);
+        ckpt_store8<A, B>(ckpt_at(e.z, e.rows, e.cols), i, j, x, row_ok);
+      } else if (ok) {
+        store8<DT>(e.z, i * e.ldz + j, x, vec_z, n);
+      }
+    }
+    activate8<DT>(e.act, x);
+    if (e.res) add8(x, f.a);
+    if (ok) store8<DT>(e.y, i * e.ldy + j, x, vec_y, n);
+  } else if constexpr (EPI == kEpiGated) {
+    add8(x, bias.a);
+    add8(u, bias.b);
+    if (e.z) {
+      if (e.z8) {
+        if constexpr (!WHOLE) {
+          clear_tail(n, x);
+          clear_tail(n, u);
+        }
+        ckpt_store8<A, B>(ckpt_at(e.z, e.rows, e.cols), i, j, x, row_ok);
+        ckpt_store8<A, B>(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols),
+                          i, j, u, row_ok);
+      } else if (ok) {
+        store8<DT>(e.z, i * e.ldz + j, x, vec_z, n);
+        store8<DT>(e.z, i * e.ldz + e.cols + j, u, vec_z, n);
+      }
+    }
+    activate8<DT>(e.act, x);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (j + k < e.cols) {
-      row[j + k] = sa.v[k];
-      row[e.cols + j + k] = sb.v[k];
+    for (int k = 0; k < 8; ++k) x.v[k] *= u.v[k];
+    if (ok) store8<DT>(e.y, i * e.ldy + j, x, vec_y, n);
+  } else {                                  // x is dh: h and [da | db]
+    Eight g, h, da, db;
+    activate_slope8<DT>(e.act, f.a, g);
+    if (!ok) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      h.v[k] = g.v[k] * f.b.v[k];
+      da.v[k] = x.v[k] * f.b.v[k] * f.a.v[k];
+      db.v[k] = x.v[k] * g.v[k];
+      if (k < n) {
+        sums.a.v[k] += da.v[k];
+        sums.b.v[k] += db.v[k];
+      }
     }
+    store8<DT>(e.h, i * (long)e.cols + j, h, WHOLE || (full && (e.vec & kVecH)), n);
+    store8<DT>(e.y, i * e.ldy + j, da, vec_y, n);
+    store8<DT>(e.y, i * e.ldy + e.cols + j, db, vec_y, n);
+  }
+}
+
+// The epilogue of a wave's 16 FR x 16 FC quarter of a tile, whose accumulators
+// are in pairs of column fragments: lane l holds row l % 16 of row fragment r
+// and columns 8 (l / 16) + 4 q .. + 3 of a pair's 32 in fragment q.  They pass
+// through the wave's own part of LDS, so that a row's columns leave in one
+// contiguous run and one copy of the epilogue's code serves all of them:
+// 16-byte unit u of row r sits at u ^ (r % 16), which keeps both the writes
+// (16 rows of a unit) and the reads (neighbouring units of a row) on distinct
+// banks.  kEpiGated: the first half of the columns is the gate's.
+// lds: kEpiRows * 64 * FC bytes of this wave; i0, j0: its first row, column;
+// group: its row of the partial column sums.
+template <int FR, int FC>
+constexpr int epilogue_rows() { return FR * FC > 32 ? 8 * FR : 16 * FR; }
+template <int FR, int FC>
+constexpr int epilogue_bytes() { return epilogue_rows<FR, FC>() * 64 * FC; }
+
+template <int DT, int EPI, int FR, int FC>
+__device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const floatx4 (&acc)[FC][FR], char* lds,
+                                              long i0, int j0, int slice, long group) {
+  constexpr int kRows = epilogue_rows<FR, FC>();       // rows per round
+  constexpr int kUnits = 4 * FC;                       // 16-byte units of a row
+  constexpr int kMask = kUnits < 16 ? kUnits - 1 : 15;
+  constexpr bool kGated = EPI == kEpiGated;
+  constexpr int kLanes = kGated ? FC : 2 * FC;         // lanes per row, eight columns each
+  constexpr int kAtOnce = 64 / kLanes;                 // rows per step
+  constexpr int kSteps = kRows / kAtOnce;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  const int c = lane % kLanes, j = j0 + 8 * c;
+  auto unit = [&](int row, int u) -> floatx4& {
+    return *reinterpret_cast<floatx4*>(lds + (row * kUnits + (u ^ (row & kMask))) * 16);
+  };
+  Fetched bias{}, sums{};
+  if constexpr (EPI == kEpiLinear || kGated) {
+    bias.a = bias8(e.bias, j, e.cols - j);
+    if constexpr (kGated) bias.b = bias8(e.bias ? e.bias + e.cols : nullptr, j, e.cols - j);
+  }
+  auto rows = [&](auto whole, long ir) {
+    constexpr bool kWhole = decltype(whole)::value;
+    // steps whose reads are in flight together
+    constexpr int kTogether = !kWhole ? 1 : kSteps < 4 ? kSteps : 4;
+#pragma unroll 1
+    for (int s = 0; s < kSteps; s += kTogether) {
+      Fetched got[kTogether];
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) fetch<DT, EPI, kWhole>(e, ir + (s + k) * kAtOnce, j, got[k]);
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) {
+        const int row = (s + k) * kAtOnce + lane / kLanes;
+        Eight x, u{};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const floatx4 v = unit(row, 2 * c + h);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) x.v[4 * h + m] = v[m];
+          if constexpr (kGated) {
+            const floatx4 w = unit(row, kUnits / 2 + 2 * c + h);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) u.v[4 * h + m] = w[m];
+          }
+        }
+        finish<DT, EPI, 1, 2, kWhole>(e, slice, ir + (s + k) * kAtOnce, j, x, u, bias, got[k], sums);
+      }
+    }
+  };
+  const bool whole = whole_columns<EPI>(e, j0, 8 * kLanes);
+  constexpr int kRounds = 16 * FR / kRows;
+#pragma unroll 1
+  for (int round = 0; round < kRounds; ++round) {
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k)
+      if (round == k) {
+#pragma unroll
+        for (int f = 0; f < FC; ++f)
+#pragma unroll
+          for (int r = 0; r < kRows / 16; ++r)
+            unit(16 * r + (lane & 15), 8 * (f / 2) + 2 * g + f % 2) = acc[f][k * (kRows / 16) + r];
+      }
+    // the wave's own writes, back in order
+    __builtin_amdgcn_wave_barrier();
+    const long ir = i0 + round * kRows + lane / kLanes;
+    if (whole) rows(std::true_type{}, ir);
+    else rows(std::false_type{}, ir);
+    __builtin_amdgcn_wave_barrier();
+  }
+  if constexpr (EPI == kEpiGatedBack) {
+    if (!e.part) return;
+    // rows of the other lanes with the same columns
+#pragma unroll
+    for (int s = kLanes; s < 64; s *= 2)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sums.a.v[k] += __shfl_xor(sums.a.v[k], s);
+        sums.b.v[k] += __shfl_xor(sums.b.v[k], s);
+      }
+    if (lane >= kLanes) return;
+    float* const row = e.part + group * 2 * e.cols;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (j + k < e.cols) {
+        row[j + k] = sums.a.v[k];
+        row[e.cols + j + k] = sums.b.v[k];
+      }
+  }
 }
 
 }  // namespace

@@ -5,8 +5,7 @@
 // quarter of it in 16 x 16 fragments of v_mfma_f32_16x16x32.  P is the MFMA's A
 // operand (its rows are C's columns), so a lane's accumulator holds
 // neighbouring columns of one row: fragments go in pairs whose rows are dealt
-// so that lane group g of a pair owns the 8 columns 32 p + 8 g .. + 7, one
-// 16-byte store per lane and 64 contiguous bytes per row.
+// so that lane group g of a pair owns the 8 columns 32 p + 8 g .. + 7.
 //
 // kDenseK = 64 summed elements are staged at a time, through registers into
 // one of two LDS buffers: the loads of the next tile are in flight while the
@@ -184,39 +183,9 @@ __global__ __launch_bounds__(256, 2) void dense_gemm16(GemmArgs a) {
     }
   }
 
-  // lane l: row l % 16 of a row fragment, columns 8 (l / 16) .. + 7 of a pair
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  auto eight = [&](int pair, int r) {
-    Eight x;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x.v[k] = acc[2 * pair][r][k];
-      x.v[4 + k] = acc[2 * pair + 1][r][k];
-    }
-    return x;
-  };
-  constexpr int PAIRS = EPI == kEpiGated ? FC / 4 : FC / 2;
-#pragma unroll
-  for (int pair = 0; pair < PAIRS; ++pair) {
-    const int j = (int)j0 + wc * (C / 2) + 32 * pair + 8 * g;
-    Eight sa{}, sb{};
-#pragma unroll
-    for (int r = 0; r < FR; ++r) {
-      const long i = i0 + wr * (TR / 2) + 16 * r + (lane & 15);
-      const bool row_ok = i < a.e.rows;
-      if constexpr (EPI == kEpiLinear)
-        epilogue_linear<DT, 16, 32>(a.e, i, j, eight(pair, r), row_ok);
-      else if constexpr (EPI == kEpiPartial)
-        epilogue_partial(a.e, blockIdx.y, i, j, eight(pair, r), row_ok);
-      else if constexpr (EPI == kEpiGated)
-        epilogue_gated<DT, 16, 32>(a.e, i, j, eight(pair, r), eight(pair + FC / 4, r), row_ok);
-      else
-        epilogue_gated_back<DT>(a.e, i, j, eight(pair, r), row_ok, sa, sb);
-    }
-    if constexpr (EPI == kEpiGatedBack) {
-      if (a.e.part) store_column_sums(a.e, (long)tr * 2 + wr, j, sa, sb);
-    }
-  }
+  __syncthreads();                       // every wave has read its last fragments
+  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, &lds[0][0] + wave * epilogue_bytes<FR, FC>(),
+                                 i0 + wr * (TR / 2), (int)j0 + wc * (C / 2), blockIdx.y, (long)tr * 2 + wr);
 }
 
 }  // namespace

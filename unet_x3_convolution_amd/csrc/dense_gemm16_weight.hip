@@ -1,19 +1,26 @@
 // 16-bit products with operands as in dw = dz^T x.
-#include "dense_gemm16.h"
+#include "dense_gemm16_direct.h"
 
 namespace oidn {
 namespace {
 
 template <bool BF, int EPI, int TR, int TC>
 hipError_t launch(const GemmArgs& a, const GemmPlan& p, hipStream_t stream) {
-  const unsigned blocks = (unsigned)((long)(a.tiles_r * (long)a.tiles_c + kXcds - 1) / kXcds * kXcds);
-  hipLaunchKernelGGL((dense_gemm16<BF, kWeightGrad, EPI, TR, TC>), dim3(blocks, p.splits), dim3(256), 0,
-                     stream, a);
+  const dim3 grid((unsigned)((a.tiles_r * (long)a.tiles_c + kXcds - 1) / kXcds * kXcds), p.splits);
+  if (p.direct)
+    hipLaunchKernelGGL((dense_gemm16_direct<BF, kWeightGrad, EPI, TR, TC>), grid, dim3(256), 0, stream, a);
+  else if constexpr (TR <= 128)
+    hipLaunchKernelGGL((dense_gemm16<BF, kWeightGrad, EPI, TR, TC>), grid, dim3(256), 0, stream, a);
+  else
+    return hipErrorInvalidValue;
   return hipGetLastError();
 }
 
 template <bool BF, int EPI>
 hipError_t launch_epi(const GemmArgs& a, const GemmPlan& p, hipStream_t stream) {
+  if constexpr (EPI != kEpiPartial) {
+    if (p.tile_r == 256) return launch<BF, EPI, 256, 256>(a, p, stream);
+  }
   if (p.tile_r == 128) return launch<BF, EPI, 128, 128>(a, p, stream);
   if constexpr (EPI == kEpiGated) return launch<BF, EPI, 64, 128>(a, p, stream);
   else return launch<BF, EPI, 64, 64>(a, p, stream);

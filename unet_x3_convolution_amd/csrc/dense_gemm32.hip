@@ -136,38 +136,9 @@ __global__ __launch_bounds__(256, 2) void dense_gemm32(GemmArgs a) {
     }
   }
 
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  auto eight = [&](int pair, int r) {
-    Eight x;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x.v[k] = acc[2 * pair][r][k];
-      x.v[4 + k] = acc[2 * pair + 1][r][k];
-    }
-    return x;
-  };
-  constexpr int PAIRS = EPI == kEpiGated ? FC / 4 : FC / 2;
-#pragma unroll
-  for (int pair = 0; pair < PAIRS; ++pair) {
-    const int j = (int)j0 + wc * (C / 2) + 32 * pair + 8 * g;
-    Eight sa{}, sb{};
-#pragma unroll
-    for (int r = 0; r < FR; ++r) {
-      const long i = i0 + wr * (TR / 2) + 16 * r + (lane & 15);
-      const bool row_ok = i < a.e.rows;
-      if constexpr (EPI == kEpiLinear)
-        epilogue_linear<DT, 16, 32>(a.e, i, j, eight(pair, r), row_ok);
-      else if constexpr (EPI == kEpiPartial)
-        epilogue_partial(a.e, blockIdx.y, i, j, eight(pair, r), row_ok);
-      else if constexpr (EPI == kEpiGated)
-        epilogue_gated<DT, 16, 32>(a.e, i, j, eight(pair, r), eight(pair + FC / 4, r), row_ok);
-      else
-        epilogue_gated_back<DT>(a.e, i, j, eight(pair, r), row_ok, sa, sb);
-    }
-    if constexpr (EPI == kEpiGatedBack) {
-      if (a.e.part) store_column_sums(a.e, (long)tr * 2 + wr, j, sa, sb);
-    }
-  }
+  __syncthreads();                       // every wave has read its last fragments
+  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, reinterpret_cast<char*>(&lds[0][0]) + wave * epilogue_bytes<FR, FC>(),
+                                 i0 + wr * (TR / 2), (int)j0 + wc * (C / 2), blockIdx.y, (long)tr * 2 + wr);
 }
 
 template <int LAYOUT, int EPI, int TR, int TC>

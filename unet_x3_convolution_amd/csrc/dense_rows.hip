@@ -30,7 +30,10 @@ __global__ __launch_bounds__(kRowThreads) void split_sum(EpilogueArgs e, const f
       for (int k = 0; k < 8; ++k) x.v[k] += v.v[k];
     }
   }
-  epilogue_linear<DT, 1, 2>(e, i, j, x, t < total);
+  Fetched f, none, bias{};
+  bias.a = bias8(e.bias, j, n);
+  fetch<DT, kEpiLinear, false>(e, i, j, f);
+  finish<DT, kEpiLinear, 1, 2, false>(e, 0, i, j, x, x, bias, f, none);
 }
 
 // A workgroup covers `chunk` rows by 8 << cs columns: 1 << cs units of eight
@@ -49,12 +52,10 @@ __global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, int cs) {
       if (a.act != OIDN_ACT_NONE) {
         const Eight z = a.z8 ? ckpt_load8(ckpt_at(const_cast<void*>(a.z), a.rows, a.cols), i, j)
                              : load8<DT>(a.z, i * a.ldz + j, full && (a.vec & 2), n);
+        Eight slope = z, value;
+        activate_slope8<DT>(a.act, slope, value);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float g, s;
-          activate_slope<DT>(a.act, z.v[k], g, s);
-          d.v[k] *= s;
-        }
+        for (int k = 0; k < 8; ++k) d.v[k] *= slope.v[k];
       }
       if (a.dz) store8<DT>(a.dz, i * (long)a.cols + j, d, full && (a.vec & 4), n);
 #pragma unroll
