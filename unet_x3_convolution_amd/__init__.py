@@ -190,7 +190,10 @@ def _p(t):
 def _s(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:   # a CPU-only torch, or one without it: the stream object, which costs 3 us to make
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

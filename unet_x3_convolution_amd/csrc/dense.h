@@ -72,13 +72,14 @@ struct GemmArgs {
 // Tile shape and slices of a launch.
 struct GemmPlan {
   int tile_r, tile_c;      // rows and columns of a workgroup's tile
+  bool few;                // few rows: launch_few
   bool direct;             // 16-bit: operands go straight from memory to LDS
   int splits;
   long per_split;
 };
 constexpr int kDenseK = 64;      // summed length of one staged 16-bit tile
 constexpr int kDenseKF32 = 32;   // the same in fp32
-GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int epi);
+GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int layout, int epi);
 // Row groups of kEpiGatedBack's column sums: one per wave row of every tile.
 inline long gated_back_groups(long rows, int tile_r) { return (rows + tile_r - 1) / tile_r * 2; }
 constexpr int kMinTile = 64;
@@ -90,6 +91,10 @@ hipError_t launch_gemm16_weight(const GemmArgs& a, const GemmPlan& p, int epi, b
                           hipStream_t stream);
 hipError_t launch_gemm_f32(const GemmArgs& a, const GemmPlan& p, int layout, int epi,
                            hipStream_t stream);
+// Forward products (kEpiLinear, kEpiGated) of at most kFewRows rows, in one
+// launch without slices.
+constexpr int kFewRows = 32;
+hipError_t launch_few(const GemmArgs& a, int epi, int dtype, hipStream_t stream);
 // Adds the slices of kEpiPartial and runs the epilogue (kEpiLinear).
 hipError_t launch_split_sum(const EpilogueArgs& e, const float* part, int splits, int dtype,
                             hipStream_t stream);

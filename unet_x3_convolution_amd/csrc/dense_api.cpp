@@ -97,7 +97,7 @@ struct Product {
   GemmPlan plan;
 };
 Product product(int layout, int epi, long rows, long cols, long len, int dtype) {
-  return {layout, epi, rows, cols, len, dtype, plan_gemm(rows, cols, len, dtype, epi)};
+  return {layout, epi, rows, cols, len, dtype, plan_gemm(rows, cols, len, dtype, layout, epi)};
 }
 size_t product_bytes(const Product& p) {
   return p.plan.splits > 1 ? align256((size_t)p.plan.splits * p.rows * p.cols * sizeof(float)) : 0;
@@ -136,7 +136,8 @@ int run_product(Product p, const void* q, long ldq, const void* pm, long ldp, co
   const int epi = split ? kEpiPartial : p.epi;
   if (split) a.e.part = static_cast<float*>(slices);
   hipError_t r;
-  if (p.dtype == OIDN_F32) r = launch_gemm_f32(a, p.plan, p.layout, epi, stream);
+  if (p.plan.few) r = launch_few(a, epi, p.dtype, stream);
+  else if (p.dtype == OIDN_F32) r = launch_gemm_f32(a, p.plan, p.layout, epi, stream);
   else if (p.layout == kForward) r = launch_gemm16_forward(a, p.plan, epi, p.dtype == OIDN_BF16, stream);
   else if (p.layout == kInputGrad) r = launch_gemm16_input(a, p.plan, epi, p.dtype == OIDN_BF16, stream);
   else r = launch_gemm16_weight(a, p.plan, epi, p.dtype == OIDN_BF16, stream);
@@ -270,14 +271,18 @@ int column_sums(const void* dy, long lddy, long m, int n, long chunk, long chunk
 
 namespace oidn {
 
-GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int epi) {
+GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int layout, int epi) {
   const long bk = dtype == OIDN_F32 ? kDenseKF32 : kDenseK;
   const long kt = (len + bk - 1) / bk;
   auto tiles = [&](long t) {
     const long c = epi == kEpiGated ? (t < 128 ? 64 : t / 2) : t;
     return ((rows + t - 1) / t) * ((cols + c - 1) / c);
   };
-  GemmPlan p{64, 64, false, 1, kt};
+  GemmPlan p{64, 64, false, false, 1, kt};
+  if (layout == kForward && rows <= kFewRows) {
+    p.few = true;
+    return p;
+  }
   if (epi == kEpiGated) p.tile_c = 128;
   // the largest tile that still gives every compute unit one
   if (tiles(128) >= 256) p.tile_r = p.tile_c = 128;

@@ -1,0 +1,175 @@
+// Products of a few rows (at most 32) with l-fastest operands: y = x w^T and
+// the gated projections, as when single pixels or tokens are served.
+//
+// The weights are all there is to read, each once, so the kernel is built
+// around keeping their loads in flight.  A workgroup of 8 waves owns 16
+// columns (two runs of 16 for a gated product, 32 where an 8-bit block has to
+// be whole) and all of the summed length, which its waves share in turns of
+// one chunk; every wave loads weight fragments straight into registers, up to
+// kDepth chunks at once, and multiplies them by the rows' fragments with
+// MFMAs (rows past the last read the last).  The waves' sums meet in LDS, are
+// added in wave order, and one launch is enough.
+//
+// A chunk is 128 bytes of every weight row: lane group g of 16 lanes takes
+// bytes 32 g .. + 31 in two 16-byte loads, so a pair of loads covers whole
+// lines.  MFMA s multiplies the s-th 16 bytes of all lanes: the order of the
+// sum is permuted alike in both operands.
+#include "dense_gemm16.h"
+
+namespace oidn {
+namespace {
+
+constexpr int kFewWaves = 8;
+constexpr int kDepth = 4;
+
+template <int DT>
+__device__ __forceinline__ uint4 part16(const char* p, int n) {
+  if constexpr (DT == OIDN_F32) {
+    const unsigned* s = reinterpret_cast<const unsigned*>(p);
+    return make_uint4(s[0], n > 1 ? s[1] : 0u, n > 2 ? s[2] : 0u, 0u);
+  } else {
+    return load16_part(p, n);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ floatx4 multiply16(uint4 a, uint4 b, floatx4 c) {
+  if constexpr (DT == OIDN_F32) {
+    const floatx4 av = __builtin_bit_cast(floatx4, a), bv = __builtin_bit_cast(floatx4, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(av[e], bv[e], c, 0, 0, 0);
+    return c;
+  } else {
+    return mfma16<DT == OIDN_BF16>(a, b, c);
+  }
+}
+
+// EPI kEpiLinear or kEpiGated; MF: fragments of 16 rows; NF: fragments of 16
+// columns of each projection.
+template <int DT, int EPI, int MF, int NF>
+__global__ __launch_bounds__(64 * kFewWaves) void dense_few(GemmArgs a) {
+  constexpr int kSize = DT == OIDN_F32 ? 4 : 2, kPer = 16 / kSize;   // elements of 16 bytes
+  constexpr int kChunk = 128 / kSize;
+  constexpr int kSets = EPI == kEpiGated ? 2 : 1, WF = NF * kSets;   // weight fragments
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int j0 = blockIdx.x * 16 * NF;
+  const long len = a.len;
+
+  const char* wp[WF];
+  const char* xp[MF];
+#pragma unroll
+  for (int f = 0; f < WF; ++f) {
+    int j = j0 + 16 * (f % NF) + r;
+    j = j < a.e.cols ? j : a.e.cols - 1;
+    wp[f] = static_cast<const char*>(a.p) + kSize * ((long)j + (f / NF) * (long)a.e.cols) * a.ldp;
+  }
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    long i = 16 * f + r;
+    i = i < a.e.rows ? i : a.e.rows - 1;
+    xp[f] = static_cast<const char*>(a.q) + kSize * i * a.ldq;
+  }
+  floatx4 acc[WF][MF];
+#pragma unroll
+  for (int f = 0; f < WF; ++f)
+#pragma unroll
+    for (int m = 0; m < MF; ++m) acc[f][m] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  auto load = [&](const char* row, long l) {
+    if (l + kPer <= len) return load16_any(row + kSize * l);
+    if (l < len) return part16<DT>(row + kSize * l, (int)(len - l));
+    return make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto load_whole = [&](const char* row, long l) { return load16_any(row + kSize * l); };
+  auto chunks = [&](long c, auto depth, auto ld) {      // `depth` chunks of this wave from chunk c on
+    constexpr int D = decltype(depth)::value;
+    uint4 w[D][2][WF], x[D][2][MF];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const long l = (c + d * kFewWaves) * kChunk + 2 * kPer * g + kPer * s;
+#pragma unroll
+        for (int f = 0; f < WF; ++f) w[d][s][f] = ld(wp[f], l);
+#pragma unroll
+        for (int m = 0; m < MF; ++m) x[d][s][m] = ld(xp[m], l);
+      }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int f = 0; f < WF; ++f)
+#pragma unroll
+          for (int m = 0; m < MF; ++m) acc[f][m] = multiply16<DT>(w[d][s][f], x[d][s][m], acc[f][m]);
+  };
+  const long whole = len / kChunk;
+  long c = wave;
+  for (; c + (kDepth - 1) * kFewWaves < whole; c += kDepth * kFewWaves)
+    chunks(c, std::integral_constant<int, kDepth>{}, load_whole);
+  for (; c < whole; c += kFewWaves) chunks(c, std::integral_constant<int, 1>{}, load_whole);
+  if (c == whole && len % kChunk) chunks(c, std::integral_constant<int, 1>{}, load);
+
+  // [wave][set][row][column]; a row's pitch is padded by 16 bytes
+  constexpr int kCols = 16 * NF, kPitch = kCols + 4;
+  __shared__ __attribute__((aligned(16))) float part[kFewWaves][kSets][16 * MF][kPitch];
+#pragma unroll
+  for (int f = 0; f < WF; ++f)
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+      *reinterpret_cast<floatx4*>(&part[wave][f / NF][16 * m + r][16 * (f % NF) + 4 * g]) = acc[f][m];
+  __syncthreads();
+  // eight columns of a row per lane; lanes of a row are neighbours
+  constexpr int kLanes = 2 * NF;
+  const int t = threadIdx.x, i = t / kLanes, j8 = 8 * (t % kLanes);
+  if (t >= 16 * MF * kLanes) return;         // whole groups of kLanes
+  Eight v[2] = {};
+#pragma unroll
+  for (int k = 0; k < kFewWaves; ++k)
+#pragma unroll
+    for (int s = 0; s < kSets; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[s].v[e] += part[k][s][i][j8 + e];
+  const int j = j0 + j8;
+  Fetched bias{}, f, none;
+  bias.a = bias8(a.e.bias, j, a.e.cols - j);
+  if constexpr (EPI == kEpiGated) bias.b = bias8(a.e.bias ? a.e.bias + a.e.cols : nullptr, j, a.e.cols - j);
+  if (whole_columns<EPI>(a.e, j0, kCols)) {
+    fetch<DT, EPI, true>(a.e, i, j, f);
+    finish<DT, EPI, 1, 2, true>(a.e, 0, i, j, v[0], v[1], bias, f, none);
+  } else {
+    fetch<DT, EPI, false>(a.e, i, j, f);
+    finish<DT, EPI, 1, 2, false>(a.e, 0, i, j, v[0], v[1], bias, f, none);
+  }
+}
+
+template <int DT, int EPI, int NF>
+hipError_t launch_rows(const GemmArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.e.cols + 16 * NF - 1) / (16 * NF))), block(64 * kFewWaves);
+  if (a.e.rows <= 16)
+    hipLaunchKernelGGL((dense_few<DT, EPI, 1, NF>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((dense_few<DT, EPI, 2, NF>), grid, block, 0, stream, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_type(const GemmArgs& a, int epi, hipStream_t stream) {
+  // 16 columns a workgroup, unless an 8-bit block of 32 has to be in one
+  const bool block32 = a.e.z && a.e.z8;
+  if (epi == kEpiLinear)
+    return block32 ? launch_rows<DT, kEpiLinear, 2>(a, stream) : launch_rows<DT, kEpiLinear, 1>(a, stream);
+  if (epi == kEpiGated)
+    return block32 ? launch_rows<DT, kEpiGated, 2>(a, stream) : launch_rows<DT, kEpiGated, 1>(a, stream);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_few(const GemmArgs& a, int epi, int dtype, hipStream_t stream) {
+  if (a.e.rows > kFewRows) return hipErrorInvalidValue;
+  if (dtype == OIDN_F32) return launch_type<OIDN_F32>(a, epi, stream);
+  return dtype == OIDN_F16 ? launch_type<OIDN_F16>(a, epi, stream) : launch_type<OIDN_BF16>(a, epi, stream);
+}
+
+}  // namespace oidn

@@ -82,6 +82,7 @@ __global__ __launch_bounds__(kRowThreads) void column_sum(const float* __restric
   const int c = threadIdx.x & 31, l = threadIdx.x >> 5, j = blockIdx.x * 32 + c;
   float s = 0.f;
   if (j < cols) {
+#pragma unroll 8
     for (long g = l; g < groups; g += 8) s += part[g * cols + j];
   }
   __shared__ float lds[8][32];
