@@ -31,9 +31,10 @@ enum DenseLayout { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 // What happens to the sums.
 enum DenseEpilogue {
   kEpiLinear = 0,     // bias, saved z, activation, residual, store
-  kEpiPartial = 1,    // fp32 sums of one slice of l to the workspace
+  kEpiPartial = 1,    // fp32 sums of one slice of l (any product with splits > 1)
   kEpiGated = 2,      // columns j and f + j of one product: h = act(a) * b
   kEpiGatedBack = 3,  // dh with the saved z: h, da, db and column sums of da, db
+  kEpiStore = 4,      // residual, store
 };
 
 // Bits of EpilogueArgs::vec: the tensor takes 16-byte accesses (base and row
@@ -84,20 +85,44 @@ GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int layout, int ep
 inline long gated_back_groups(long rows, int tile_r) { return (rows + tile_r - 1) / tile_r * 2; }
 constexpr int kMinTile = 64;
 
-// 16-bit products, one entry for each layout.
+// Workgroups of a product: its tiles, rounded up so that every slice starts on
+// the first XCD, times its slices.
+inline long gemm_blocks(const GemmArgs& a) {
+  return ((long)a.tiles_r * a.tiles_c + 7) / 8 * 8 * a.splits;
+}
+
+// Up to three gradients' products in one launch (kEpiStore), the ones with the
+// longest tiles first.
+constexpr int kMaxGroup = 3;
+struct GemmGroup {
+  int count;
+  int start[kMaxGroup];      // first workgroup of each
+  int layout[kMaxGroup];     // kInputGrad or kWeightGrad
+  GemmArgs a[kMaxGroup];
+};
+
+// 16-bit: kForward with kEpiLinear or kEpiGated, kInputGrad with kEpiGatedBack.
 hipError_t launch_gemm16_forward(const GemmArgs& a, const GemmPlan& p, int epi, bool bf16, hipStream_t stream);
-hipError_t launch_gemm16_input(const GemmArgs& a, const GemmPlan& p, int epi, bool bf16, hipStream_t stream);
-hipError_t launch_gemm16_weight(const GemmArgs& a, const GemmPlan& p, int epi, bool bf16,
-                          hipStream_t stream);
-hipError_t launch_gemm_f32(const GemmArgs& a, const GemmPlan& p, int layout, int epi,
-                           hipStream_t stream);
+hipError_t launch_gemm16_gated_back(const GemmArgs& a, const GemmPlan& p, bool bf16, hipStream_t stream);
+hipError_t launch_gemm16_group(const GemmGroup& g, const GemmPlan& p, bool bf16, hipStream_t stream);
+// fp32: the same.
+hipError_t launch_gemm32(const GemmArgs& a, const GemmPlan& p, int epi, hipStream_t stream);
+hipError_t launch_gemm32_group(const GemmGroup& g, const GemmPlan& p, hipStream_t stream);
 // Forward products (kEpiLinear, kEpiGated) of at most kFewRows rows, in one
 // launch without slices.
 constexpr int kFewRows = 32;
 hipError_t launch_few(const GemmArgs& a, int epi, int dtype, hipStream_t stream);
-// Adds the slices of kEpiPartial and runs the epilogue (kEpiLinear).
-hipError_t launch_split_sum(const EpilogueArgs& e, const float* part, int splits, int dtype,
-                            hipStream_t stream);
+// Adds a product's slices (e.part) and runs the epilogue (kEpiLinear).
+hipError_t launch_split_sum(const EpilogueArgs& e, int splits, int dtype, hipStream_t stream);
+
+// What ends a backward pass, in one launch: sums of products' slices
+// (kEpiStore) and of partial column sums, all in a fixed order.
+struct FinishArgs {
+  int products, columns;
+  struct { EpilogueArgs e; int splits; } product[kMaxGroup];
+  struct { const float* part; long groups; int cols; float* out; } column[2];
+};
+hipError_t launch_finish(const FinishArgs& a, int dtype, hipStream_t stream);
 
 // dz = dy * act'(z) (dz may be null: column sums alone; act none: z unused)
 // and, with part, partial column sums of dz over `chunk` rows: part[r / chunk][n].
@@ -117,10 +142,6 @@ struct SlopeArgs {
 };
 long slope_chunk(long rows);
 hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream);
-// out[j] = sum over `groups` rows of part (fixed order); groups may be 0.
-hipError_t launch_column_sum(const float* part, long groups, int cols, float* out,
-                             hipStream_t stream);
-
 hipError_t launch_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
                             hipStream_t stream);
 hipError_t launch_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ldy, int dtype,

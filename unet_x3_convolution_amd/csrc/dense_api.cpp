@@ -109,43 +109,99 @@ bool direct_operand(const void* p, long ld, long extent, long span) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0 && extent % 8 == 0 &&
          span * ld < (1L << 30);
 }
-int run_product(Product p, const void* q, long ldq, const void* pm, long ldp, const EpilogueArgs& e,
-                void* slices, hipStream_t stream, long* groups = nullptr) {
+GemmArgs gemm_args(Product& p, const void* q, long ldq, const void* pm, long ldp, const EpilogueArgs& e,
+                   void* slices) {
   if (p.dtype != OIDN_F32) {
     const bool ps = p.layout != kForward, qs = p.layout == kWeightGrad;
     p.plan.direct = direct_operand(q, ldq, qs ? p.rows : p.len, 256) &&
                     direct_operand(pm, ldp, ps ? p.cols : p.len, (p.epi == kEpiGated ? p.cols : 0) + 256);
   }
   if (!p.plan.direct && p.plan.tile_r > 128) p.plan.tile_r = p.plan.tile_c = 128;
-  if (groups) *groups = gated_back_groups(p.rows, p.plan.tile_r);
   GemmArgs a{};
   a.q = q;
   a.ldq = ldq;
   a.p = pm;
   a.ldp = ldp;
   a.len = p.len;
-  a.tiles_r = (int)((p.rows + p.plan.tile_r - 1) / p.plan.tile_r);
-  const long c = p.epi == kEpiGated ? p.plan.tile_c / 2 : p.plan.tile_c;
-  a.tiles_c = (int)((p.cols + c - 1) / c);
   a.splits = p.plan.splits;
   a.per_split = p.plan.per_split;
   a.e = e;
   a.e.rows = p.rows;
   a.e.cols = (int)p.cols;
-  const bool split = p.plan.splits > 1;
-  const int epi = split ? kEpiPartial : p.epi;
-  if (split) a.e.part = static_cast<float*>(slices);
+  if (p.plan.splits > 1) a.e.part = static_cast<float*>(slices);
+  return a;
+}
+void set_tiles(const Product& p, GemmArgs& a) {
+  a.tiles_r = (int)((p.rows + p.plan.tile_r - 1) / p.plan.tile_r);
+  const long c = p.epi == kEpiGated ? p.plan.tile_c / 2 : p.plan.tile_c;
+  a.tiles_c = (int)((p.cols + c - 1) / c);
+}
+// A forward or gated backward product; `groups` receives the row groups of the
+// latter's column sums.
+int run_product(Product p, const void* q, long ldq, const void* pm, long ldp, const EpilogueArgs& e,
+                void* slices, hipStream_t stream, long* groups = nullptr) {
+  GemmArgs a = gemm_args(p, q, ldq, pm, ldp, e, slices);
+  set_tiles(p, a);
+  if (groups) *groups = gated_back_groups(p.rows, p.plan.tile_r);
   hipError_t r;
-  if (p.plan.few) r = launch_few(a, epi, p.dtype, stream);
-  else if (p.dtype == OIDN_F32) r = launch_gemm_f32(a, p.plan, p.layout, epi, stream);
-  else if (p.layout == kForward) r = launch_gemm16_forward(a, p.plan, epi, p.dtype == OIDN_BF16, stream);
-  else if (p.layout == kInputGrad) r = launch_gemm16_input(a, p.plan, epi, p.dtype == OIDN_BF16, stream);
-  else r = launch_gemm16_weight(a, p.plan, epi, p.dtype == OIDN_BF16, stream);
+  if (p.plan.few) r = launch_few(a, p.epi, p.dtype, stream);
+  else if (p.dtype == OIDN_F32) r = launch_gemm32(a, p.plan, p.epi, stream);
+  else if (p.epi == kEpiGatedBack) r = launch_gemm16_gated_back(a, p.plan, p.dtype == OIDN_BF16, stream);
+  else r = launch_gemm16_forward(a, p.plan, p.epi, p.dtype == OIDN_BF16, stream);
   OIDN_TRY(ran(r, "matrix product launch"));
-  if (split)
-    OIDN_TRY(ran(launch_split_sum(a.e, a.e.part, p.plan.splits, p.dtype, stream), "slice sum launch"));
+  if (p.plan.splits > 1)
+    OIDN_TRY(ran(launch_split_sum(a.e, p.plan.splits, p.dtype, stream), "slice sum launch"));
   return OIDN_OK;
 }
+
+// The products that end a backward pass.  They run together in one launch
+// where they can share a kernel (same tile, operands alike), and what is left
+// to sum after them goes into `finish`.
+struct Gradients {
+  int dtype;
+  int count;
+  Product p[kMaxGroup];
+  GemmArgs a[kMaxGroup];
+  FinishArgs finish;
+  void add(const Product& pr, const void* q, long ldq, const void* pm, long ldp, const EpilogueArgs& e,
+           void* slices) {
+    p[count] = pr;
+    a[count] = gemm_args(p[count], q, ldq, pm, ldp, e, slices);
+    ++count;
+  }
+  void add_columns(const void* part, long groups, int cols, float* out) {
+    auto& c = finish.column[finish.columns++];
+    c.part = static_cast<const float*>(part);
+    c.groups = groups;
+    c.cols = cols;
+    c.out = out;
+  }
+  int run(hipStream_t stream) {
+    bool done[kMaxGroup] = {};
+    for (int first = 0; first < count; ++first) {
+      if (done[first]) continue;
+      const GemmPlan& plan = p[first].plan;
+      GemmGroup g{};
+      for (int k = first; k < count; ++k) {
+        if (done[k] || p[k].plan.tile_r != plan.tile_r || p[k].plan.direct != plan.direct) continue;
+        done[k] = true;
+        set_tiles(p[k], a[k]);
+        g.start[g.count] = g.count ? g.start[g.count - 1] + (int)gemm_blocks(g.a[g.count - 1]) : 0;
+        g.layout[g.count] = p[k].layout;
+        g.a[g.count++] = a[k];
+        if (p[k].plan.splits > 1) {
+          finish.product[finish.products].e = a[k].e;
+          finish.product[finish.products++].splits = p[k].plan.splits;
+        }
+      }
+      OIDN_TRY(ran(dtype == OIDN_F32 ? launch_gemm32_group(g, plan, stream)
+                                     : launch_gemm16_group(g, plan, dtype == OIDN_BF16, stream),
+                   "gradient products launch"));
+    }
+    return ran(launch_finish(finish, dtype, stream), "sums launch");
+  }
+};
+
 // The plain epilogue: store, with `add` (may be null) added.
 EpilogueArgs store_to(void* y, long ldy, const void* add, long ldadd, int dtype) {
   EpilogueArgs e{};
@@ -168,26 +224,25 @@ struct Regions {
   }
 };
 
-size_t most(size_t a, size_t b) { return a > b ? a : b; }
-
 // ---------------------------------------------------------------- linear
 struct LinearBack {
   Product dx, dw;
   long chunk, chunks;
-  void *dz, *x, *sums, *slices;
+  void *dz, *x, *sums, *dx_slices, *dw_slices;
   size_t bytes;
 };
 LinearBack linear_back(long m, int k, int n, int act, int dtype, unsigned flags, void* ws) {
   LinearBack b{};
-  b.dx = product(kInputGrad, kEpiLinear, m, k, n, dtype);
-  b.dw = product(kWeightGrad, kEpiLinear, n, k, m, dtype);
+  b.dx = product(kInputGrad, kEpiStore, m, k, n, dtype);
+  b.dw = product(kWeightGrad, kEpiStore, n, k, m, dtype);
   b.chunk = slope_chunk(m);
   b.chunks = (m + b.chunk - 1) / b.chunk;
   Regions r{static_cast<char*>(ws), 0};
   b.dz = act != OIDN_ACT_NONE ? r.take(bytes_of(m, n, dtype)) : nullptr;
   b.x = flags & OIDN_X_CKPT8 ? r.take(bytes_of(m, k, dtype)) : nullptr;
   b.sums = r.take(align256(b.chunks * (size_t)n * sizeof(float)));
-  b.slices = r.take(most(product_bytes(b.dx), product_bytes(b.dw)));
+  b.dx_slices = r.take(product_bytes(b.dx));
+  b.dw_slices = r.take(product_bytes(b.dw));
   b.bytes = r.used;
   return b;
 }
@@ -219,15 +274,15 @@ Ffn ffn_plan(long m, int d, int f, int dtype, void* ws) {
 struct FfnBack {
   Product dh, dx, dw_in, dw_out;
   long groups, chunk, chunks;
-  void *h, *dz, *x, *in_sums, *out_sums, *slices;
+  void *h, *dz, *x, *in_sums, *out_sums, *dx_slices, *in_slices, *out_slices;
   size_t bytes;
 };
 FfnBack ffn_back(long m, int d, int f, int dtype, unsigned flags, void* ws) {
   FfnBack b{};
   b.dh = product(kInputGrad, kEpiGatedBack, m, f, d, dtype);
-  b.dx = product(kInputGrad, kEpiLinear, m, d, 2L * f, dtype);
-  b.dw_in = product(kWeightGrad, kEpiLinear, 2L * f, d, m, dtype);
-  b.dw_out = product(kWeightGrad, kEpiLinear, d, f, m, dtype);
+  b.dx = product(kInputGrad, kEpiStore, m, d, 2L * f, dtype);
+  b.dw_in = product(kWeightGrad, kEpiStore, 2L * f, d, m, dtype);
+  b.dw_out = product(kWeightGrad, kEpiStore, d, f, m, dtype);
   b.groups = gated_back_groups(m, kMinTile);
   b.chunk = slope_chunk(m);
   b.chunks = (m + b.chunk - 1) / b.chunk;
@@ -237,7 +292,9 @@ FfnBack ffn_back(long m, int d, int f, int dtype, unsigned flags, void* ws) {
   b.x = flags & OIDN_X_CKPT8 ? r.take(bytes_of(m, d, dtype)) : nullptr;
   b.in_sums = r.take(align256(b.groups * 2 * (size_t)f * sizeof(float)));
   b.out_sums = r.take(align256(b.chunks * (size_t)d * sizeof(float)));
-  b.slices = r.take(most(product_bytes(b.dx), most(product_bytes(b.dw_in), product_bytes(b.dw_out))));
+  b.dx_slices = r.take(product_bytes(b.dx));
+  b.in_slices = r.take(product_bytes(b.dw_in));
+  b.out_slices = r.take(product_bytes(b.dw_out));
   b.bytes = r.used;
   return b;
 }
@@ -249,22 +306,6 @@ int check_ffn(long m, int d, int f, int dtype) {
     return fail(f < 1 ? OIDN_E_INVALID : OIDN_E_UNSUPPORTED, "hidden width %d is out of range", f);
   OIDN_TRY(check_size("z", m, 2L * f));
   return check_size("w_in", 2L * f, d);
-}
-
-// Column sums of dy (m x n) into out.
-int column_sums(const void* dy, long lddy, long m, int n, long chunk, long chunks, void* sums,
-                float* out, int dtype, hipStream_t stream) {
-  SlopeArgs s{};
-  s.dy = dy;
-  s.lddy = lddy;
-  s.part = static_cast<float*>(sums);
-  s.rows = m;
-  s.cols = n;
-  s.chunk = chunk;
-  s.act = OIDN_ACT_NONE;
-  s.vec = vec(dy, lddy, dtype) ? 1 : 0;
-  OIDN_TRY(ran(launch_slope(s, dtype, stream), "column sum launch"));
-  return ran(launch_column_sum(s.part, chunks, n, out, stream), "column sum launch");
 }
 
 }  // namespace
@@ -287,7 +328,7 @@ GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int layout, int ep
   // the largest tile that still gives every compute unit one
   if (tiles(128) >= 256) p.tile_r = p.tile_c = 128;
   if (dtype != OIDN_F32 && tiles(256) >= 256) p.tile_r = p.tile_c = 256;
-  if (epi == kEpiLinear && p.tile_r == 64 && tiles(64) < 256 && kt >= 8) {
+  if ((epi == kEpiLinear || epi == kEpiStore) && p.tile_r == 64 && tiles(64) < 256 && kt >= 8) {
     long s = (512 + tiles(64) - 1) / tiles(64);
     if (s > kt / 4) s = kt / 4;
     if (s > 1) {
@@ -417,7 +458,7 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
     s.ldz = ldz;
     s.z8 = z8;
     s.dz = slope ? b.dz : nullptr;
-    s.part = dbias ? static_cast<float*>(b.sums) : nullptr;
+    s.part = dbias && b.chunks > 1 ? static_cast<float*>(b.sums) : dbias;   // one chunk: the sums themselves
     s.rows = m;
     s.cols = n;
     s.chunk = b.chunk;
@@ -425,19 +466,21 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
     s.vec = (vec(dy, lddy, dtype) ? 1 : 0) | (slope && !z8 && vec(z, ldz, dtype) ? 2 : 0) |
             (slope && vec(b.dz, n, dtype) ? 4 : 0);
     OIDN_TRY(ran(launch_slope(s, dtype, stream), "slope pass launch"));
-    if (dbias) OIDN_TRY(ran(launch_column_sum(s.part, b.chunks, n, dbias, stream), "column sum launch"));
   }
   const void* dz = slope ? b.dz : dy;
   const long lddz = slope ? n : lddy;
-  if (dx) OIDN_TRY(run_product(b.dx, dz, lddz, w, ldw, store_to(dx, lddx, nullptr, 0, dtype), b.slices, stream));
+  Gradients g{dtype};
+  if (dbias && b.chunks > 1) g.add_columns(b.sums, b.chunks, n, dbias);
   if (dw) {
     if (x8) {
       OIDN_TRY(ran(launch_ckpt_unpack(x, m, k, b.x, k, dtype, stream), "checkpoint unpack launch"));
       x = b.x;
       ldx = k;
     }
-    OIDN_TRY(run_product(b.dw, dz, lddz, x, ldx, store_to(dw, lddw, nullptr, 0, dtype), b.slices, stream));
+    g.add(b.dw, dz, lddz, x, ldx, store_to(dw, lddw, nullptr, 0, dtype), b.dw_slices);
   }
+  if (dx) g.add(b.dx, dz, lddz, w, ldw, store_to(dx, lddx, nullptr, 0, dtype), b.dx_slices);
+  OIDN_TRY(g.run(stream));
   return clear_error();
 }
 
@@ -532,6 +575,7 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
   OIDN_TRY(check_workspace(workspace, ws_bytes, b.bytes));
 
   const long f2 = 2L * f;
+  Gradients g{dtype};
   if (inner) {
     EpilogueArgs e{};
     e.y = b.dz;
@@ -546,21 +590,33 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
             (!z8 && vec(z, f2, dtype, f) ? kVecZ : 0);
     long groups = 0;
     OIDN_TRY(run_product(b.dh, dy, lddy, w_out, f, e, nullptr, stream, &groups));
-    if (db_in) OIDN_TRY(ran(launch_column_sum(e.part, groups, (int)f2, db_in, stream), "column sum launch"));
+    if (db_in) g.add_columns(e.part, groups, (int)f2, db_in);
   }
-  if (db_out) OIDN_TRY(column_sums(dy, lddy, m, d, b.chunk, b.chunks, b.out_sums, db_out, dtype, stream));
-  if (dx)
-    OIDN_TRY(run_product(b.dx, b.dz, f2, w_in, d, store_to(dx, lddx, add, ldadd, dtype), b.slices, stream));
+  if (db_out) {
+    SlopeArgs s{};
+    s.dy = dy;
+    s.lddy = lddy;
+    s.part = b.chunks > 1 ? static_cast<float*>(b.out_sums) : db_out;
+    s.rows = m;
+    s.cols = d;
+    s.chunk = b.chunk;
+    s.act = OIDN_ACT_NONE;
+    s.vec = vec(dy, lddy, dtype) ? 1 : 0;
+    OIDN_TRY(ran(launch_slope(s, dtype, stream), "column sum launch"));
+    if (b.chunks > 1) g.add_columns(b.out_sums, b.chunks, d, db_out);
+  }
+  // the longest sums first
   if (dw_in) {
     if (x8) {
       OIDN_TRY(ran(launch_ckpt_unpack(x, m, d, b.x, d, dtype, stream), "checkpoint unpack launch"));
       x = b.x;
       ldx = d;
     }
-    OIDN_TRY(run_product(b.dw_in, b.dz, f2, x, ldx, store_to(dw_in, d, nullptr, 0, dtype), b.slices, stream));
+    g.add(b.dw_in, b.dz, f2, x, ldx, store_to(dw_in, d, nullptr, 0, dtype), b.in_slices);
   }
-  if (dw_out)
-    OIDN_TRY(run_product(b.dw_out, dy, lddy, b.h, f, store_to(dw_out, f, nullptr, 0, dtype), b.slices, stream));
+  if (dw_out) g.add(b.dw_out, dy, lddy, b.h, f, store_to(dw_out, f, nullptr, 0, dtype), b.out_slices);
+  if (dx) g.add(b.dx, b.dz, f2, w_in, d, store_to(dx, lddx, add, ldadd, dtype), b.dx_slices);
+  OIDN_TRY(g.run(stream));
   return clear_error();
 }
 

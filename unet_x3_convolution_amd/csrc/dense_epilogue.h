@@ -14,6 +14,13 @@ namespace {
 typedef float floatx8 __attribute__((ext_vector_type(8)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
 
+// Tile and slice of workgroup `block` (gemm_blocks); false for a padding one.
+__device__ __forceinline__ bool tile_and_slice(const GemmArgs& a, int block, int& tc, int& tr, int& slice) {
+  const int per = (a.tiles_r * a.tiles_c + kXcds - 1) / kXcds * kXcds;
+  slice = block / per;
+  return tile_of_block(block - slice * per, a.tiles_c, a.tiles_r, tc, tr);
+}
+
 // ------------------------------------------------------------ storage types
 // DT is OIDN_F32, OIDN_F16 or OIDN_BF16.  Values are computed in fp32 and
 // rounded to nearest even once, where they are stored.
@@ -283,20 +290,20 @@ __device__ __forceinline__ bool whole_columns(const EpilogueArgs& e, int j0, int
   if (j0 + width > e.cols) return false;
   if (EPI == kEpiPartial) return (e.cols & 3) == 0;
   unsigned need = kVecY;
-  if (EPI == kEpiLinear && e.res) need |= kVecRes;
+  if ((EPI == kEpiLinear || EPI == kEpiStore) && e.res) need |= kVecRes;
   if (EPI == kEpiGatedBack) need |= kVecH;
-  if (e.z && !e.z8) need |= kVecZ;
+  if (EPI != kEpiStore && e.z && !e.z8) need |= kVecZ;
   return (e.vec & need) == need;
 }
 
 template <int DT, int EPI, bool WHOLE>
 __device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, Fetched& f) {
   const int n = WHOLE ? 8 : e.cols - j;     // columns that exist from j on
-  if constexpr (EPI != kEpiLinear && EPI != kEpiGatedBack) return;
+  if constexpr (EPI == kEpiPartial || EPI == kEpiGated) return;
   if constexpr (WHOLE) i = i < e.rows ? i : e.rows - 1;
   else if (i >= e.rows || n <= 0) return;
   const bool full = WHOLE || n >= 8;
-  if constexpr (EPI == kEpiLinear) {
+  if constexpr (EPI == kEpiLinear || EPI == kEpiStore) {
     if (e.res) f.a = load8<DT>(e.res, i * e.ldr + j, WHOLE || (full && (e.vec & kVecRes)), n);
   }
   if constexpr (EPI == kEpiGatedBack) {
@@ -324,6 +331,9 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
     if (ok)
       store8<OIDN_F32>(e.part, ((long)slice * e.rows + i) * e.cols + j, x,
                        WHOLE || (full && (e.cols & 3) == 0), n);
+  } else if constexpr (EPI == kEpiStore) {
+    if (e.res) add8(x, f.a);
+    if (ok) store8<DT>(e.y, i * e.ldy + j, x, vec_y, n);
   } else if constexpr (EPI == kEpiLinear) {
     add8(x, bias.a);
     if (e.z) {
@@ -386,8 +396,9 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
 // 16-byte unit u of row r sits at u ^ (r % 16), which keeps both the writes
 // (16 rows of a unit) and the reads (neighbouring units of a row) on distinct
 // banks.  kEpiGated: the first half of the columns is the gate's.
-// lds: kEpiRows * 64 * FC bytes of this wave; i0, j0: its first row, column;
-// group: its row of the partial column sums.
+// lds: epilogue_bytes of this wave; i0, j0: its first row and column; slice:
+// -1 for a whole sum, else the slice that kEpiPartial stores; group: its row
+// of the partial column sums.
 template <int FR, int FC>
 constexpr int epilogue_rows() { return FR * FC > 32 ? 8 * FR : 16 * FR; }
 template <int FR, int FC>
@@ -396,6 +407,9 @@ constexpr int epilogue_bytes() { return epilogue_rows<FR, FC>() * 64 * FC; }
 template <int DT, int EPI, int FR, int FC>
 __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const floatx4 (&acc)[FC][FR], char* lds,
                                               long i0, int j0, int slice, long group) {
+  if constexpr (EPI == kEpiLinear || EPI == kEpiStore) {
+    if (slice >= 0) return tile_epilogue<DT, kEpiPartial, FR, FC>(e, acc, lds, i0, j0, slice, group);
+  }
   constexpr int kRows = epilogue_rows<FR, FC>();       // rows per round
   constexpr int kUnits = 4 * FC;                       // 16-byte units of a row
   constexpr int kMask = kUnits < 16 ? kUnits - 1 : 15;

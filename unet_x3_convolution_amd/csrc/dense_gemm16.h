@@ -119,25 +119,29 @@ struct Stage16 {
   }
 };
 
+template <int TR, int TC>
+constexpr int gemm16_lds() { return 2 * (TR + TC) * kDenseK * 2; }
+
+// Workgroup `block` of the product; lds: gemm16_lds<TR, TC>() bytes.
 template <bool BF, int LAYOUT, int EPI, int TR, int TC>
-__global__ __launch_bounds__(256, 2) void dense_gemm16(GemmArgs a) {
+__device__ __forceinline__ void gemm16_staged(const GemmArgs& a, int block, char* lds) {
   constexpr int DT = BF ? OIDN_BF16 : OIDN_F16;
   constexpr bool PS = LAYOUT != kForward, QS = LAYOUT == kWeightGrad;
   constexpr int FR = TR / 32, FC = TC / 32;      // 16-wide fragments per wave
   static_assert(EPI != kEpiGated || FC % 4 == 0, "a wave holds pairs of both projections");
   typedef Stage16<TC, PS, 256> P;
   typedef Stage16<TR, QS, 256> Q;
-  __shared__ __attribute__((aligned(16))) char lds[2][P::kBytes + Q::kBytes];
 
   int tc, tr;
-  if (!tile_of_block(blockIdx.x, a.tiles_c, a.tiles_r, tc, tr)) return;
+  int slice;
+  if (!tile_and_slice(a, block, tc, tr, slice)) return;
   const long i0 = (long)tr * TR;
   // a gated tile covers TC / 2 columns of both projections
   constexpr int C = EPI == kEpiGated ? TC / 2 : TC;
   const long j0 = (long)tc * C;
   const long half = EPI == kEpiGated ? a.e.cols : 0;
   const int wave = threadIdx.x >> 6, wr = wave >> 1, wc = wave & 1;
-  const long t0 = (long)blockIdx.y * a.per_split;
+  const long t0 = (long)slice * a.per_split;
   const long nt = (a.len + kDenseK - 1) / kDenseK;
   const long t1 = t0 + a.per_split < nt ? t0 + a.per_split : nt;
 
@@ -151,7 +155,7 @@ __global__ __launch_bounds__(256, 2) void dense_gemm16(GemmArgs a) {
   P::load(up, a.p, a.ldp, j0, a.e.cols, t0 * kDenseK, a.len, half);
   Q::load(uq, a.q, a.ldq, i0, a.e.rows, t0 * kDenseK, a.len, 0);
   for (long t = t0; t < t1; ++t) {
-    char* const lp = lds[(t - t0) & 1];
+    char* const lp = lds + ((t - t0) & 1) * (P::kBytes + Q::kBytes);
     char* const lq = lp + P::kBytes;
     // this buffer was last read two tiles ago, before the previous barrier
     P::store(up, lp);
@@ -184,8 +188,8 @@ __global__ __launch_bounds__(256, 2) void dense_gemm16(GemmArgs a) {
   }
 
   __syncthreads();                       // every wave has read its last fragments
-  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, &lds[0][0] + wave * epilogue_bytes<FR, FC>(),
-                                 i0 + wr * (TR / 2), (int)j0 + wc * (C / 2), blockIdx.y, (long)tr * 2 + wr);
+  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, lds + wave * epilogue_bytes<FR, FC>(), i0 + wr * (TR / 2),
+                                 (int)j0 + wc * (C / 2), a.splits > 1 ? slice : -1, (long)tr * 2 + wr);
 }
 
 }  // namespace

@@ -122,8 +122,10 @@ struct Direct16 {
   }
 };
 
+// Workgroup `block` of the product; lds: gemm16_lds<TR, TC>() bytes, two
+// buffers of a P and a Q tile.
 template <bool BF, int LAYOUT, int EPI, int TR, int TC>
-__global__ __launch_bounds__(256, TR * TC >= 256 * 256 ? 1 : 2) void dense_gemm16_direct(GemmArgs a) {
+__device__ __forceinline__ void gemm16_direct(const GemmArgs& a, int block, char* lds) {
   constexpr int DT = BF ? OIDN_BF16 : OIDN_F16;
   constexpr bool PS = LAYOUT != kForward, QS = LAYOUT == kWeightGrad;
   constexpr int FR = TR / 32, FC = TC / 32;
@@ -133,16 +135,16 @@ __global__ __launch_bounds__(256, TR * TC >= 256 * 256 ? 1 : 2) void dense_gemm1
   typedef typename PD::S P;
   typedef typename QD::S Q;
   constexpr unsigned kBuf = P::kBytes + Q::kBytes;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kBuf];    // two buffers: P tile, Q tile
 
   int tc, tr;
-  if (!tile_of_block(blockIdx.x, a.tiles_c, a.tiles_r, tc, tr)) return;
+  int slice;
+  if (!tile_and_slice(a, block, tc, tr, slice)) return;
   const long i0 = (long)tr * TR;
   constexpr int C = EPI == kEpiGated ? TC / 2 : TC;
   const long j0 = (long)tc * C;
   const long half = EPI == kEpiGated ? a.e.cols : 0;
   const int wave = threadIdx.x >> 6, wr = wave >> 1, wc = wave & 1;
-  const long t0 = (long)blockIdx.y * a.per_split;
+  const long t0 = (long)slice * a.per_split;
   const long nt = (a.len + kDenseK - 1) / kDenseK;
   const long t1 = t0 + a.per_split < nt ? t0 + a.per_split : nt;
   const long whole = a.len / kDenseK < t1 ? a.len / kDenseK : t1;   // tiles before it are complete
@@ -259,8 +261,34 @@ __global__ __launch_bounds__(256, TR * TC >= 256 * 256 ? 1 : 2) void dense_gemm1
            acc[(n + 3) / FR][(n + 3) % FR]);
   }
   __syncthreads();                       // every wave has read its last fragments
-  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, lds + wave * epilogue_bytes<FR, FC>(),
-                                 i0 + wr * (TR / 2), (int)j0 + wc * (C / 2), blockIdx.y, (long)tr * 2 + wr);
+  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, lds + wave * epilogue_bytes<FR, FC>(), i0 + wr * (TR / 2),
+                                 (int)j0 + wc * (C / 2), a.splits > 1 ? slice : -1, (long)tr * 2 + wr);
+}
+
+// The kernels.  DIRECT: operands go straight to LDS, else through registers.
+template <bool BF, int LAYOUT, int EPI, int TR, int TC, bool DIRECT>
+__device__ __forceinline__ void gemm16(const GemmArgs& a, int block, char* lds) {
+  if constexpr (DIRECT) gemm16_direct<BF, LAYOUT, EPI, TR, TC>(a, block, lds);
+  else gemm16_staged<BF, LAYOUT, EPI, TR, TC>(a, block, lds);
+}
+constexpr int workgroups_per_cu(int tr, int tc) { return tr * tc >= 256 * 256 ? 1 : 2; }
+
+template <bool BF, int LAYOUT, int EPI, int TR, int TC, bool DIRECT>
+__global__ __launch_bounds__(256, workgroups_per_cu(TR, TC)) void dense_gemm16(GemmArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[gemm16_lds<TR, TC>()];
+  gemm16<BF, LAYOUT, EPI, TR, TC, DIRECT>(a, blockIdx.x, lds);
+}
+
+// Several gradients' products in one launch: they fill the device together,
+// and the last tiles of one run beside the first of the next.
+template <bool BF, int T, bool DIRECT>
+__global__ __launch_bounds__(256, workgroups_per_cu(T, T)) void dense_gemm16_group(GemmGroup g) {
+  __shared__ __attribute__((aligned(1024))) char lds[gemm16_lds<T, T>()];
+  int k = 0;
+  while (k + 1 < g.count && (int)blockIdx.x >= g.start[k + 1]) ++k;
+  const int block = blockIdx.x - g.start[k];
+  if (g.layout[k] == kInputGrad) gemm16<BF, kInputGrad, kEpiStore, T, T, DIRECT>(g.a[k], block, lds);
+  else gemm16<BF, kWeightGrad, kEpiStore, T, T, DIRECT>(g.a[k], block, lds);
 }
 
 }  // namespace

@@ -72,24 +72,27 @@ struct Stage32 {
   }
 };
 
+template <int TR, int TC>
+constexpr int gemm32_lds() { return 2 * (TR + TC) * kPad32 * 4; }
+
 template <int LAYOUT, int EPI, int TR, int TC>
-__global__ __launch_bounds__(256, 2) void dense_gemm32(GemmArgs a) {
+__device__ __forceinline__ void gemm32(const GemmArgs& a, int block, float* lds) {
   constexpr int DT = OIDN_F32;
   constexpr bool PS = LAYOUT != kForward, QS = LAYOUT == kWeightGrad;
   constexpr int FR = TR / 32, FC = TC / 32;
   static_assert(EPI != kEpiGated || FC % 4 == 0, "a wave holds pairs of both projections");
   typedef Stage32<TC, PS> P;
   typedef Stage32<TR, QS> Q;
-  __shared__ __attribute__((aligned(16))) float lds[2][P::kFloats + Q::kFloats];
 
   int tc, tr;
-  if (!tile_of_block(blockIdx.x, a.tiles_c, a.tiles_r, tc, tr)) return;
+  int slice;
+  if (!tile_and_slice(a, block, tc, tr, slice)) return;
   const long i0 = (long)tr * TR;
   constexpr int C = EPI == kEpiGated ? TC / 2 : TC;
   const long j0 = (long)tc * C;
   const long half = EPI == kEpiGated ? a.e.cols : 0;
   const int wave = threadIdx.x >> 6, wr = wave >> 1, wc = wave & 1;
-  const long t0 = (long)blockIdx.y * a.per_split;
+  const long t0 = (long)slice * a.per_split;
   const long nt = (a.len + kDenseKF32 - 1) / kDenseKF32;
   const long t1 = t0 + a.per_split < nt ? t0 + a.per_split : nt;
 
@@ -103,7 +106,7 @@ __global__ __launch_bounds__(256, 2) void dense_gemm32(GemmArgs a) {
   P::load(up, a.p, a.ldp, j0, a.e.cols, t0 * kDenseKF32, a.len, half);
   Q::load(uq, a.q, a.ldq, i0, a.e.rows, t0 * kDenseKF32, a.len, 0);
   for (long t = t0; t < t1; ++t) {
-    float* const lp = lds[(t - t0) & 1];
+    float* const lp = lds + ((t - t0) & 1) * (P::kFloats + Q::kFloats);
     float* const lq = lp + P::kFloats;
     P::store(up, lp);
     Q::store(uq, lq);
@@ -137,40 +140,53 @@ __global__ __launch_bounds__(256, 2) void dense_gemm32(GemmArgs a) {
   }
 
   __syncthreads();                       // every wave has read its last fragments
-  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, reinterpret_cast<char*>(&lds[0][0]) + wave * epilogue_bytes<FR, FC>(),
-                                 i0 + wr * (TR / 2), (int)j0 + wc * (C / 2), blockIdx.y, (long)tr * 2 + wr);
+  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, reinterpret_cast<char*>(lds) + wave * epilogue_bytes<FR, FC>(),
+                                 i0 + wr * (TR / 2), (int)j0 + wc * (C / 2), a.splits > 1 ? slice : -1,
+                                 (long)tr * 2 + wr);
 }
 
 template <int LAYOUT, int EPI, int TR, int TC>
-hipError_t launch(const GemmArgs& a, const GemmPlan& p, hipStream_t stream) {
-  const unsigned blocks = (unsigned)((a.tiles_r * (long)a.tiles_c + kXcds - 1) / kXcds * kXcds);
-  hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, TR, TC>), dim3(blocks, p.splits), dim3(256), 0,
-                     stream, a);
-  return hipGetLastError();
+__global__ __launch_bounds__(256, 2) void dense_gemm32(GemmArgs a) {
+  __shared__ __attribute__((aligned(16))) float lds[gemm32_lds<TR, TC>() / 4];
+  gemm32<LAYOUT, EPI, TR, TC>(a, blockIdx.x, lds);
+}
+
+// Several gradients' products in one launch.
+template <int T>
+__global__ __launch_bounds__(256, 2) void dense_gemm32_group(GemmGroup g) {
+  __shared__ __attribute__((aligned(16))) float lds[gemm32_lds<T, T>() / 4];
+  int k = 0;
+  while (k + 1 < g.count && (int)blockIdx.x >= g.start[k + 1]) ++k;
+  const int block = blockIdx.x - g.start[k];
+  if (g.layout[k] == kInputGrad) gemm32<kInputGrad, kEpiStore, T, T>(g.a[k], block, lds);
+  else gemm32<kWeightGrad, kEpiStore, T, T>(g.a[k], block, lds);
 }
 
 template <int LAYOUT, int EPI>
 hipError_t launch_epi(const GemmArgs& a, const GemmPlan& p, hipStream_t stream) {
-  if (p.tile_r == 128) return launch<LAYOUT, EPI, 128, 128>(a, p, stream);
-  if constexpr (EPI == kEpiGated) return launch<LAYOUT, EPI, 64, 128>(a, p, stream);
-  else return launch<LAYOUT, EPI, 64, 64>(a, p, stream);
+  const dim3 grid((unsigned)gemm_blocks(a)), block(256);
+  constexpr int SC = EPI == kEpiGated ? 128 : 64;
+  if (p.tile_r == 128)
+    hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 128, 128>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 64, SC>), grid, block, 0, stream, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gemm_f32(const GemmArgs& a, const GemmPlan& p, int layout, int epi,
-                           hipStream_t stream) {
-  switch (layout * 4 + epi) {
-    case kForward * 4 + kEpiLinear: return launch_epi<kForward, kEpiLinear>(a, p, stream);
-    case kForward * 4 + kEpiPartial: return launch_epi<kForward, kEpiPartial>(a, p, stream);
-    case kForward * 4 + kEpiGated: return launch_epi<kForward, kEpiGated>(a, p, stream);
-    case kInputGrad * 4 + kEpiLinear: return launch_epi<kInputGrad, kEpiLinear>(a, p, stream);
-    case kInputGrad * 4 + kEpiPartial: return launch_epi<kInputGrad, kEpiPartial>(a, p, stream);
-    case kInputGrad * 4 + kEpiGatedBack: return launch_epi<kInputGrad, kEpiGatedBack>(a, p, stream);
-    case kWeightGrad * 4 + kEpiLinear: return launch_epi<kWeightGrad, kEpiLinear>(a, p, stream);
-    case kWeightGrad * 4 + kEpiPartial: return launch_epi<kWeightGrad, kEpiPartial>(a, p, stream);
-  }
+hipError_t launch_gemm32(const GemmArgs& a, const GemmPlan& p, int epi, hipStream_t stream) {
+  if (epi == kEpiLinear) return launch_epi<kForward, kEpiLinear>(a, p, stream);
+  if (epi == kEpiGated) return launch_epi<kForward, kEpiGated>(a, p, stream);
+  if (epi == kEpiGatedBack) return launch_epi<kInputGrad, kEpiGatedBack>(a, p, stream);
   return hipErrorInvalidValue;
+}
+
+hipError_t launch_gemm32_group(const GemmGroup& g, const GemmPlan& p, hipStream_t stream) {
+  const dim3 grid((unsigned)(g.start[g.count - 1] + gemm_blocks(g.a[g.count - 1]))), block(256);
+  if (p.tile_r == 128) hipLaunchKernelGGL(dense_gemm32_group<128>, grid, block, 0, stream, g);
+  else hipLaunchKernelGGL(dense_gemm32_group<64>, grid, block, 0, stream, g);
+  return hipGetLastError();
 }
 
 }  // namespace oidn

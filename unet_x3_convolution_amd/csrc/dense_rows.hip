@@ -8,32 +8,91 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// A thread sums eight columns of a row over the slices in order, so the result
-// does not depend on which workgroup finished when.  Four neighbouring lanes
-// hold a 32-column block.
-template <int DT>
-__global__ __launch_bounds__(kRowThreads) void split_sum(EpilogueArgs e, const float* __restrict__ part,
-                                                         int splits, long units, long total) {
-  const long t = (long)blockIdx.x * kRowThreads + threadIdx.x;
-  const long i = t / units;
-  const int j = (int)(t - i * units) * 8;
-  const int n = e.cols - j;
-  const bool ok = t < total && n > 0;
+// Sums of a product's slices: a workgroup takes 256 >> lg units of eight
+// columns, 1 << lg of its threads share a unit's slices, several reads in
+// flight each, and their sums are added in order, so the result does not
+// depend on timing.  Units of a row are padded to whole 32-column blocks: four
+// neighbouring threads hold one.
+template <int DT, int EPI>
+__device__ __forceinline__ void sum_slices(const EpilogueArgs& e, int splits, int lg, long block, char* lds) {
+  const int at_once = kRowThreads >> lg, u = threadIdx.x & (at_once - 1), lane = threadIdx.x >> (8 - lg);
+  const long units = (e.cols + 31) / 32 * 4, total = e.rows * units;
+  const long t = block * at_once + u, i = t / units;
+  const int j = (int)(t - i * units) * 8, n = e.cols - j;
   Eight x{};
-  if (ok) {
+  if (t < total && n > 0) {
     const bool vec = n >= 8 && (e.cols & 3) == 0;
     const long step = e.rows * (long)e.cols;
-    const float* p = part + i * e.cols + j;
-    for (int s = 0; s < splits; ++s) {
-      const Eight v = load8<OIDN_F32>(p, s * step, vec, n);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x.v[k] += v.v[k];
-    }
+    const float* p = e.part + i * e.cols + j;
+#pragma unroll 4
+    for (int s = lane; s < splits; s += 1 << lg) add8(x, load8<OIDN_F32>(p, s * step, vec, n));
+  }
+  if (lg) {
+    Eight* const sums = reinterpret_cast<Eight*>(lds);
+    if (lane) sums[threadIdx.x - at_once] = x;
+    __syncthreads();
+    if (lane) return;
+    for (int s = 1; s < 1 << lg; ++s) add8(x, sums[(s - 1) * at_once + u]);
   }
   Fetched f, none, bias{};
-  bias.a = bias8(e.bias, j, n);
-  fetch<DT, kEpiLinear, false>(e, i, j, f);
-  finish<DT, kEpiLinear, 1, 2, false>(e, 0, i, j, x, x, bias, f, none);
+  if constexpr (EPI == kEpiLinear) bias.a = bias8(e.bias, j, n);
+  fetch<DT, EPI, false>(e, i, j, f);
+  finish<DT, EPI, 1, 2, false>(e, 0, i, j, x, x, bias, f, none);
+}
+constexpr int kSumLds = kRowThreads * 32;
+
+// Threads that share a unit: as many as have four slices each, at most 8.
+int slice_lanes(int splits) {
+  int lg = 0;
+  while (lg < 3 && (8 << lg) <= splits) ++lg;
+  return lg;
+}
+long slice_blocks(const EpilogueArgs& e, int splits) {
+  const long per = kRowThreads >> slice_lanes(splits);
+  return (e.rows * ((e.cols + 31) / 32 * 4) + per - 1) / per;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void split_sum(EpilogueArgs e, int splits, int lg) {
+  __shared__ __attribute__((aligned(16))) char lds[kSumLds];
+  sum_slices<DT, kEpiLinear>(e, splits, lg, blockIdx.x, lds);
+}
+
+// 32 columns x 8 lanes over the groups of partial column sums.
+__device__ __forceinline__ void sum_columns(const float* __restrict__ part, long groups, int cols,
+                                            float* __restrict__ out, int block, char* mem) {
+  const int c = threadIdx.x & 31, l = threadIdx.x >> 5, j = block * 32 + c;
+  float s = 0.f;
+  if (j < cols) {
+#pragma unroll 8
+    for (long g = l; g < groups; g += 8) s += part[g * cols + j];
+  }
+  float* const lds = reinterpret_cast<float*>(mem);
+  lds[threadIdx.x] = s;
+  __syncthreads();
+  if (l == 0 && j < cols) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += lds[k * 32 + c];
+    out[j] = s;
+  }
+}
+
+struct FinishPlan {
+  int start[kMaxGroup + 2 + 1];     // first workgroup of each job, products first
+  int lg[kMaxGroup];
+};
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void finish_sums(FinishArgs a, FinishPlan p) {
+  __shared__ __attribute__((aligned(16))) char lds[kSumLds];
+  int k = 0;
+  while ((int)blockIdx.x >= p.start[k + 1]) ++k;
+  const int block = blockIdx.x - p.start[k];
+  if (k < a.products) {
+    sum_slices<DT, kEpiStore>(a.product[k].e, a.product[k].splits, p.lg[k], block, lds);
+  } else {
+    const auto& c = a.column[k - a.products];
+    sum_columns(c.part, c.groups, c.cols, c.out, block, lds);
+  }
 }
 
 // A workgroup covers `chunk` rows by 8 << cs columns: 1 << cs units of eight
@@ -47,19 +106,31 @@ __global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, int cs) {
   const long r0 = blockIdx.x * a.chunk, r1 = r0 + a.chunk < a.rows ? r0 + a.chunk : a.rows;
   Eight sum{};
   if (n > 0) {
-    for (long i = r0 + rl; i < r1; i += rows_at_once) {
-      Eight d = load8<DT>(a.dy, i * a.lddy + j, full && (a.vec & 1), n);
-      if (a.act != OIDN_ACT_NONE) {
-        const Eight z = a.z8 ? ckpt_load8(ckpt_at(const_cast<void*>(a.z), a.rows, a.cols), i, j)
-                             : load8<DT>(a.z, i * a.ldz + j, full && (a.vec & 2), n);
-        Eight slope = z, value;
-        activate_slope8<DT>(a.act, slope, value);
+    // four rows' reads in flight
+    for (long i0 = r0 + rl; i0 < r1; i0 += 4 * rows_at_once) {
+      Eight d[4], z[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d.v[k] *= slope.v[k];
+      for (int k = 0; k < 4; ++k) {
+        const long i = i0 + k * rows_at_once;
+        if (i >= r1) break;
+        d[k] = load8<DT>(a.dy, i * a.lddy + j, full && (a.vec & 1), n);
+        if (a.act != OIDN_ACT_NONE)
+          z[k] = a.z8 ? ckpt_load8(ckpt_at(const_cast<void*>(a.z), a.rows, a.cols), i, j)
+                      : load8<DT>(a.z, i * a.ldz + j, full && (a.vec & 2), n);
       }
-      if (a.dz) store8<DT>(a.dz, i * (long)a.cols + j, d, full && (a.vec & 4), n);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum.v[k] += d.v[k];
+      for (int k = 0; k < 4; ++k) {
+        const long i = i0 + k * rows_at_once;
+        if (i >= r1) break;
+        if (a.act != OIDN_ACT_NONE) {
+          Eight value;
+          activate_slope8<DT>(a.act, z[k], value);
+#pragma unroll
+          for (int m = 0; m < 8; ++m) d[k].v[m] *= z[k].v[m];
+        }
+        if (a.dz) store8<DT>(a.dz, i * (long)a.cols + j, d[k], full && (a.vec & 4), n);
+        add8(sum, d[k]);
+      }
     }
   }
   if (!a.part) return;
@@ -73,25 +144,6 @@ __global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, int cs) {
     for (int r = 0; r < rows_at_once; ++r) s += lds[(r << cs) + c / 8][c % 8];
     const int col = (int)(blockIdx.y << cs) * 8 + c;
     if (col < a.cols) a.part[(long)blockIdx.x * a.cols + col] = s;
-  }
-}
-
-// 32 columns x 8 lanes over the groups.
-__global__ __launch_bounds__(kRowThreads) void column_sum(const float* __restrict__ part, long groups,
-                                                          int cols, float* __restrict__ out) {
-  const int c = threadIdx.x & 31, l = threadIdx.x >> 5, j = blockIdx.x * 32 + c;
-  float s = 0.f;
-  if (j < cols) {
-#pragma unroll 8
-    for (long g = l; g < groups; g += 8) s += part[g * cols + j];
-  }
-  __shared__ float lds[8][32];
-  lds[l][c] = s;
-  __syncthreads();
-  if (l == 0 && j < cols) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) s += lds[k][c];
-    out[j] = s;
   }
 }
 
@@ -131,16 +183,28 @@ unsigned blocks_of(long n) { return (unsigned)((n + kRowThreads - 1) / kRowThrea
 
 }  // namespace
 
-hipError_t launch_split_sum(const EpilogueArgs& e, const float* part, int splits, int dtype,
-                            hipStream_t stream) {
-  const long units = ckpt_cols(e.cols) / 8, total = e.rows * units;
-  const dim3 grid(blocks_of(total)), block(kRowThreads);
-  if (dtype == OIDN_F32)
-    hipLaunchKernelGGL(split_sum<OIDN_F32>, grid, block, 0, stream, e, part, splits, units, total);
-  else if (dtype == OIDN_F16)
-    hipLaunchKernelGGL(split_sum<OIDN_F16>, grid, block, 0, stream, e, part, splits, units, total);
-  else
-    hipLaunchKernelGGL(split_sum<OIDN_BF16>, grid, block, 0, stream, e, part, splits, units, total);
+hipError_t launch_split_sum(const EpilogueArgs& e, int splits, int dtype, hipStream_t stream) {
+  const int lg = slice_lanes(splits);
+  const dim3 grid((unsigned)slice_blocks(e, splits)), block(kRowThreads);
+  if (dtype == OIDN_F32) hipLaunchKernelGGL(split_sum<OIDN_F32>, grid, block, 0, stream, e, splits, lg);
+  else if (dtype == OIDN_F16) hipLaunchKernelGGL(split_sum<OIDN_F16>, grid, block, 0, stream, e, splits, lg);
+  else hipLaunchKernelGGL(split_sum<OIDN_BF16>, grid, block, 0, stream, e, splits, lg);
+  return hipGetLastError();
+}
+
+hipError_t launch_finish(const FinishArgs& a, int dtype, hipStream_t stream) {
+  FinishPlan p{};
+  int k = 0;
+  for (; k < a.products; ++k) {
+    p.lg[k] = slice_lanes(a.product[k].splits);
+    p.start[k + 1] = p.start[k] + (int)slice_blocks(a.product[k].e, a.product[k].splits);
+  }
+  for (int c = 0; c < a.columns; ++c, ++k) p.start[k + 1] = p.start[k] + (a.column[c].cols + 31) / 32;
+  if (k == 0) return hipSuccess;
+  const dim3 grid((unsigned)p.start[k]), block(kRowThreads);
+  if (dtype == OIDN_F32) hipLaunchKernelGGL(finish_sums<OIDN_F32>, grid, block, 0, stream, a, p);
+  else if (dtype == OIDN_F16) hipLaunchKernelGGL(finish_sums<OIDN_F16>, grid, block, 0, stream, a, p);
+  else hipLaunchKernelGGL(finish_sums<OIDN_BF16>, grid, block, 0, stream, a, p);
   return hipGetLastError();
 }
 
@@ -162,13 +226,6 @@ hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream) {
     hipLaunchKernelGGL(slope_pass<OIDN_F16>, grid, dim3(kRowThreads), 0, stream, a, cs);
   else
     hipLaunchKernelGGL(slope_pass<OIDN_BF16>, grid, dim3(kRowThreads), 0, stream, a, cs);
-  return hipGetLastError();
-}
-
-hipError_t launch_column_sum(const float* part, long groups, int cols, float* out,
-                             hipStream_t stream) {
-  hipLaunchKernelGGL(column_sum, dim3((unsigned)((cols + 31) / 32)), dim3(kRowThreads), 0, stream, part,
-                     groups, cols, out);
   return hipGetLastError();
 }
 
