@@ -37,10 +37,6 @@ enum DenseEpilogue {
   kEpiStore = 4,      // residual, store
 };
 
-// Bits of EpilogueArgs::vec: the tensor takes 16-byte accesses (base and row
-// pitch multiples of 16 bytes).
-enum DenseVec { kVecRes = 1, kVecY = 2, kVecZ = 4, kVecH = 8 };
-
 struct EpilogueArgs {
   const float* bias;       // cols floats (kEpiGated: 2 * cols), may be null
   const void* res;         // rows x cols, row pitch ldr, may be null
@@ -52,7 +48,6 @@ struct EpilogueArgs {
   void* h;                 // kEpiGatedBack: rows x cols, contiguous
   float* part;             // kEpiPartial: [slice][rows][cols]; kEpiGatedBack: column sums or null
   int act;
-  unsigned vec;
   int z8;                  // z is held in 8 bits
   long rows;
   int cols;
@@ -80,7 +75,15 @@ struct GemmPlan {
 };
 constexpr int kDenseK = 64;      // summed length of one staged 16-bit tile
 constexpr int kDenseKF32 = 32;   // the same in fp32
-GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int layout, int epi);
+// Plans `count` (at most kMaxGroup) products that are to share a launch: one
+// tile for all, slices for each.  direct: the operands' sizes let them go
+// straight to LDS.
+struct PlanShape {
+  long rows, cols, len;
+  int epi;
+};
+constexpr int kMaxGroup = 3;
+void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, int dtype, bool direct);
 // Row groups of kEpiGatedBack's column sums: one per wave row of every tile.
 inline long gated_back_groups(long rows, int tile_r) { return (rows + tile_r - 1) / tile_r * 2; }
 constexpr int kMinTile = 64;
@@ -93,7 +96,6 @@ inline long gemm_blocks(const GemmArgs& a) {
 
 // Up to three gradients' products in one launch (kEpiStore), the ones with the
 // longest tiles first.
-constexpr int kMaxGroup = 3;
 struct GemmGroup {
   int count;
   int start[kMaxGroup];      // first workgroup of each
@@ -138,7 +140,6 @@ struct SlopeArgs {
   int cols;
   long chunk;
   int act;
-  unsigned vec;            // bit 0: dy, bit 1: z, bit 2: dz take 16-byte accesses
 };
 long slope_chunk(long rows);
 hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream);

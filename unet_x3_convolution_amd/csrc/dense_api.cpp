@@ -82,13 +82,6 @@ int check_workspace(const void* ws, size_t have, size_t need) {
     if (rc_) return rc_;      \
   } while (0)
 
-// Whether a tensor takes 16-byte accesses at every row and, with `step`, at
-// that many columns further.
-bool vec(const void* p, long ld, int dtype, long step = 0) {
-  const long e = (long)esize(dtype);
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * e % 16 == 0 && step * e % 16 == 0;
-}
-
 // One product: bytes of the workspace its slices take, and its launch.
 struct Product {
   int layout, epi;
@@ -96,8 +89,32 @@ struct Product {
   int dtype;
   GemmPlan plan;
 };
+// Whether the sizes alone let a 16-bit product's operands go straight to LDS.
+bool direct_sizes(const Product& p) {
+  const bool ps = p.layout != kForward, qs = p.layout == kWeightGrad;
+  return (qs ? p.rows : p.len) % 8 == 0 && (ps ? p.cols : p.len) % 8 == 0;
+}
+// Plans products that are to share a launch.
+void plan_together(Product* const* p, int count) {
+  GemmPlan* plans[kMaxGroup];
+  PlanShape shapes[kMaxGroup];
+  bool direct = true;
+  for (int k = 0; k < count; ++k) {
+    plans[k] = &p[k]->plan;
+    shapes[k] = {p[k]->rows, p[k]->cols, p[k]->len, p[k]->epi};
+    direct = direct && direct_sizes(*p[k]);
+  }
+  plan_products(plans, shapes, count, p[0]->dtype, direct);
+}
 Product product(int layout, int epi, long rows, long cols, long len, int dtype) {
-  return {layout, epi, rows, cols, len, dtype, plan_gemm(rows, cols, len, dtype, layout, epi)};
+  Product p{layout, epi, rows, cols, len, dtype, {}};
+  if (layout == kForward && rows <= kFewRows) {
+    p.plan = GemmPlan{64, 64, true, false, 1, 0};
+  } else {
+    Product* one = &p;
+    plan_together(&one, 1);
+  }
+  return p;
 }
 size_t product_bytes(const Product& p) {
   return p.plan.splits > 1 ? align256((size_t)p.plan.splits * p.rows * p.cols * sizeof(float)) : 0;
@@ -203,13 +220,12 @@ struct Gradients {
 };
 
 // The plain epilogue: store, with `add` (may be null) added.
-EpilogueArgs store_to(void* y, long ldy, const void* add, long ldadd, int dtype) {
+EpilogueArgs store_to(void* y, long ldy, const void* add, long ldadd) {
   EpilogueArgs e{};
   e.y = y;
   e.ldy = ldy;
   e.res = add;
   e.ldr = ldadd;
-  e.vec = (vec(y, ldy, dtype) ? kVecY : 0) | (add && vec(add, ldadd, dtype) ? kVecRes : 0);
   return e;
 }
 
@@ -233,8 +249,10 @@ struct LinearBack {
 };
 LinearBack linear_back(long m, int k, int n, int act, int dtype, unsigned flags, void* ws) {
   LinearBack b{};
-  b.dx = product(kInputGrad, kEpiStore, m, k, n, dtype);
-  b.dw = product(kWeightGrad, kEpiStore, n, k, m, dtype);
+  b.dx = Product{kInputGrad, kEpiStore, m, k, n, dtype, {}};
+  b.dw = Product{kWeightGrad, kEpiStore, n, k, m, dtype, {}};
+  Product* const both[] = {&b.dw, &b.dx};
+  plan_together(both, 2);
   b.chunk = slope_chunk(m);
   b.chunks = (m + b.chunk - 1) / b.chunk;
   Regions r{static_cast<char*>(ws), 0};
@@ -280,9 +298,11 @@ struct FfnBack {
 FfnBack ffn_back(long m, int d, int f, int dtype, unsigned flags, void* ws) {
   FfnBack b{};
   b.dh = product(kInputGrad, kEpiGatedBack, m, f, d, dtype);
-  b.dx = product(kInputGrad, kEpiStore, m, d, 2L * f, dtype);
-  b.dw_in = product(kWeightGrad, kEpiStore, 2L * f, d, m, dtype);
-  b.dw_out = product(kWeightGrad, kEpiStore, d, f, m, dtype);
+  b.dx = Product{kInputGrad, kEpiStore, m, d, 2L * f, dtype, {}};
+  b.dw_in = Product{kWeightGrad, kEpiStore, 2L * f, d, m, dtype, {}};
+  b.dw_out = Product{kWeightGrad, kEpiStore, d, f, m, dtype, {}};
+  Product* const all[] = {&b.dw_in, &b.dw_out, &b.dx};
+  plan_together(all, 3);
   b.groups = gated_back_groups(m, kMinTile);
   b.chunk = slope_chunk(m);
   b.chunks = (m + b.chunk - 1) / b.chunk;
@@ -312,31 +332,73 @@ int check_ffn(long m, int d, int f, int dtype) {
 
 namespace oidn {
 
-GemmPlan plan_gemm(long rows, long cols, long len, int dtype, int layout, int epi) {
+// Launch plans come from what the kernels were measured to take (us, one
+// MI355X, 256 compute units; q = tiles per compute unit, kt = staged tiles of
+// the summed length; 4096 x 1024 and 4096 x 4096 outputs, kt 1 to 32):
+//   64 x 64     3.5 + 0.27 kt at q = 1,  5.0 + 0.76 kt at q = 4,  14 + 2.6 kt at q = 16
+//   128 x 128   6.2 + 0.49 kt at q = 1,  15 + 1.6 kt at q = 4
+//   256 x 256   16 + 1.4 kt at q = 1,    19 + 2.9 kt at q = 2
+// that is, a start, a cost per tile, and per staged tile the larger of a
+// workgroup's own pace and its share of the compute unit's.  fp32 tiles hold
+// half as many summed elements at a sixteenth of the rate.  Summing slices
+// costs a launch and moves their bytes twice.
+struct TileCost { long tile; double start, each, own, share; };
+constexpr TileCost kCost16[] = {{64, 2.8, 0.7, 0.27, 0.17}, {128, 3.4, 2.9, 0.49, 0.40}, {256, 6.5, 9.0, 1.35, 1.40}};
+constexpr TileCost kCost32[] = {{64, 3.0, 1.0, 0.70, 0.55}, {128, 5.0, 4.0, 2.2, 2.0}};
+constexpr long kMaxSlices = 256;
+constexpr double kCus = 256, kSliceLaunch = 3.0, kSliceBytesPerUs = 4e6;
+
+void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, int dtype, bool direct) {
   const long bk = dtype == OIDN_F32 ? kDenseKF32 : kDenseK;
-  const long kt = (len + bk - 1) / bk;
-  auto tiles = [&](long t) {
-    const long c = epi == kEpiGated ? (t < 128 ? 64 : t / 2) : t;
-    return ((rows + t - 1) / t) * ((cols + c - 1) / c);
-  };
-  GemmPlan p{64, 64, false, false, 1, kt};
-  if (layout == kForward && rows <= kFewRows) {
-    p.few = true;
-    return p;
-  }
-  if (epi == kEpiGated) p.tile_c = 128;
-  // the largest tile that still gives every compute unit one
-  if (tiles(128) >= 256) p.tile_r = p.tile_c = 128;
-  if (dtype != OIDN_F32 && tiles(256) >= 256) p.tile_r = p.tile_c = 256;
-  if ((epi == kEpiLinear || epi == kEpiStore) && p.tile_r == 64 && tiles(64) < 256 && kt >= 8) {
-    long s = (512 + tiles(64) - 1) / tiles(64);
-    if (s > kt / 4) s = kt / 4;
-    if (s > 1) {
-      p.per_split = (kt + s - 1) / s;
-      p.splits = (int)((kt + p.per_split - 1) / p.per_split);
+  const TileCost* const table = dtype == OIDN_F32 ? kCost32 : kCost16;
+  const int choices = dtype == OIDN_F32 || !direct ? 2 : 3;
+  double best = 0;
+  for (int c = 0; c < choices; ++c) {
+    const TileCost& t = table[c];
+    long tiles[kMaxGroup], kt[kMaxGroup], longest = 1;
+    for (int k = 0; k < count; ++k) {
+      const PlanShape& s = shapes[k];
+      // a gated tile holds half its columns of each projection, 64 at least
+      const long tc = s.epi == kEpiGated ? (t.tile < 128 ? 64 : t.tile / 2) : t.tile;
+      tiles[k] = ((s.rows + t.tile - 1) / t.tile) * ((s.cols + tc - 1) / tc);
+      kt[k] = (s.len + bk - 1) / bk;
+      if (kt[k] > longest) longest = kt[k];
+    }
+    // slices of at most `cap` staged tiles, from none down to two tiles each
+    for (long cap = longest; cap >= 1; cap = cap * 3 / 4) {
+      GemmPlan tried[kMaxGroup];
+      double work = 0, number = 0, slices = 0, own = 0;
+      for (int k = 0; k < count; ++k) {
+        const PlanShape& s = shapes[k];
+        GemmPlan& p = tried[k];
+        p = GemmPlan{(int)t.tile, s.epi == kEpiGated && t.tile < 128 ? 128 : (int)t.tile, false, false, 1, kt[k]};
+        if ((s.epi == kEpiLinear || s.epi == kEpiStore) && kt[k] > cap && cap >= 2) {
+          long n = (kt[k] + cap - 1) / cap;
+          if (n > kMaxSlices) n = kMaxSlices;
+          p.per_split = (kt[k] + n - 1) / n;
+          p.splits = (int)((kt[k] + p.per_split - 1) / p.per_split);
+          if (p.splits > 1) slices += (double)p.splits * s.rows * s.cols * 8 / kSliceBytesPerUs;
+        }
+        number += (double)tiles[k] * p.splits;
+        work += (double)tiles[k] * kt[k];
+        if (t.own * p.per_split > own) own = t.own * p.per_split;
+      }
+      // a lone product goes in whole rounds; several fill each other's last one
+      double q = number / kCus;
+      if (count == 1 || q < 1) {
+        const double whole = (double)(long)((number + kCus - 1) / kCus);
+        work *= whole / q;
+        q = whole;
+      }
+      const double pace = t.share * work / kCus;
+      const double cost = t.start + t.each * q + (pace > own ? pace : own) + (slices > 0 ? kSliceLaunch + slices : 0);
+      if (best == 0 || cost < best) {
+        best = cost;
+        for (int k = 0; k < count; ++k) *plans[k] = tried[k];
+      }
+      if (cap < 3) break;
     }
   }
-  return p;
 }
 
 }  // namespace oidn
@@ -397,13 +459,12 @@ int oidn_linear(const void* x, long ldx, const void* w, long ldw, const float* b
   else OIDN_TRY(check_matrix("z", z, ldz, n, dtype, true));
   const Product p = product(kForward, kEpiLinear, m, n, k, dtype);
   OIDN_TRY(check_workspace(workspace, ws_bytes, product_bytes(p)));
-  EpilogueArgs e = store_to(y, ldy, residual, ldr, dtype);
+  EpilogueArgs e = store_to(y, ldy, residual, ldr);
   e.bias = bias;
   e.z = z;
   e.ldz = ldz;
   e.z8 = z8;
   e.act = act;
-  if (z && !z8 && vec(z, ldz, dtype)) e.vec |= kVecZ;
   OIDN_TRY(run_product(p, x, ldx, w, ldw, e, workspace, stream));
   return clear_error();
 }
@@ -463,8 +524,6 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
     s.cols = n;
     s.chunk = b.chunk;
     s.act = act;
-    s.vec = (vec(dy, lddy, dtype) ? 1 : 0) | (slope && !z8 && vec(z, ldz, dtype) ? 2 : 0) |
-            (slope && vec(b.dz, n, dtype) ? 4 : 0);
     OIDN_TRY(ran(launch_slope(s, dtype, stream), "slope pass launch"));
   }
   const void* dz = slope ? b.dz : dy;
@@ -477,9 +536,9 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
       x = b.x;
       ldx = k;
     }
-    g.add(b.dw, dz, lddz, x, ldx, store_to(dw, lddw, nullptr, 0, dtype), b.dw_slices);
+    g.add(b.dw, dz, lddz, x, ldx, store_to(dw, lddw, nullptr, 0), b.dw_slices);
   }
-  if (dx) g.add(b.dx, dz, lddz, w, ldw, store_to(dx, lddx, nullptr, 0, dtype), b.dx_slices);
+  if (dx) g.add(b.dx, dz, lddz, w, ldw, store_to(dx, lddx, nullptr, 0), b.dx_slices);
   OIDN_TRY(g.run(stream));
   return clear_error();
 }
@@ -513,15 +572,14 @@ int oidn_ffn(const void* x, long ldx, const void* w_in, const float* b_in, const
   const Ffn p = ffn_plan(m, d, f, dtype, workspace);
   OIDN_TRY(check_workspace(workspace, ws_bytes, p.bytes));
 
-  EpilogueArgs e = store_to(p.h, f, nullptr, 0, dtype);
+  EpilogueArgs e = store_to(p.h, f, nullptr, 0);
   e.bias = b_in;
   e.z = z;
   e.ldz = 2L * f;
   e.z8 = z8;
   e.act = act;
-  if (z && !z8 && vec(z, 2L * f, dtype, f)) e.vec |= kVecZ;
   OIDN_TRY(run_product(p.in, x, ldx, w_in, d, e, nullptr, stream));
-  EpilogueArgs o = store_to(y, ldy, residual, ldr, dtype);
+  EpilogueArgs o = store_to(y, ldy, residual, ldr);
   o.bias = b_out;
   OIDN_TRY(run_product(p.out, p.h, f, w_out, f, o, p.slices, stream));
   return clear_error();
@@ -586,8 +644,6 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
     e.z8 = z8;
     e.act = act;
     e.part = db_in ? static_cast<float*>(b.in_sums) : nullptr;
-    e.vec = (vec(b.dz, f2, dtype, f) ? kVecY : 0) | (vec(b.h, f, dtype) ? kVecH : 0) |
-            (!z8 && vec(z, f2, dtype, f) ? kVecZ : 0);
     long groups = 0;
     OIDN_TRY(run_product(b.dh, dy, lddy, w_out, f, e, nullptr, stream, &groups));
     if (db_in) g.add_columns(e.part, groups, (int)f2, db_in);
@@ -601,7 +657,6 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
     s.cols = d;
     s.chunk = b.chunk;
     s.act = OIDN_ACT_NONE;
-    s.vec = vec(dy, lddy, dtype) ? 1 : 0;
     OIDN_TRY(ran(launch_slope(s, dtype, stream), "column sum launch"));
     if (b.chunks > 1) g.add_columns(b.out_sums, b.chunks, d, db_out);
   }
@@ -612,10 +667,10 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
       x = b.x;
       ldx = d;
     }
-    g.add(b.dw_in, b.dz, f2, x, ldx, store_to(dw_in, d, nullptr, 0, dtype), b.in_slices);
+    g.add(b.dw_in, b.dz, f2, x, ldx, store_to(dw_in, d, nullptr, 0), b.in_slices);
   }
-  if (dw_out) g.add(b.dw_out, dy, lddy, b.h, f, store_to(dw_out, f, nullptr, 0, dtype), b.out_slices);
-  if (dx) g.add(b.dx, b.dz, f2, w_in, d, store_to(dx, lddx, add, ldadd, dtype), b.dx_slices);
+  if (dw_out) g.add(b.dw_out, dy, lddy, b.h, f, store_to(dw_out, f, nullptr, 0), b.out_slices);
+  if (dx) g.add(b.dx, b.dz, f2, w_in, d, store_to(dx, lddx, add, ldadd), b.dx_slices);
   OIDN_TRY(g.run(stream));
   return clear_error();
 }

@@ -40,22 +40,21 @@ __device__ __forceinline__ void store1(void* p, long i, float v) {
   static_cast<typename Storage<DT>::T*>(p)[i] = (typename Storage<DT>::T)v;
 }
 
-// Eight elements from element offset i; `vec`: the address is a multiple of
-// 16 bytes and all eight exist, else only the first n are read (0 after).
+// Eight elements from element offset i, of which n (if less than eight) exist;
+// 0 in place of the others.  Accesses are 16 bytes wide at any element
+// alignment (unaligned access is enabled on this target).
 template <int DT>
-__device__ __forceinline__ Eight load8(const void* p, long i, bool vec, int n) {
+__device__ __forceinline__ Eight load8(const void* p, long i, int n) {
   typedef typename Storage<DT>::T T;
   const T* s = static_cast<const T*>(p) + i;
   Eight r;
-  if (vec) {
+  if (n >= 8) {
     if constexpr (DT == OIDN_F32) {
-      const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
-      r.v[0] = a.x; r.v[1] = a.y; r.v[2] = a.z; r.v[3] = a.w;
-      r.v[4] = b.x; r.v[5] = b.y; r.v[6] = b.z; r.v[7] = b.w;
+      __builtin_memcpy(r.v, s, 32);
     } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(s);
       typedef T T8 __attribute__((ext_vector_type(8)));
-      const T8 t = __builtin_bit_cast(T8, u);
+      T8 t;
+      __builtin_memcpy(&t, s, 16);
 #pragma unroll
       for (int k = 0; k < 8; ++k) r.v[k] = (float)t[k];
     }
@@ -67,19 +66,18 @@ __device__ __forceinline__ Eight load8(const void* p, long i, bool vec, int n) {
 }
 
 template <int DT>
-__device__ __forceinline__ void store8(void* p, long i, const Eight& r, bool vec, int n) {
+__device__ __forceinline__ void store8(void* p, long i, const Eight& r, int n) {
   typedef typename Storage<DT>::T T;
   T* s = static_cast<T*>(p) + i;
-  if (vec) {
+  if (n >= 8) {
     if constexpr (DT == OIDN_F32) {
-      reinterpret_cast<float4*>(s)[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-      reinterpret_cast<float4*>(s)[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+      __builtin_memcpy(s, r.v, 32);
     } else {
       typedef T T8 __attribute__((ext_vector_type(8)));
       T8 t;
 #pragma unroll
       for (int k = 0; k < 8; ++k) t[k] = (T)r.v[k];
-      *reinterpret_cast<uint4*>(s) = __builtin_bit_cast(uint4, t);
+      __builtin_memcpy(s, &t, 16);
     }
   } else {
 #pragma unroll
@@ -227,8 +225,7 @@ __device__ __forceinline__ Eight ckpt_load8(const CkptAt& c, long i, int j) {
 // the epilogue needs from memory, finish() computes and stores; apart, so that
 // several rows' reads are in flight together.  All lanes call finish(): the
 // 8-bit stores exchange maxima between the lanes XOR A and XOR B.
-// WHOLE: all eight columns exist and every tensor takes 16-byte accesses
-// (whole_columns()), so no element is looked at by itself.
+// WHOLE: all eight columns exist, so no element is looked at by itself.
 __device__ __forceinline__ Eight bias8(const float* bias, int j, int n) {
   Eight b{};
   if (bias) {
@@ -284,36 +281,22 @@ __device__ __forceinline__ void activate_slope8(int act, Eight& z, Eight& g) {
 
 struct Fetched { Eight a, b; };
 
-// Whether columns j0 .. j0 + width - 1 can be taken as WHOLE.
-template <int EPI>
-__device__ __forceinline__ bool whole_columns(const EpilogueArgs& e, int j0, int width) {
-  if (j0 + width > e.cols) return false;
-  if (EPI == kEpiPartial) return (e.cols & 3) == 0;
-  unsigned need = kVecY;
-  if ((EPI == kEpiLinear || EPI == kEpiStore) && e.res) need |= kVecRes;
-  if (EPI == kEpiGatedBack) need |= kVecH;
-  if (EPI != kEpiStore && e.z && !e.z8) need |= kVecZ;
-  return (e.vec & need) == need;
-}
-
 template <int DT, int EPI, bool WHOLE>
 __device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, Fetched& f) {
   const int n = WHOLE ? 8 : e.cols - j;     // columns that exist from j on
   if constexpr (EPI == kEpiPartial || EPI == kEpiGated) return;
   if constexpr (WHOLE) i = i < e.rows ? i : e.rows - 1;
   else if (i >= e.rows || n <= 0) return;
-  const bool full = WHOLE || n >= 8;
   if constexpr (EPI == kEpiLinear || EPI == kEpiStore) {
-    if (e.res) f.a = load8<DT>(e.res, i * e.ldr + j, WHOLE || (full && (e.vec & kVecRes)), n);
+    if (e.res) f.a = load8<DT>(e.res, i * e.ldr + j, n);
   }
   if constexpr (EPI == kEpiGatedBack) {
     if (e.z8) {
       f.a = ckpt_load8(ckpt_at(e.z, e.rows, e.cols), i, j);
       f.b = ckpt_load8(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols), i, j);
     } else {
-      const bool vec = WHOLE || (full && (e.vec & kVecZ));
-      f.a = load8<DT>(e.z, i * e.ldz + j, vec, n);
-      f.b = load8<DT>(e.z, i * e.ldz + e.cols + j, vec, n);
+      f.a = load8<DT>(e.z, i * e.ldz + j, n);
+      f.b = load8<DT>(e.z, i * e.ldz + e.cols + j, n);
     }
   }
 }
@@ -325,15 +308,13 @@ template <int DT, int EPI, int A, int B, bool WHOLE>
 __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i, int j, Eight x, Eight u,
                                        const Fetched& bias, Fetched& f, Fetched& sums) {
   const int n = WHOLE ? 8 : e.cols - j;
-  const bool row_ok = i < e.rows, ok = row_ok && n > 0, full = n >= 8;
-  const bool vec_y = WHOLE || (full && (e.vec & kVecY)), vec_z = WHOLE || (full && (e.vec & kVecZ));
+  const bool row_ok = i < e.rows, ok = row_ok && n > 0;
   if constexpr (EPI == kEpiPartial) {       // fp32 sums of one slice
     if (ok)
-      store8<OIDN_F32>(e.part, ((long)slice * e.rows + i) * e.cols + j, x,
-                       WHOLE || (full && (e.cols & 3) == 0), n);
+      store8<OIDN_F32>(e.part, ((long)slice * e.rows + i) * e.cols + j, x, n);
   } else if constexpr (EPI == kEpiStore) {
     if (e.res) add8(x, f.a);
-    if (ok) store8<DT>(e.y, i * e.ldy + j, x, vec_y, n);
+    if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
   } else if constexpr (EPI == kEpiLinear) {
     add8(x, bias.a);
     if (e.z) {
@@ -341,12 +322,12 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
         if constexpr (!WHOLE) clear_tail(n, x);
         ckpt_store8<A, B>(ckpt_at(e.z, e.rows, e.cols), i, j, x, row_ok);
       } else if (ok) {
-        store8<DT>(e.z, i * e.ldz + j, x, vec_z, n);
+        store8<DT>(e.z, i * e.ldz + j, x, n);
       }
     }
     activate8<DT>(e.act, x);
     if (e.res) add8(x, f.a);
-    if (ok) store8<DT>(e.y, i * e.ldy + j, x, vec_y, n);
+    if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
   } else if constexpr (EPI == kEpiGated) {
     add8(x, bias.a);
     add8(u, bias.b);
@@ -360,14 +341,14 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
         ckpt_store8<A, B>(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols),
                           i, j, u, row_ok);
       } else if (ok) {
-        store8<DT>(e.z, i * e.ldz + j, x, vec_z, n);
-        store8<DT>(e.z, i * e.ldz + e.cols + j, u, vec_z, n);
+        store8<DT>(e.z, i * e.ldz + j, x, n);
+        store8<DT>(e.z, i * e.ldz + e.cols + j, u, n);
       }
     }
     activate8<DT>(e.act, x);
 #pragma unroll
     for (int k = 0; k < 8; ++k) x.v[k] *= u.v[k];
-    if (ok) store8<DT>(e.y, i * e.ldy + j, x, vec_y, n);
+    if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
   } else {                                  // x is dh: h and [da | db]
     Eight g, h, da, db;
     activate_slope8<DT>(e.act, f.a, g);
@@ -382,9 +363,9 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
         sums.b.v[k] += db.v[k];
       }
     }
-    store8<DT>(e.h, i * (long)e.cols + j, h, WHOLE || (full && (e.vec & kVecH)), n);
-    store8<DT>(e.y, i * e.ldy + j, da, vec_y, n);
-    store8<DT>(e.y, i * e.ldy + e.cols + j, db, vec_y, n);
+    store8<DT>(e.h, i * (long)e.cols + j, h, n);
+    store8<DT>(e.y, i * e.ldy + j, da, n);
+    store8<DT>(e.y, i * e.ldy + e.cols + j, db, n);
   }
 }
 
@@ -455,7 +436,7 @@ __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const float
       }
     }
   };
-  const bool whole = whole_columns<EPI>(e, j0, 8 * kLanes);
+  const bool whole = j0 + 8 * kLanes <= e.cols;
   constexpr int kRounds = 16 * FR / kRows;
 #pragma unroll 1
   for (int round = 0; round < kRounds; ++round) {

@@ -134,7 +134,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void dense_few(GemmArgs a) {
   Fetched bias{}, f, none;
   bias.a = bias8(a.e.bias, j, a.e.cols - j);
   if constexpr (EPI == kEpiGated) bias.b = bias8(a.e.bias ? a.e.bias + a.e.cols : nullptr, j, a.e.cols - j);
-  if (whole_columns<EPI>(a.e, j0, kCols)) {
+  if (j0 + kCols <= a.e.cols) {
     fetch<DT, EPI, true>(a.e, i, j, f);
     finish<DT, EPI, 1, 2, true>(a.e, 0, i, j, v[0], v[1], bias, f, none);
   } else {

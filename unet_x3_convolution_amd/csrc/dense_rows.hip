@@ -21,11 +21,10 @@ __device__ __forceinline__ void sum_slices(const EpilogueArgs& e, int splits, in
   const int j = (int)(t - i * units) * 8, n = e.cols - j;
   Eight x{};
   if (t < total && n > 0) {
-    const bool vec = n >= 8 && (e.cols & 3) == 0;
     const long step = e.rows * (long)e.cols;
     const float* p = e.part + i * e.cols + j;
 #pragma unroll 4
-    for (int s = lane; s < splits; s += 1 << lg) add8(x, load8<OIDN_F32>(p, s * step, vec, n));
+    for (int s = lane; s < splits; s += 1 << lg) add8(x, load8<OIDN_F32>(p, s * step, n));
   }
   if (lg) {
     Eight* const sums = reinterpret_cast<Eight*>(lds);
@@ -102,7 +101,6 @@ __global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, int cs) {
   const int u = threadIdx.x & ((1 << cs) - 1), rl = threadIdx.x >> cs, rows_at_once = kRowThreads >> cs;
   const int j = (int)((blockIdx.y << cs) + u) * 8;
   const int n = a.cols - j;
-  const bool full = n >= 8;
   const long r0 = blockIdx.x * a.chunk, r1 = r0 + a.chunk < a.rows ? r0 + a.chunk : a.rows;
   Eight sum{};
   if (n > 0) {
@@ -113,10 +111,10 @@ __global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, int cs) {
       for (int k = 0; k < 4; ++k) {
         const long i = i0 + k * rows_at_once;
         if (i >= r1) break;
-        d[k] = load8<DT>(a.dy, i * a.lddy + j, full && (a.vec & 1), n);
+        d[k] = load8<DT>(a.dy, i * a.lddy + j, n);
         if (a.act != OIDN_ACT_NONE)
           z[k] = a.z8 ? ckpt_load8(ckpt_at(const_cast<void*>(a.z), a.rows, a.cols), i, j)
-                      : load8<DT>(a.z, i * a.ldz + j, full && (a.vec & 2), n);
+                      : load8<DT>(a.z, i * a.ldz + j, n);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -128,7 +126,7 @@ __global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, int cs) {
 #pragma unroll
           for (int m = 0; m < 8; ++m) d[k].v[m] *= z[k].v[m];
         }
-        if (a.dz) store8<DT>(a.dz, i * (long)a.cols + j, d[k], full && (a.vec & 4), n);
+        if (a.dz) store8<DT>(a.dz, i * (long)a.cols + j, d[k], n);
         add8(sum, d[k]);
       }
     }
@@ -150,24 +148,23 @@ __global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, int cs) {
 // A thread codes eight columns; four neighbouring lanes hold a block.
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void ckpt_pack(const void* __restrict__ x, long ldx, long m,
-                                                         long n, void* ckpt, long units, long total,
-                                                         int vec) {
+                                                         long n, void* ckpt, long units, long total) {
   const long t = (long)blockIdx.x * kRowThreads + threadIdx.x;
   const long i = t / units, j = (t - i * units) * 8;
   Eight v{};
   const int left = n - j < 8 ? (int)(n - j) : 8;
-  if (t < total && left > 0) v = load8<DT>(x, i * ldx + j, vec && left == 8, left);
+  if (t < total && left > 0) v = load8<DT>(x, i * ldx + j, left);
   ckpt_store8<1, 2>(ckpt_at(ckpt, m, n), i, (int)j, v, t < total);
 }
 
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void ckpt_unpack(void* ckpt, long m, long n, void* __restrict__ y,
-                                                           long ldy, long units, long total, int vec) {
+                                                           long ldy, long units, long total) {
   const long t = (long)blockIdx.x * kRowThreads + threadIdx.x;
   const long i = t / units, j = (t - i * units) * 8;
   const int left = n - j < 8 ? (int)(n - j) : 8;
   if (t >= total || left <= 0) return;
-  store8<DT>(y, i * ldy + j, ckpt_load8(ckpt_at(ckpt, m, n), i, (int)j), vec && left == 8, left);
+  store8<DT>(y, i * ldy + j, ckpt_load8(ckpt_at(ckpt, m, n), i, (int)j), left);
 }
 
 __global__ __launch_bounds__(kRowThreads) void zero_bytes(unsigned char* p, size_t n) {
@@ -175,10 +172,6 @@ __global__ __launch_bounds__(kRowThreads) void zero_bytes(unsigned char* p, size
   for (size_t i = (size_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += step) p[i] = 0;
 }
 
-bool vec16(const void* p, long ld, int dtype) {
-  const long e = dtype == OIDN_F32 ? 4 : 2;
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * e % 16 == 0;
-}
 unsigned blocks_of(long n) { return (unsigned)((n + kRowThreads - 1) / kRowThreads); }
 
 }  // namespace
@@ -232,14 +225,13 @@ hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream) {
 hipError_t launch_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
                             hipStream_t stream) {
   const long units = ckpt_cols(n) / 8, total = m * units;
-  const int vec = vec16(x, ldx, dtype);
   const dim3 grid(blocks_of(total)), block(kRowThreads);
   if (dtype == OIDN_F32)
-    hipLaunchKernelGGL(ckpt_pack<OIDN_F32>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total, vec);
+    hipLaunchKernelGGL(ckpt_pack<OIDN_F32>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total);
   else if (dtype == OIDN_F16)
-    hipLaunchKernelGGL(ckpt_pack<OIDN_F16>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total, vec);
+    hipLaunchKernelGGL(ckpt_pack<OIDN_F16>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total);
   else
-    hipLaunchKernelGGL(ckpt_pack<OIDN_BF16>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total, vec);
+    hipLaunchKernelGGL(ckpt_pack<OIDN_BF16>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total);
   return hipGetLastError();
 }
 
@@ -247,14 +239,13 @@ hipError_t launch_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ld
                               hipStream_t stream) {
   void* const c = const_cast<void*>(ckpt);
   const long units = (n + 7) / 8, total = m * units;
-  const int vec = vec16(y, ldy, dtype);
   const dim3 grid(blocks_of(total)), block(kRowThreads);
   if (dtype == OIDN_F32)
-    hipLaunchKernelGGL(ckpt_unpack<OIDN_F32>, grid, block, 0, stream, c, m, n, y, ldy, units, total, vec);
+    hipLaunchKernelGGL(ckpt_unpack<OIDN_F32>, grid, block, 0, stream, c, m, n, y, ldy, units, total);
   else if (dtype == OIDN_F16)
-    hipLaunchKernelGGL(ckpt_unpack<OIDN_F16>, grid, block, 0, stream, c, m, n, y, ldy, units, total, vec);
+    hipLaunchKernelGGL(ckpt_unpack<OIDN_F16>, grid, block, 0, stream, c, m, n, y, ldy, units, total);
   else
-    hipLaunchKernelGGL(ckpt_unpack<OIDN_BF16>, grid, block, 0, stream, c, m, n, y, ldy, units, total, vec);
+    hipLaunchKernelGGL(ckpt_unpack<OIDN_BF16>, grid, block, 0, stream, c, m, n, y, ldy, units, total);
   return hipGetLastError();
 }
 
