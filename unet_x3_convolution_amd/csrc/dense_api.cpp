@@ -344,6 +344,7 @@ namespace oidn {
 // costs a launch and moves their bytes twice.
 struct TileCost { long tile; double start, each, own, share; };
 constexpr TileCost kCost16[] = {{64, 2.8, 0.7, 0.27, 0.17}, {128, 3.4, 2.9, 0.49, 0.40}, {256, 6.5, 9.0, 1.35, 1.40}};
+constexpr TileCost kCostGated = {64, 2.8, 1.3, 0.35, 0.30};      // a gated product's 64 x 128
 constexpr TileCost kCost32[] = {{64, 3.0, 1.0, 0.70, 0.55}, {128, 5.0, 4.0, 2.2, 2.0}};
 constexpr long kMaxSlices = 256;
 constexpr double kCus = 256, kSliceLaunch = 3.0, kSliceBytesPerUs = 4e6;
@@ -354,7 +355,7 @@ void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, i
   const int choices = dtype == OIDN_F32 || !direct ? 2 : 3;
   double best = 0;
   for (int c = 0; c < choices; ++c) {
-    const TileCost& t = table[c];
+    const TileCost t = shapes[0].epi == kEpiGated && table[c].tile == 64 ? kCostGated : table[c];
     long tiles[kMaxGroup], kt[kMaxGroup], longest = 1;
     for (int k = 0; k < count; ++k) {
       const PlanShape& s = shapes[k];

@@ -105,21 +105,20 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
     const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * 0.70710678f * __builtin_fabsf(z));
     const float poly = t * (0.254829592f + t * (-0.284496736f +
                        t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-    const float tail = 0.5f * poly * e;        // Phi(-|z|)
-    return z >= 0.f ? 1.f - tail : tail;
+    return 0.5f + __builtin_copysignf(0.5f - 0.5f * poly * e, z);   // 0.5 poly e = Phi(-|z|)
   }
 }
 
 // Past |z| = 100 (silu) and 30 (gelu) the functions have reached 0, z and the
-// slopes 0, 1 in fp32; taking them there keeps infinities from giving 0 * inf.
-// NaN stays NaN.
+// slopes 0, 1 in fp32; holding the factor z there keeps infinities from giving
+// 0 * inf.  NaN stays NaN through the other factor.
 template <int DT>
 __device__ __forceinline__ float activate(int act, float z) {
   if (act == OIDN_ACT_RELU) return z < 0.f ? 0.f : z;
-  if (act == OIDN_ACT_SILU) return z < -100.f ? 0.f : z * logistic(z);
+  if (act == OIDN_ACT_SILU) return fmaxf(z, -100.f) * logistic(z);
   if (act == OIDN_ACT_GELU) {
     float e;
-    return z < -30.f ? 0.f : z * normal_cdf<DT>(z, e);
+    return fmaxf(z, -30.f) * normal_cdf<DT>(z, e);
   }
   return z;
 }
@@ -132,12 +131,12 @@ __device__ __forceinline__ void activate_slope(int act, float z, float& a, float
     s = z < 0.f ? 0.f : s;
   } else if (act == OIDN_ACT_SILU) {
     const float p = logistic(z), c = fminf(fmaxf(z, -100.f), 100.f);
-    a = z < -100.f ? 0.f : z * p;
+    a = fmaxf(z, -100.f) * p;
     s = p + c * p * (1.f - p);
   } else if (act == OIDN_ACT_GELU) {
     float e;
     const float p = normal_cdf<DT>(z, e), c = fminf(fmaxf(z, -30.f), 30.f);
-    a = z < -30.f ? 0.f : z * p;
+    a = fmaxf(z, -30.f) * p;
     s = p + c * e * 0.39894228f;
   } else {
     a = z;
@@ -170,61 +169,60 @@ __device__ __forceinline__ long ckpt_size(long rows, long cols) {
   return (codes + codes / (kCkptBlock / 2) + 255) / 256 * 256;
 }
 
-// Scale of a block from its largest magnitude (NaN if any value is not finite).
-__device__ __forceinline__ float ckpt_scale(float top) {
-  if (!(top <= 3.4028234e38f)) return __builtin_nanf("");
-  const float s = bf16_round(top / 127.f);
+// Scale of a block from the bits of its largest magnitude (infinities and NaN
+// are the largest bit patterns).  The division by 127 is a multiplication and
+// one correction step, which rounds it correctly.
+__device__ __forceinline__ float ckpt_scale(unsigned top) {
+  if (top >= 0x7f800000u) return __builtin_nanf("");
+  const float t = __uint_as_float(top), r = 1.f / 127.f, q = t * r;
+  const float s = bf16_round(__builtin_fmaf(__builtin_fmaf(-q, 127.f, t), r, q));
   return s < 7.52316385e-37f ? 0.f : s;
 }
+// Adding 1.5 * 2^23 rounds to a whole number, nearest even, and leaves its two's
+// complement in the low byte.
 __device__ __forceinline__ uint2 ckpt_codes(const Eight& x, float s) {
-  const float inv = s > 0.f ? 1.f / s : 0.f;
-  unsigned w[2] = {0u, 0u};
+  const float inv = s > 0.f ? __builtin_amdgcn_rcpf(s) : 0.f, magic = 12582912.f;
+  unsigned q[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float q = fminf(fmaxf(__builtin_rintf(x.v[k] * inv), -127.f), 127.f);
-    w[k / 4] |= ((unsigned)(int)q & 255u) << (8 * (k % 4));
-  }
-  return make_uint2(w[0], w[1]);
+  for (int k = 0; k < 8; ++k)
+    q[k] = __float_as_uint(__builtin_amdgcn_fmed3f(__builtin_fmaf(x.v[k], inv, magic), magic - 127.f, magic + 127.f));
+  auto four = [&](const unsigned* p) {        // low bytes of four values
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(p[3], p[2], 0x0c0c0400),
+                                 __builtin_amdgcn_perm(p[1], p[0], 0x0c0c0400), 0x05040100);
+  };
+  return make_uint2(four(q), four(q + 4));
 }
-// Largest magnitude of eight values; a NaN or infinity gives infinity.
-__device__ __forceinline__ float top_of(const Eight& x) {
-  float t = 0.f;
+__device__ __forceinline__ unsigned top_of(const Eight& x) {
+  unsigned t = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float a = __builtin_fabsf(x.v[k]);
-    t = a <= t ? t : (a == a ? a : __builtin_inff());
+    const unsigned a = __float_as_uint(x.v[k]) & 0x7fffffffu;
+    t = a > t ? a : t;
   }
   return t;
 }
-// Stores eight columns of a row.  The four lanes that hold a block (lane XOR
-// A, lane XOR B) call it together; columns past `cols` must hold 0.
-template <int A, int B>
+// The largest over the lanes XOR 1 and XOR 2 (in the lane's quad).
+__device__ __forceinline__ unsigned top_of_quad(unsigned t) {
+  unsigned o = __builtin_amdgcn_mov_dpp(t, 0xB1, 0xF, 0xF, false);
+  t = o > t ? o : t;
+  o = __builtin_amdgcn_mov_dpp(t, 0x4E, 0xF, 0xF, false);
+  return o > t ? o : t;
+}
+// Stores eight columns of a row.  The four neighbouring lanes that hold a block
+// call it together; columns past `cols` must hold 0.
 __device__ __forceinline__ void ckpt_store8(const CkptAt& c, long i, int j, const Eight& x,
                                             bool row_ok) {
-  float t = top_of(x);
-  t = fmaxf(t, __shfl_xor(t, A));
-  t = fmaxf(t, __shfl_xor(t, B));
-  const float s = ckpt_scale(t);
+  const float s = ckpt_scale(top_of_quad(top_of(x)));
   if (row_ok && j < c.pitch) {
     *reinterpret_cast<uint2*>(c.codes + i * c.pitch + j) = ckpt_codes(x, s);
     if (j % kCkptBlock == 0) c.scales[(i * c.pitch + j) / kCkptBlock] = (__bf16)s;
   }
 }
-__device__ __forceinline__ Eight ckpt_load8(const CkptAt& c, long i, int j) {
-  Eight r;
-  const uint2 w = *reinterpret_cast<const uint2*>(c.codes + i * c.pitch + j);
-  const float s = (float)c.scales[(i * c.pitch + j) / kCkptBlock];
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    r.v[k] = s * (float)(int)(signed char)((k < 4 ? w.x : w.y) >> (8 * (k % 4)));
-  return r;
-}
-
 // ---------------------------------------------------------------- epilogues
 // Eight columns j .. j + 7 (j a multiple of 8) of row i.  fetch() reads what
 // the epilogue needs from memory, finish() computes and stores; apart, so that
 // several rows' reads are in flight together.  All lanes call finish(): the
-// 8-bit stores exchange maxima between the lanes XOR A and XOR B.
+// 8-bit stores exchange maxima between the four lanes of a block.
 // WHOLE: all eight columns exist, so no element is looked at by itself.
 __device__ __forceinline__ Eight bias8(const float* bias, int j, int n) {
   Eight b{};
@@ -281,22 +279,72 @@ __device__ __forceinline__ void activate_slope8(int act, Eight& z, Eight& g) {
 
 struct Fetched { Eight a, b; };
 
+// What fetch() has read, as it is stored: eight elements, or eight codes and a
+// scale (fewer registers than their values, so more of them can be in flight).
+template <int DT>
+struct Raw {
+  typedef typename Storage<DT>::T T;
+  typedef T T8 __attribute__((ext_vector_type(8)));
+  T8 e;
+  __device__ __forceinline__ Eight value() const {
+    Eight r;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r.v[k] = (float)e[k];
+    return r;
+  }
+};
+struct RawCodes {
+  uint2 q;
+  __bf16 s;
+  __device__ __forceinline__ Eight value() const {
+    Eight r;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      r.v[k] = (float)s * (float)(int)(signed char)((k < 4 ? q.x : q.y) >> (8 * (k % 4)));
+    return r;
+  }
+};
+template <int DT>
+struct RawFetched {
+  union { Raw<DT> a; RawCodes ca; };
+  union { Raw<DT> b; RawCodes cb; };
+};
+
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_raw(const void* p, long i, int n) {
+  typedef typename Storage<DT>::T T;
+  const T* s = static_cast<const T*>(p) + i;
+  Raw<DT> r;
+  if (n >= 8) {
+    __builtin_memcpy(&r.e, s, sizeof(r.e));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r.e[k] = k < n ? s[k] : (T)0.f;
+  }
+  return r;
+}
+__device__ __forceinline__ RawCodes load_codes(const CkptAt& c, long i, int j) {
+  return {*reinterpret_cast<const uint2*>(c.codes + i * c.pitch + j), c.scales[(i * c.pitch + j) / kCkptBlock]};
+}
+
+__device__ __forceinline__ Eight ckpt_load8(const CkptAt& c, long i, int j) { return load_codes(c, i, j).value(); }
+
 template <int DT, int EPI, bool WHOLE>
-__device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, Fetched& f) {
+__device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, RawFetched<DT>& f) {
   const int n = WHOLE ? 8 : e.cols - j;     // columns that exist from j on
   if constexpr (EPI == kEpiPartial || EPI == kEpiGated) return;
   if constexpr (WHOLE) i = i < e.rows ? i : e.rows - 1;
   else if (i >= e.rows || n <= 0) return;
   if constexpr (EPI == kEpiLinear || EPI == kEpiStore) {
-    if (e.res) f.a = load8<DT>(e.res, i * e.ldr + j, n);
+    if (e.res) f.a = load_raw<DT>(e.res, i * e.ldr + j, n);
   }
   if constexpr (EPI == kEpiGatedBack) {
     if (e.z8) {
-      f.a = ckpt_load8(ckpt_at(e.z, e.rows, e.cols), i, j);
-      f.b = ckpt_load8(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols), i, j);
+      f.ca = load_codes(ckpt_at(e.z, e.rows, e.cols), i, j);
+      f.cb = load_codes(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols), i, j);
     } else {
-      f.a = load8<DT>(e.z, i * e.ldz + j, n);
-      f.b = load8<DT>(e.z, i * e.ldz + e.cols + j, n);
+      f.a = load_raw<DT>(e.z, i * e.ldz + j, n);
+      f.b = load_raw<DT>(e.z, i * e.ldz + e.cols + j, n);
     }
   }
 }
@@ -304,29 +352,29 @@ __device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, Fetc
 // x: the sums (kEpiGated: the gate's, u the up projection's); bias: that of
 // the same columns, zeros if there is none.  kEpiGatedBack adds da and db to
 // sums.
-template <int DT, int EPI, int A, int B, bool WHOLE>
+template <int DT, int EPI, bool WHOLE>
 __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i, int j, Eight x, Eight u,
-                                       const Fetched& bias, Fetched& f, Fetched& sums) {
+                                       const Fetched& bias, const RawFetched<DT>& f, Fetched& sums) {
   const int n = WHOLE ? 8 : e.cols - j;
   const bool row_ok = i < e.rows, ok = row_ok && n > 0;
   if constexpr (EPI == kEpiPartial) {       // fp32 sums of one slice
     if (ok)
       store8<OIDN_F32>(e.part, ((long)slice * e.rows + i) * e.cols + j, x, n);
   } else if constexpr (EPI == kEpiStore) {
-    if (e.res) add8(x, f.a);
+    if (e.res) add8(x, f.a.value());
     if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
   } else if constexpr (EPI == kEpiLinear) {
     add8(x, bias.a);
     if (e.z) {
       if (e.z8) {
         if constexpr (!WHOLE) clear_tail(n, x);
-        ckpt_store8<A, B>(ckpt_at(e.z, e.rows, e.cols), i, j, x, row_ok);
+        ckpt_store8(ckpt_at(e.z, e.rows, e.cols), i, j, x, row_ok);
       } else if (ok) {
         store8<DT>(e.z, i * e.ldz + j, x, n);
       }
     }
     activate8<DT>(e.act, x);
-    if (e.res) add8(x, f.a);
+    if (e.res) add8(x, f.a.value());
     if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
   } else if constexpr (EPI == kEpiGated) {
     add8(x, bias.a);
@@ -337,8 +385,8 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
           clear_tail(n, x);
           clear_tail(n, u);
         }
-        ckpt_store8<A, B>(ckpt_at(e.z, e.rows, e.cols), i, j, x, row_ok);
-        ckpt_store8<A, B>(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols),
+        ckpt_store8(ckpt_at(e.z, e.rows, e.cols), i, j, x, row_ok);
+        ckpt_store8(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols),
                           i, j, u, row_ok);
       } else if (ok) {
         store8<DT>(e.z, i * e.ldz + j, x, n);
@@ -350,13 +398,20 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
     for (int k = 0; k < 8; ++k) x.v[k] *= u.v[k];
     if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
   } else {                                  // x is dh: h and [da | db]
-    Eight g, h, da, db;
-    activate_slope8<DT>(e.act, f.a, g);
+    Eight a, b, g, h, da, db;
+    if (e.z8) {
+      a = f.ca.value();
+      b = f.cb.value();
+    } else {
+      a = f.a.value();
+      b = f.b.value();
+    }
+    activate_slope8<DT>(e.act, a, g);
     if (!ok) return;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      h.v[k] = g.v[k] * f.b.v[k];
-      da.v[k] = x.v[k] * f.b.v[k] * f.a.v[k];
+      h.v[k] = g.v[k] * b.v[k];
+      da.v[k] = x.v[k] * b.v[k] * a.v[k];
       db.v[k] = x.v[k] * g.v[k];
       if (k < n) {
         sums.a.v[k] += da.v[k];
@@ -408,38 +463,43 @@ __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const float
     bias.a = bias8(e.bias, j, e.cols - j);
     if constexpr (kGated) bias.b = bias8(e.bias ? e.bias + e.cols : nullptr, j, e.cols - j);
   }
-  auto rows = [&](auto whole, long ir) {
-    constexpr bool kWhole = decltype(whole)::value;
-    // steps whose reads are in flight together
-    constexpr int kTogether = !kWhole ? 1 : kSteps < 4 ? kSteps : 4;
-#pragma unroll 1
-    for (int s = 0; s < kSteps; s += kTogether) {
-      Fetched got[kTogether];
+  // steps whose reads are in flight together; the first ones' are issued before
+  // the accumulators go to LDS
+  constexpr bool kReads = EPI != kEpiPartial && EPI != kEpiGated;
+  constexpr int kTogether = kSteps < 8 ? kSteps : kReads ? 8 : 4;
+  RawFetched<DT> got[kReads ? kTogether : 1];
+  const bool whole = j0 + 8 * kLanes <= e.cols;
+  auto read = [&](long ir, int s) {
+    if constexpr (kReads) {
+      if (whole) {
 #pragma unroll
-      for (int k = 0; k < kTogether; ++k) fetch<DT, EPI, kWhole>(e, ir + (s + k) * kAtOnce, j, got[k]);
-#pragma unroll
-      for (int k = 0; k < kTogether; ++k) {
-        const int row = (s + k) * kAtOnce + lane / kLanes;
-        Eight x, u{};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const floatx4 v = unit(row, 2 * c + h);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) x.v[4 * h + m] = v[m];
-          if constexpr (kGated) {
-            const floatx4 w = unit(row, kUnits / 2 + 2 * c + h);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) u.v[4 * h + m] = w[m];
-          }
-        }
-        finish<DT, EPI, 1, 2, kWhole>(e, slice, ir + (s + k) * kAtOnce, j, x, u, bias, got[k], sums);
+        for (int k = 0; k < kTogether; ++k) fetch<DT, EPI, true>(e, ir + (s + k) * kAtOnce, j, got[k]);
       }
     }
   };
-  const bool whole = j0 + 8 * kLanes <= e.cols;
+  auto step = [&](auto is_whole, long ir, int s, RawFetched<DT>& f) {
+    constexpr bool kWhole = decltype(is_whole)::value;
+    const int row = s * kAtOnce + lane / kLanes;
+    Eight x, u{};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const floatx4 v = unit(row, 2 * c + h);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) x.v[4 * h + m] = v[m];
+      if constexpr (kGated) {
+        const floatx4 w = unit(row, kUnits / 2 + 2 * c + h);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) u.v[4 * h + m] = w[m];
+      }
+    }
+    if constexpr (!kWhole) fetch<DT, EPI, false>(e, ir + s * kAtOnce, j, f);
+    finish<DT, EPI, kWhole>(e, slice, ir + s * kAtOnce, j, x, u, bias, f, sums);
+  };
   constexpr int kRounds = 16 * FR / kRows;
 #pragma unroll 1
   for (int round = 0; round < kRounds; ++round) {
+    const long ir = i0 + round * kRows + lane / kLanes;
+    read(ir, 0);
 #pragma unroll
     for (int k = 0; k < kRounds; ++k)
       if (round == k) {
@@ -451,9 +511,17 @@ __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const float
       }
     // the wave's own writes, back in order
     __builtin_amdgcn_wave_barrier();
-    const long ir = i0 + round * kRows + lane / kLanes;
-    if (whole) rows(std::true_type{}, ir);
-    else rows(std::false_type{}, ir);
+    if (whole) {
+#pragma unroll 1
+      for (int s = 0; s < kSteps; s += kTogether) {
+        if (s) read(ir, s);
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) step(std::true_type{}, ir, s + k, got[kReads ? k : 0]);
+      }
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < kSteps; ++s) step(std::false_type{}, ir, s, got[0]);
+    }
     __builtin_amdgcn_wave_barrier();
   }
   if constexpr (EPI == kEpiGatedBack) {

@@ -131,15 +131,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void dense_few(GemmArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[s].v[e] += part[k][s][i][j8 + e];
   const int j = j0 + j8;
-  Fetched bias{}, f, none;
+  Fetched bias{}, none;
+  RawFetched<DT> f;
   bias.a = bias8(a.e.bias, j, a.e.cols - j);
   if constexpr (EPI == kEpiGated) bias.b = bias8(a.e.bias ? a.e.bias + a.e.cols : nullptr, j, a.e.cols - j);
   if (j0 + kCols <= a.e.cols) {
     fetch<DT, EPI, true>(a.e, i, j, f);
-    finish<DT, EPI, 1, 2, true>(a.e, 0, i, j, v[0], v[1], bias, f, none);
+    finish<DT, EPI, true>(a.e, 0, i, j, v[0], v[1], bias, f, none);
   } else {
     fetch<DT, EPI, false>(a.e, i, j, f);
-    finish<DT, EPI, 1, 2, false>(a.e, 0, i, j, v[0], v[1], bias, f, none);
+    finish<DT, EPI, false>(a.e, 0, i, j, v[0], v[1], bias, f, none);
   }
 }
 

@@ -33,10 +33,11 @@ __device__ __forceinline__ void sum_slices(const EpilogueArgs& e, int splits, in
     if (lane) return;
     for (int s = 1; s < 1 << lg; ++s) add8(x, sums[(s - 1) * at_once + u]);
   }
-  Fetched f, none, bias{};
+  Fetched none, bias{};
+  RawFetched<DT> f;
   if constexpr (EPI == kEpiLinear) bias.a = bias8(e.bias, j, n);
   fetch<DT, EPI, false>(e, i, j, f);
-  finish<DT, EPI, 1, 2, false>(e, 0, i, j, x, x, bias, f, none);
+  finish<DT, EPI, false>(e, 0, i, j, x, x, bias, f, none);
 }
 constexpr int kSumLds = kRowThreads * 32;
 
@@ -154,7 +155,7 @@ __global__ __launch_bounds__(kRowThreads) void ckpt_pack(const void* __restrict_
   Eight v{};
   const int left = n - j < 8 ? (int)(n - j) : 8;
   if (t < total && left > 0) v = load8<DT>(x, i * ldx + j, left);
-  ckpt_store8<1, 2>(ckpt_at(ckpt, m, n), i, (int)j, v, t < total);
+  ckpt_store8(ckpt_at(ckpt, m, n), i, (int)j, v, t < total);
 }
 
 template <int DT>
