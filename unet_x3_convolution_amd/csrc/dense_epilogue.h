@@ -304,11 +304,9 @@ struct RawCodes {
     return r;
   }
 };
-template <int DT>
-struct RawFetched {
-  union { Raw<DT> a; RawCodes ca; };
-  union { Raw<DT> b; RawCodes cb; };
-};
+// Z8: the saved z of kEpiGatedBack is held in 8 bits.
+template <int DT, bool Z8> struct RawFetched { Raw<DT> a, b; };
+template <int DT> struct RawFetched<DT, true> { RawCodes a, b; };
 
 template <int DT>
 __device__ __forceinline__ Raw<DT> load_raw(const void* p, long i, int n) {
@@ -329,8 +327,8 @@ __device__ __forceinline__ RawCodes load_codes(const CkptAt& c, long i, int j) {
 
 __device__ __forceinline__ Eight ckpt_load8(const CkptAt& c, long i, int j) { return load_codes(c, i, j).value(); }
 
-template <int DT, int EPI, bool WHOLE>
-__device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, RawFetched<DT>& f) {
+template <int DT, int EPI, bool WHOLE, bool Z8>
+__device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, RawFetched<DT, Z8>& f) {
   const int n = WHOLE ? 8 : e.cols - j;     // columns that exist from j on
   if constexpr (EPI == kEpiPartial || EPI == kEpiGated) return;
   if constexpr (WHOLE) i = i < e.rows ? i : e.rows - 1;
@@ -339,9 +337,9 @@ __device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, RawF
     if (e.res) f.a = load_raw<DT>(e.res, i * e.ldr + j, n);
   }
   if constexpr (EPI == kEpiGatedBack) {
-    if (e.z8) {
-      f.ca = load_codes(ckpt_at(e.z, e.rows, e.cols), i, j);
-      f.cb = load_codes(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols), i, j);
+    if constexpr (Z8) {
+      f.a = load_codes(ckpt_at(e.z, e.rows, e.cols), i, j);
+      f.b = load_codes(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols), i, j);
     } else {
       f.a = load_raw<DT>(e.z, i * e.ldz + j, n);
       f.b = load_raw<DT>(e.z, i * e.ldz + e.cols + j, n);
@@ -352,9 +350,9 @@ __device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, RawF
 // x: the sums (kEpiGated: the gate's, u the up projection's); bias: that of
 // the same columns, zeros if there is none.  kEpiGatedBack adds da and db to
 // sums.
-template <int DT, int EPI, bool WHOLE>
+template <int DT, int EPI, bool WHOLE, bool Z8>
 __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i, int j, Eight x, Eight u,
-                                       const Fetched& bias, const RawFetched<DT>& f, Fetched& sums) {
+                                       const Fetched& bias, const RawFetched<DT, Z8>& f, Fetched& sums) {
   const int n = WHOLE ? 8 : e.cols - j;
   const bool row_ok = i < e.rows, ok = row_ok && n > 0;
   if constexpr (EPI == kEpiPartial) {       // fp32 sums of one slice
@@ -398,14 +396,8 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
     for (int k = 0; k < 8; ++k) x.v[k] *= u.v[k];
     if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
   } else {                                  // x is dh: h and [da | db]
-    Eight a, b, g, h, da, db;
-    if (e.z8) {
-      a = f.ca.value();
-      b = f.cb.value();
-    } else {
-      a = f.a.value();
-      b = f.b.value();
-    }
+    Eight a = f.a.value(), g, h, da, db;
+    const Eight b = f.b.value();
     activate_slope8<DT>(e.act, a, g);
     if (!ok) return;
 #pragma unroll
@@ -440,11 +432,14 @@ constexpr int epilogue_rows() { return FR * FC > 32 ? 8 * FR : 16 * FR; }
 template <int FR, int FC>
 constexpr int epilogue_bytes() { return epilogue_rows<FR, FC>() * 64 * FC; }
 
-template <int DT, int EPI, int FR, int FC>
+template <int DT, int EPI, int FR, int FC, bool Z8 = false>
 __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const floatx4 (&acc)[FC][FR], char* lds,
                                               long i0, int j0, int slice, long group) {
   if constexpr (EPI == kEpiLinear || EPI == kEpiStore) {
     if (slice >= 0) return tile_epilogue<DT, kEpiPartial, FR, FC>(e, acc, lds, i0, j0, slice, group);
+  }
+  if constexpr (EPI == kEpiGatedBack && !Z8) {
+    if (e.z8) return tile_epilogue<DT, EPI, FR, FC, true>(e, acc, lds, i0, j0, slice, group);
   }
   constexpr int kRows = epilogue_rows<FR, FC>();       // rows per round
   constexpr int kUnits = 4 * FC;                       // 16-byte units of a row
@@ -467,17 +462,20 @@ __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const float
   // the accumulators go to LDS
   constexpr bool kReads = EPI != kEpiPartial && EPI != kEpiGated;
   constexpr int kTogether = kSteps < 8 ? kSteps : kReads ? 8 : 4;
-  RawFetched<DT> got[kReads ? kTogether : 1];
+  RawFetched<DT, Z8> got[kReads ? kTogether : 1];
   const bool whole = j0 + 8 * kLanes <= e.cols;
   auto read = [&](long ir, int s) {
     if constexpr (kReads) {
-      if (whole) {
+      if (whole || j + 8 <= e.cols) {
 #pragma unroll
-        for (int k = 0; k < kTogether; ++k) fetch<DT, EPI, true>(e, ir + (s + k) * kAtOnce, j, got[k]);
+        for (int k = 0; k < kTogether; ++k) fetch<DT, EPI, true, Z8>(e, ir + (s + k) * kAtOnce, j, got[k]);
+      } else if (j < e.cols) {
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) fetch<DT, EPI, false, Z8>(e, ir + (s + k) * kAtOnce, j, got[k]);
       }
     }
   };
-  auto step = [&](auto is_whole, long ir, int s, RawFetched<DT>& f) {
+  auto step = [&](auto is_whole, long ir, int s, RawFetched<DT, Z8>& f) {
     constexpr bool kWhole = decltype(is_whole)::value;
     const int row = s * kAtOnce + lane / kLanes;
     Eight x, u{};
@@ -492,8 +490,7 @@ __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const float
         for (int m = 0; m < 4; ++m) u.v[4 * h + m] = w[m];
       }
     }
-    if constexpr (!kWhole) fetch<DT, EPI, false>(e, ir + s * kAtOnce, j, f);
-    finish<DT, EPI, kWhole>(e, slice, ir + s * kAtOnce, j, x, u, bias, f, sums);
+    finish<DT, EPI, kWhole, Z8>(e, slice, ir + s * kAtOnce, j, x, u, bias, f, sums);
   };
   constexpr int kRounds = 16 * FR / kRows;
 #pragma unroll 1
@@ -511,16 +508,16 @@ __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const float
       }
     // the wave's own writes, back in order
     __builtin_amdgcn_wave_barrier();
-    if (whole) {
 #pragma unroll 1
-      for (int s = 0; s < kSteps; s += kTogether) {
-        if (s) read(ir, s);
+    for (int s = 0; s < kSteps; s += kTogether) {
+      if (s) read(ir, s);
+      if (whole) {
 #pragma unroll
         for (int k = 0; k < kTogether; ++k) step(std::true_type{}, ir, s + k, got[kReads ? k : 0]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k) step(std::false_type{}, ir, s + k, got[kReads ? k : 0]);
       }
-    } else {
-#pragma unroll 1
-      for (int s = 0; s < kSteps; ++s) step(std::false_type{}, ir, s, got[0]);
     }
     __builtin_amdgcn_wave_barrier();
   }

@@ -23,16 +23,6 @@ constexpr int kFewWaves = 8;
 constexpr int kDepth = 4;
 
 template <int DT>
-__device__ __forceinline__ uint4 part16(const char* p, int n) {
-  if constexpr (DT == OIDN_F32) {
-    const unsigned* s = reinterpret_cast<const unsigned*>(p);
-    return make_uint4(s[0], n > 1 ? s[1] : 0u, n > 2 ? s[2] : 0u, 0u);
-  } else {
-    return load16_part(p, n);
-  }
-}
-
-template <int DT>
 __device__ __forceinline__ floatx4 multiply16(uint4 a, uint4 b, floatx4 c) {
   if constexpr (DT == OIDN_F32) {
     const floatx4 av = __builtin_bit_cast(floatx4, a), bv = __builtin_bit_cast(floatx4, b);
@@ -75,24 +65,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void dense_few(GemmArgs a) {
 #pragma unroll
     for (int m = 0; m < MF; ++m) acc[f][m] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  auto load = [&](const char* row, long l) {
-    if (l + kPer <= len) return load16_any(row + kSize * l);
-    if (l < len) return part16<DT>(row + kSize * l, (int)(len - l));
-    return make_uint4(0u, 0u, 0u, 0u);
-  };
-  auto load_whole = [&](const char* row, long l) { return load16_any(row + kSize * l); };
-  auto chunks = [&](long c, auto depth, auto ld) {      // `depth` chunks of this wave from chunk c on
+  const Extent<kSize> all_w(a.p, (long)a.e.cols * kSets, a.ldp, len), all_x(a.q, a.e.rows, a.ldq, len);
+  // `depth` chunks of this wave from chunk c on; the last one of all may end early
+  auto chunks = [&](long c, auto depth, auto is_whole) {
     constexpr int D = decltype(depth)::value;
+    constexpr bool kWhole = decltype(is_whole)::value;
     uint4 w[D][2][WF], x[D][2][MF];
 #pragma unroll
     for (int d = 0; d < D; ++d)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const long l = (c + d * kFewWaves) * kChunk + 2 * kPer * g + kPer * s;
+        if constexpr (kWhole) {
 #pragma unroll
-        for (int f = 0; f < WF; ++f) w[d][s][f] = ld(wp[f], l);
+          for (int f = 0; f < WF; ++f) w[d][s][f] = load16_any(wp[f] + kSize * l);
 #pragma unroll
-        for (int m = 0; m < MF; ++m) x[d][s][m] = ld(xp[m], l);
+          for (int m = 0; m < MF; ++m) x[d][s][m] = load16_any(xp[m] + kSize * l);
+        } else {
+          all_w.load(w[d][s], [&](int f, const char*& p, long& n) { p = wp[f] + kSize * l, n = len - l; });
+          all_x.load(x[d][s], [&](int m, const char*& p, long& n) { p = xp[m] + kSize * l, n = len - l; });
+        }
       }
 #pragma unroll
     for (int d = 0; d < D; ++d)
@@ -106,9 +98,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void dense_few(GemmArgs a) {
   const long whole = len / kChunk;
   long c = wave;
   for (; c + (kDepth - 1) * kFewWaves < whole; c += kDepth * kFewWaves)
-    chunks(c, std::integral_constant<int, kDepth>{}, load_whole);
-  for (; c < whole; c += kFewWaves) chunks(c, std::integral_constant<int, 1>{}, load_whole);
-  if (c == whole && len % kChunk) chunks(c, std::integral_constant<int, 1>{}, load);
+    chunks(c, std::integral_constant<int, kDepth>{}, std::true_type{});
+  for (; c < whole; c += kFewWaves) chunks(c, std::integral_constant<int, 1>{}, std::true_type{});
+  if (c == whole && len % kChunk) chunks(c, std::integral_constant<int, 1>{}, std::false_type{});
 
   // [wave][set][row][column]; a row's pitch is padded by 16 bytes
   constexpr int kCols = 16 * NF, kPitch = kCols + 4;
@@ -132,15 +124,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void dense_few(GemmArgs a) {
       for (int e = 0; e < 8; ++e) v[s].v[e] += part[k][s][i][j8 + e];
   const int j = j0 + j8;
   Fetched bias{}, none;
-  RawFetched<DT> f;
+  RawFetched<DT, false> f;
   bias.a = bias8(a.e.bias, j, a.e.cols - j);
   if constexpr (EPI == kEpiGated) bias.b = bias8(a.e.bias ? a.e.bias + a.e.cols : nullptr, j, a.e.cols - j);
   if (j0 + kCols <= a.e.cols) {
-    fetch<DT, EPI, true>(a.e, i, j, f);
-    finish<DT, EPI, true>(a.e, 0, i, j, v[0], v[1], bias, f, none);
+    fetch<DT, EPI, true, false>(a.e, i, j, f);
+    finish<DT, EPI, true, false>(a.e, 0, i, j, v[0], v[1], bias, f, none);
   } else {
-    fetch<DT, EPI, false>(a.e, i, j, f);
-    finish<DT, EPI, false>(a.e, 0, i, j, v[0], v[1], bias, f, none);
+    fetch<DT, EPI, false, false>(a.e, i, j, f);
+    finish<DT, EPI, false, false>(a.e, 0, i, j, v[0], v[1], bias, f, none);
   }
 }
 

@@ -8,8 +8,8 @@
 // so that lane group g of a pair owns the 8 columns 32 p + 8 g .. + 7.
 //
 // kDenseK = 64 summed elements are staged at a time, through registers into
-// one of two LDS buffers: the loads of the next tile are in flight while the
-// current one is multiplied.  An l-fastest operand keeps rows of 64 elements
+// one of two LDS buffers: the loads of the next two or three tiles are in
+// flight while the current one is multiplied.  An l-fastest operand keeps rows of 64 elements
 // (128 B); its 16-byte slot s of row r sits at s ^ (r / 2 % 8), which spreads
 // the 16 rows that a fragment read touches over all banks.  A strided operand
 // keeps rows of T elements, one per l, and is read with the transposing
@@ -34,14 +34,159 @@ __device__ __forceinline__ uint4 load16_any(const char* p) {
   __builtin_memcpy(&u, p, 16);     // one 16-byte load: unaligned access is enabled on this target
   return u;
 }
-// The first n (1 .. 7) 16-bit elements at p, zeros after.
-__device__ __forceinline__ uint4 load16_part(const char* p, int n) {
-  unsigned w[4] = {0u, 0u, 0u, 0u};
+// A matrix's memory, for 16-byte loads near its end: a load that would pass the
+// end is moved back inside and what it read is shifted, without a branch, so
+// that all loads of a tile are in flight together.  A matrix of fewer than 16
+// bytes is read once, element by element, into `all`.
+template <int SIZE>
+struct Extent {
+  static constexpr int kPer = 16 / SIZE;
+  const char* first;
+  const char* last;        // where the last 16 bytes begin; before `first` if there are fewer
+  uint4 all;
+  __device__ __forceinline__ Extent(const void* base, long rows, long ld, long cols)
+      : first(static_cast<const char*>(base)), last(first + ((rows - 1) * ld + cols) * SIZE - 16),
+        all(make_uint4(0u, 0u, 0u, 0u)) {
+    if (last >= first) return;
+    const long n = (rows - 1) * ld + cols;
+    unsigned w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int k = 0; k < 7; ++k)
-    if (k < n) w[k / 2] |= (unsigned)reinterpret_cast<const unsigned short*>(p)[k] << (16 * (k % 2));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+    for (int k = 0; k < kPer - 1; ++k)
+      if (k < n) {
+        if constexpr (SIZE == 4) w[k] = reinterpret_cast<const unsigned*>(first)[k];
+        else w[k / 2] |= (unsigned)reinterpret_cast<const unsigned short*>(first)[k] << (16 * (k % 2));
+      }
+    all = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // Where to load for the unit at p of which n elements exist (n <= 0: none).
+  __device__ __forceinline__ const char* from(const char* p, long n) const {
+    const char* f = n > 0 ? p : first;
+    f = f < last ? f : last;
+    return f > first ? f : first;
+  }
+  // The unit's n elements, zeros after, from what was loaded at from(p, n).
+  __device__ __forceinline__ uint4 shifted(uint4 u, const char* p, long n) const {
+    const bool in = n > 0;
+    const unsigned back = in ? (unsigned)(p - from(p, n)) * 8 : 0;    // bits, < 128
+    const unsigned keep = n >= kPer ? 128u : in ? (unsigned)n * SIZE * 8 : 0u;
+    unsigned long long lo = u.x | (unsigned long long)u.y << 32, hi = u.z | (unsigned long long)u.w << 32;
+    if (back >= 64) lo = hi, hi = 0;
+    const unsigned sh = back & 63;
+    lo = lo >> sh | (sh ? hi << (64 - sh) : 0);
+    hi >>= sh;
+    lo = keep >= 64 ? lo : lo & ((1ull << keep) - 1);
+    hi = keep >= 128 ? hi : keep > 64 ? hi & ((1ull << (keep - 64)) - 1) : 0;
+    return make_uint4((unsigned)lo, (unsigned)(lo >> 32), (unsigned)hi, (unsigned)(hi >> 32));
+  }
+  // N units; at(k, p, n) gives the address of unit k and its elements.
+  template <int N, class At>
+  __device__ __forceinline__ void load(uint4 (&u)[N], At at) const {
+    const char* p[N];
+    long n[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) at(k, p[k], n[k]);
+    uint4 raw[N];
+    if (last < first) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) raw[k] = all;
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) raw[k] = load16_any(from(p[k], n[k]));
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) u[k] = shifted(raw[k], p[k], n[k]);
+  }
+};
+
+// The loads of one operand's tiles through registers, in units of 16 bytes;
+// SIZE: bytes of an element, T: output rows of a tile, D: its summed length.
+// Unit k of a thread is unit `threadIdx.x + 256 k` of the tile: rows of D
+// elements (l-fastest) or of T (STRIDED).
+template <int SIZE, int T, int D, bool STRIDED>
+struct Loader {
+  static constexpr int kPer = 16 / SIZE;
+  static constexpr int kUnits = T * D / kPer / 256;
+  static constexpr int kPerRow = (STRIDED ? T : D) / kPer;
+  const Extent<SIZE> all;
+  const char* p[kUnits];     // of the next tile
+  uint4 mask[STRIDED ? kUnits : 1];
+  long step;                 // bytes to the next tile
+  long i0, rows, ld, len, half;
+  bool columns;              // STRIDED: every column of the tile exists
+
+  // Row and unit in the row of unit k.  A strided fp32 tile deals its units so
+  // that a wave's LDS writes, which transpose, spread over the banks.
+  static __device__ __forceinline__ void place(int k, int& r, int& s) {
+    if constexpr (STRIDED && SIZE == 4) {
+      r = threadIdx.x >> 3;
+      s = (threadIdx.x & 7) + 8 * k;
+    } else {
+      const int t = threadIdx.x + k * 256;
+      r = t / kPerRow;
+      s = t % kPerRow;
+    }
+  }
+  // Tiles start at output row i0_ (of rows_) and summed element l0 (of len_).
+  // half_: tile rows from T / 2 on come from `half` further matrix rows
+  // (l-fastest only; the up projection's rows of a gated product).
+  __device__ __forceinline__ Loader(const void* base, long ld_, long i0_, long rows_, long l0, long len_, long half_)
+      : all(base, STRIDED ? len_ : rows_ + half_, ld_, STRIDED ? rows_ : len_), step((STRIDED ? D * ld_ : D) * SIZE),
+        i0(i0_), rows(rows_), ld(ld_), len(len_), half(half_), columns(i0_ + T <= rows_) {
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      long n;
+      at(k, l0, p[k], n);
+      if constexpr (STRIDED) {
+        int r, s;
+        place(k, r, s);
+        n = rows - (i0 + kPer * s);
+        // a unit past the columns reads its row's first ones, and keeps none
+        if (n <= 0) p[k] = all.first + (l0 + r) * ld * SIZE;
+        auto word = [&](int m) {         // bits of 32-bit word m whose elements exist
+          const long left = n * SIZE - 4 * m;
+          return left >= 4 ? ~0u : left == 2 ? 0xffffu : 0u;
+        };
+        mask[k] = make_uint4(word(0), word(1), word(2), word(3));
+      }
+    }
+  }
+  __device__ __forceinline__ void at(int k, long l0, const char*& q, long& n) const {
+    int r, s;
+    place(k, r, s);
+    if constexpr (!STRIDED) {
+      long i = i0 + (half ? r & (T / 2 - 1) : r);
+      i = (i < rows ? i : rows - 1) + (half && r >= T / 2 ? half : 0);
+      const long l = l0 + kPer * s;
+      q = all.first + SIZE * (i * ld + l);
+      n = len - l;
+    } else {
+      const long l = l0 + r, i = i0 + kPer * s;
+      q = all.first + SIZE * (l * ld + i);
+      n = l < len ? rows - i : 0;
+    }
+  }
+  // The next tile, which starts at l0.
+  __device__ __forceinline__ void load(uint4 (&u)[kUnits], long l0) {
+    // a strided row that is read past its columns goes on in the next row: all
+    // but the last row may
+    const bool inside = STRIDED ? l0 + D + (columns ? 0 : 1) <= len : l0 + D <= len;
+    if (inside) {
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) u[k] = load16_any(p[k]);
+      if (STRIDED && !columns) {
+#pragma unroll
+        for (int k = 0; k < kUnits; ++k) {
+          const uint4 m = mask[STRIDED ? k : 0];
+          u[k] = make_uint4(u[k].x & m.x, u[k].y & m.y, u[k].z & m.z, u[k].w & m.w);
+        }
+      }
+    } else {
+      all.load(u, [&](int k, const char*& q, long& n) { at(k, l0, q, n); });
+    }
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) p[k] += step;
+  }
+};
 
 // One operand's tile in LDS: T rows of the output side x 64 of l.
 template <int T, bool STRIDED, int THREADS_>
@@ -55,36 +200,6 @@ struct Stage16 {
     else return row * (T / 8) + (s ^ ((row & 2) << 1));
   }
 
-  // Tile starting at output row i0 (of `rows`) and l0 (of `len`).  `half`:
-  // tile rows from T / 2 on come from `half` further matrix rows (l-fastest
-  // only; the up projection's rows of a gated product).
-  static __device__ __forceinline__ void load(uint4 (&u)[kUnits], const void* base, long ld, long i0,
-                                              long rows, long l0, long len, long half) {
-    const char* b = static_cast<const char*>(base);
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const int t = threadIdx.x + k * THREADS_;
-      if constexpr (!STRIDED) {
-        const int r = t >> 3;
-        long i = i0 + (half ? r & (T / 2 - 1) : r);
-        i = (i < rows ? i : rows - 1) + (half && r >= T / 2 ? half : 0);
-        const long l = l0 + 8 * (t & 7);
-        const char* p = b + 2 * (i * ld + l);
-        u[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (l + 8 <= len) u[k] = load16_any(p);
-        else if (l < len) u[k] = load16_part(p, (int)(len - l));
-      } else {
-        const int r = t / (T / 8);
-        const long l = l0 + r, i = i0 + 8 * (t % (T / 8));
-        const char* p = b + 2 * (l * ld + i);
-        u[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (l < len) {
-          if (i + 8 <= rows) u[k] = load16_any(p);
-          else if (i < rows) u[k] = load16_part(p, (int)(rows - i));
-        }
-      }
-    }
-  }
   static __device__ __forceinline__ void store(const uint4 (&u)[kUnits], char* lds) {
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
@@ -151,42 +266,52 @@ __device__ __forceinline__ void gemm16_staged(const GemmArgs& a, int block, char
 #pragma unroll
     for (int r = 0; r < FR; ++r) acc[c][r] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  uint4 up[P::kUnits], uq[Q::kUnits];
-  P::load(up, a.p, a.ldp, j0, a.e.cols, t0 * kDenseK, a.len, half);
-  Q::load(uq, a.q, a.ldq, i0, a.e.rows, t0 * kDenseK, a.len, 0);
-  for (long t = t0; t < t1; ++t) {
-    char* const lp = lds + ((t - t0) & 1) * (P::kBytes + Q::kBytes);
-    char* const lq = lp + P::kBytes;
-    // this buffer was last read two tiles ago, before the previous barrier
-    P::store(up, lp);
-    Q::store(uq, lq);
-    __syncthreads();
-    if (t + 1 < t1) {
-      P::load(up, a.p, a.ldp, j0, a.e.cols, (t + 1) * kDenseK, a.len, half);
-      Q::load(uq, a.q, a.ldq, i0, a.e.rows, (t + 1) * kDenseK, a.len, 0);
-    }
+  // Tiles in flight in registers; tile t waits in set (t - t0) % kAhead.
+  constexpr int kAhead = TR * TC > 64 * 128 ? 2 : 3;
+  Loader<2, TC, kDenseK, PS> from_p(a.p, a.ldp, j0, a.e.cols, t0 * kDenseK, a.len, half);
+  Loader<2, TR, kDenseK, QS> from_q(a.q, a.ldq, i0, a.e.rows, t0 * kDenseK, a.len, 0);
+  uint4 up[kAhead][P::kUnits], uq[kAhead][Q::kUnits];
+  auto load = [&](long t, int set) {
+    from_p.load(up[set], t * kDenseK);
+    from_q.load(uq[set], t * kDenseK);
+  };
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      uint4 fp[FC], fq[FR];
+  for (int s = 0; s < kAhead; ++s)
+    if (t0 + s < t1) load(t0 + s, s);
+  for (long tt = t0; tt < t1; tt += kAhead) {
 #pragma unroll
-      for (int c = 0; c < FC; ++c) {
-        // pair c / 2 of the wave: a gated wave's second half is the up side
-        const int pair = c / 2;
-        const int base = EPI == kEpiGated
-                             ? (pair < FC / 4 ? wc * (TC / 4) + 32 * pair
-                                              : TC / 2 + wc * (TC / 4) + 32 * (pair - FC / 4))
-                             : wc * (TC / 2) + 32 * pair;
-        fp[c] = P::template fragment<true>(lp, base, c & 1, kk);
+    for (int s = 0; s < kAhead; ++s) {
+      const long t = tt + s;
+      if (t >= t1) break;
+      char* const lp = lds + ((t - t0) & 1) * (P::kBytes + Q::kBytes);
+      char* const lq = lp + P::kBytes;
+      // this buffer was last read two tiles ago, before the previous barrier
+      P::store(up[s], lp);
+      Q::store(uq[s], lq);
+      __syncthreads();
+      if (t + kAhead < t1) load(t + kAhead, s);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        uint4 fp[FC], fq[FR];
+#pragma unroll
+        for (int c = 0; c < FC; ++c) {
+          // pair c / 2 of the wave: a gated wave's second half is the up side
+          const int pair = c / 2;
+          const int base = EPI == kEpiGated
+                               ? (pair < FC / 4 ? wc * (TC / 4) + 32 * pair
+                                                : TC / 2 + wc * (TC / 4) + 32 * (pair - FC / 4))
+                               : wc * (TC / 2) + 32 * pair;
+          fp[c] = P::template fragment<true>(lp, base, c & 1, kk);
+        }
+#pragma unroll
+        for (int r = 0; r < FR; ++r) fq[r] = Q::template fragment<false>(lq, wr * (TR / 2), r, kk);
+#pragma unroll
+        for (int c = 0; c < FC; ++c)
+#pragma unroll
+          for (int r = 0; r < FR; ++r) acc[c][r] = mfma16<BF>(fp[c], fq[r], acc[c][r]);
       }
-#pragma unroll
-      for (int r = 0; r < FR; ++r) fq[r] = Q::template fragment<false>(lq, wr * (TR / 2), r, kk);
-#pragma unroll
-      for (int c = 0; c < FC; ++c)
-#pragma unroll
-        for (int r = 0; r < FR; ++r) acc[c][r] = mfma16<BF>(fp[c], fq[r], acc[c][r]);
     }
   }
-
   __syncthreads();                       // every wave has read its last fragments
   tile_epilogue<DT, EPI, FR, FC>(a.e, acc, lds + wave * epilogue_bytes<FR, FC>(), i0 + wr * (TR / 2),
                                  (int)j0 + wc * (C / 2), a.splits > 1 ? slice : -1, (long)tr * 2 + wr);

@@ -8,7 +8,7 @@
 // in both operands, so the order of the sum is permuted within 16 elements
 // and nothing is shuffled.  Strided operands are transposed by the LDS write:
 // eight neighbouring lanes read 128 contiguous bytes.
-#include "dense_epilogue.h"
+#include "dense_gemm16.h"
 
 namespace oidn {
 namespace {
@@ -20,47 +20,18 @@ struct Stage32 {
   static constexpr int kUnits = T * kDenseKF32 / 4 / 256;
   static constexpr int kFloats = T * kPad32;
 
-  static __device__ __forceinline__ float4 load4(const float* p, long n) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (n >= 4) {
-      __builtin_memcpy(&v, p, 16);
-    } else {
-      if (n > 0) v.x = p[0];
-      if (n > 1) v.y = p[1];
-      if (n > 2) v.z = p[2];
-    }
-    return v;
-  }
-
-  static __device__ __forceinline__ void load(float4 (&u)[kUnits], const void* base, long ld, long i0,
-                                              long rows, long l0, long len, long half) {
-    const float* b = static_cast<const float*>(base);
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      if constexpr (!STRIDED) {
-        const int t = threadIdx.x + k * 256, r = t >> 3;
-        long i = i0 + (half ? r & (T / 2 - 1) : r);
-        i = (i < rows ? i : rows - 1) + (half && r >= T / 2 ? half : 0);
-        const long l = l0 + 4 * (t & 7);
-        u[k] = load4(b + i * ld + l, len - l);
-      } else {
-        const long l = l0 + (threadIdx.x >> 3), i = i0 + 32 * k + 4 * (threadIdx.x & 7);
-        u[k] = load4(b + l * ld + i, l < len ? rows - i : 0);
-      }
-    }
-  }
-  static __device__ __forceinline__ void store(const float4 (&u)[kUnits], float* lds) {
+  static __device__ __forceinline__ void store(const uint4 (&u)[kUnits], float* lds) {
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
       if constexpr (!STRIDED) {
         const int t = threadIdx.x + k * 256;
-        *reinterpret_cast<float4*>(lds + (t >> 3) * kPad32 + 4 * (t & 7)) = u[k];
+        *reinterpret_cast<uint4*>(lds + (t >> 3) * kPad32 + 4 * (t & 7)) = u[k];
       } else {
         float* p = lds + (32 * k + 4 * (threadIdx.x & 7)) * kPad32 + (threadIdx.x >> 3);
-        p[0] = u[k].x;
-        p[kPad32] = u[k].y;
-        p[2 * kPad32] = u[k].z;
-        p[3 * kPad32] = u[k].w;
+        p[0] = __uint_as_float(u[k].x);
+        p[kPad32] = __uint_as_float(u[k].y);
+        p[2 * kPad32] = __uint_as_float(u[k].z);
+        p[3 * kPad32] = __uint_as_float(u[k].w);
       }
     }
   }
@@ -102,43 +73,53 @@ __device__ __forceinline__ void gemm32(const GemmArgs& a, int block, float* lds)
 #pragma unroll
     for (int r = 0; r < FR; ++r) acc[c][r] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  float4 up[P::kUnits], uq[Q::kUnits];
-  P::load(up, a.p, a.ldp, j0, a.e.cols, t0 * kDenseKF32, a.len, half);
-  Q::load(uq, a.q, a.ldq, i0, a.e.rows, t0 * kDenseKF32, a.len, 0);
-  for (long t = t0; t < t1; ++t) {
-    float* const lp = lds + ((t - t0) & 1) * (P::kFloats + Q::kFloats);
-    float* const lq = lp + P::kFloats;
-    P::store(up, lp);
-    Q::store(uq, lq);
-    __syncthreads();
-    if (t + 1 < t1) {
-      P::load(up, a.p, a.ldp, j0, a.e.cols, (t + 1) * kDenseKF32, a.len, half);
-      Q::load(uq, a.q, a.ldq, i0, a.e.rows, (t + 1) * kDenseKF32, a.len, 0);
-    }
+  // Tiles in flight in registers; tile t waits in set (t - t0) % kAhead.
+  constexpr int kAhead = 2;
+  Loader<4, TC, kDenseKF32, PS> from_p(a.p, a.ldp, j0, a.e.cols, t0 * kDenseKF32, a.len, half);
+  Loader<4, TR, kDenseKF32, QS> from_q(a.q, a.ldq, i0, a.e.rows, t0 * kDenseKF32, a.len, 0);
+  uint4 up[kAhead][P::kUnits], uq[kAhead][Q::kUnits];
+  auto load = [&](long t, int set) {
+    from_p.load(up[set], t * kDenseKF32);
+    from_q.load(uq[set], t * kDenseKF32);
+  };
 #pragma unroll
-    for (int kk = 0; kk < kDenseKF32 / 16; ++kk) {
-      floatx4 fp[FC], fq[FR];
+  for (int s = 0; s < kAhead; ++s)
+    if (t0 + s < t1) load(t0 + s, s);
+  for (long tt = t0; tt < t1; tt += kAhead) {
 #pragma unroll
-      for (int c = 0; c < FC; ++c) {
-        const int pair = c / 2;
-        const int base = EPI == kEpiGated
-                             ? (pair < FC / 4 ? wc * (TC / 4) + 32 * pair
-                                              : TC / 2 + wc * (TC / 4) + 32 * (pair - FC / 4))
-                             : wc * (TC / 2) + 32 * pair;
-        fp[c] = P::template fragment<true>(lp, base, c & 1, kk);
+    for (int s = 0; s < kAhead; ++s) {
+      const long t = tt + s;
+      if (t >= t1) break;
+      float* const lp = lds + ((t - t0) & 1) * (P::kFloats + Q::kFloats);
+      float* const lq = lp + P::kFloats;
+      P::store(up[s], lp);
+      Q::store(uq[s], lq);
+      __syncthreads();
+      if (t + kAhead < t1) load(t + kAhead, s);
+#pragma unroll
+      for (int kk = 0; kk < kDenseKF32 / 16; ++kk) {
+        floatx4 fp[FC], fq[FR];
+#pragma unroll
+        for (int c = 0; c < FC; ++c) {
+          const int pair = c / 2;
+          const int base = EPI == kEpiGated
+                               ? (pair < FC / 4 ? wc * (TC / 4) + 32 * pair
+                                                : TC / 2 + wc * (TC / 4) + 32 * (pair - FC / 4))
+                               : wc * (TC / 2) + 32 * pair;
+          fp[c] = P::template fragment<true>(lp, base, c & 1, kk);
+        }
+#pragma unroll
+        for (int r = 0; r < FR; ++r) fq[r] = Q::template fragment<false>(lq, wr * (TR / 2), r, kk);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < FC; ++c)
+#pragma unroll
+            for (int r = 0; r < FR; ++r)
+              acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(fp[c][e], fq[r][e], acc[c][r], 0, 0, 0);
       }
-#pragma unroll
-      for (int r = 0; r < FR; ++r) fq[r] = Q::template fragment<false>(lq, wr * (TR / 2), r, kk);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int c = 0; c < FC; ++c)
-#pragma unroll
-          for (int r = 0; r < FR; ++r)
-            acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(fp[c][e], fq[r][e], acc[c][r], 0, 0, 0);
     }
   }
-
   __syncthreads();                       // every wave has read its last fragments
   tile_epilogue<DT, EPI, FR, FC>(a.e, acc, reinterpret_cast<char*>(lds) + wave * epilogue_bytes<FR, FC>(),
                                  i0 + wr * (TR / 2), (int)j0 + wc * (C / 2), a.splits > 1 ? slice : -1,

@@ -34,10 +34,10 @@ __device__ __forceinline__ void sum_slices(const EpilogueArgs& e, int splits, in
     for (int s = 1; s < 1 << lg; ++s) add8(x, sums[(s - 1) * at_once + u]);
   }
   Fetched none, bias{};
-  RawFetched<DT> f;
+  RawFetched<DT, false> f;
   if constexpr (EPI == kEpiLinear) bias.a = bias8(e.bias, j, n);
-  fetch<DT, EPI, false>(e, i, j, f);
-  finish<DT, EPI, false>(e, 0, i, j, x, x, bias, f, none);
+  fetch<DT, EPI, false, false>(e, i, j, f);
+  finish<DT, EPI, false, false>(e, 0, i, j, x, x, bias, f, none);
 }
 constexpr int kSumLds = kRowThreads * 32;
 
