@@ -180,11 +180,10 @@ def _check(rc: int):
 
 def _p(t):
     """Device address of a tensor (or int / None)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:
         return t
-    return t.data_ptr()
 
 
 def _s(stream):

@@ -94,6 +94,23 @@ inline long gemm_blocks(const GemmArgs& a) {
   return ((long)a.tiles_r * a.tiles_c + 7) / 8 * 8 * a.splits;
 }
 
+// dz = dy * act'(z) (dz may be null: column sums alone; act none: z unused)
+// and, with part, partial column sums of dz over `chunk` rows: part[r / chunk][n].
+struct SlopeArgs {
+  const void* dy;
+  long lddy;
+  const void* z;
+  long ldz;
+  int z8;
+  void* dz;                // contiguous rows x cols
+  float* part;
+  long rows;
+  int cols;
+  long chunk;
+  int lanes;               // slope_lanes(cols)
+  int act;
+};
+
 // Up to three gradients' products in one launch (kEpiStore), the ones with the
 // longest tiles first.
 struct GemmGroup {
@@ -101,11 +118,15 @@ struct GemmGroup {
   int start[kMaxGroup];      // first workgroup of each
   int layout[kMaxGroup];     // kInputGrad or kWeightGrad
   GemmArgs a[kMaxGroup];
+  int sums_start;            // first workgroup of the column sums (the grid's size if there are none)
+  int blocks;
+  SlopeArgs sums;            // column sums alone
 };
 
 // 16-bit: kForward with kEpiLinear or kEpiGated, kInputGrad with kEpiGatedBack.
 hipError_t launch_gemm16_forward(const GemmArgs& a, const GemmPlan& p, int epi, bool bf16, hipStream_t stream);
 hipError_t launch_gemm16_gated_back(const GemmArgs& a, const GemmPlan& p, bool bf16, hipStream_t stream);
+// They also run a group's column sums, after its products.
 hipError_t launch_gemm16_group(const GemmGroup& g, const GemmPlan& p, bool bf16, hipStream_t stream);
 // fp32: the same.
 hipError_t launch_gemm32(const GemmArgs& a, const GemmPlan& p, int epi, hipStream_t stream);
@@ -126,22 +147,9 @@ struct FinishArgs {
 };
 hipError_t launch_finish(const FinishArgs& a, int dtype, hipStream_t stream);
 
-// dz = dy * act'(z) (dz may be null: column sums alone; act none: z unused)
-// and, with part, partial column sums of dz over `chunk` rows: part[r / chunk][n].
-struct SlopeArgs {
-  const void* dy;
-  long lddy;
-  const void* z;
-  long ldz;
-  int z8;
-  void* dz;                // contiguous rows x cols
-  float* part;
-  long rows;
-  int cols;
-  long chunk;
-  int act;
-};
 long slope_chunk(long rows);
+int slope_lanes(int cols);
+long slope_blocks(const SlopeArgs& a);
 hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
                             hipStream_t stream);

@@ -180,6 +180,8 @@ struct Gradients {
   Product p[kMaxGroup];
   GemmArgs a[kMaxGroup];
   FinishArgs finish;
+  bool summing;            // sums is to run (its column sums alone)
+  SlopeArgs sums;
   void add(const Product& pr, const void* q, long ldq, const void* pm, long ldp, const EpilogueArgs& e,
            void* slices) {
     p[count] = pr;
@@ -193,6 +195,21 @@ struct Gradients {
     c.cols = cols;
     c.out = out;
   }
+  // Column sums of dy (rows x cols) into out, through `part` (chunk by chunk).
+  void sum_columns(const void* dy, long lddy, long rows, int cols, long chunk, void* part, float* out) {
+    const long chunks = (rows + chunk - 1) / chunk;
+    sums = SlopeArgs{};
+    sums.dy = dy;
+    sums.lddy = lddy;
+    sums.part = chunks > 1 ? static_cast<float*>(part) : out;     // one chunk: the sums themselves
+    sums.rows = rows;
+    sums.cols = cols;
+    sums.chunk = chunk;
+    sums.lanes = slope_lanes(cols);
+    sums.act = OIDN_ACT_NONE;
+    summing = true;
+    if (chunks > 1) add_columns(part, chunks, cols, out);
+  }
   int run(hipStream_t stream) {
     bool done[kMaxGroup] = {};
     for (int first = 0; first < count; ++first) {
@@ -203,7 +220,8 @@ struct Gradients {
         if (done[k] || p[k].plan.tile_r != plan.tile_r || p[k].plan.direct != plan.direct) continue;
         done[k] = true;
         set_tiles(p[k], a[k]);
-        g.start[g.count] = g.count ? g.start[g.count - 1] + (int)gemm_blocks(g.a[g.count - 1]) : 0;
+        g.start[g.count] = g.blocks;
+        g.blocks += (int)gemm_blocks(a[k]);
         g.layout[g.count] = p[k].layout;
         g.a[g.count++] = a[k];
         if (p[k].plan.splits > 1) {
@@ -211,10 +229,17 @@ struct Gradients {
           finish.product[finish.products++].splits = p[k].plan.splits;
         }
       }
+      g.sums_start = g.blocks;
+      if (summing) {
+        g.sums = sums;
+        g.blocks += (int)slope_blocks(sums);
+        summing = false;
+      }
       OIDN_TRY(ran(dtype == OIDN_F32 ? launch_gemm32_group(g, plan, stream)
                                      : launch_gemm16_group(g, plan, dtype == OIDN_BF16, stream),
                    "gradient products launch"));
     }
+    if (summing) OIDN_TRY(ran(launch_slope(sums, dtype, stream), "column sum launch"));
     return ran(launch_finish(finish, dtype, stream), "sums launch");
   }
 };
@@ -512,25 +537,29 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
   LinearBack b = linear_back(m, k, n, act, dtype, flags, workspace);
   OIDN_TRY(check_workspace(workspace, ws_bytes, b.bytes));
 
-  if (slope || dbias) {
+  Gradients g{};
+  g.dtype = dtype;
+  if (slope) {
     SlopeArgs s{};
     s.dy = dy;
     s.lddy = lddy;
     s.z = z;
     s.ldz = ldz;
     s.z8 = z8;
-    s.dz = slope ? b.dz : nullptr;
+    s.dz = b.dz;
     s.part = dbias && b.chunks > 1 ? static_cast<float*>(b.sums) : dbias;   // one chunk: the sums themselves
     s.rows = m;
     s.cols = n;
     s.chunk = b.chunk;
+    s.lanes = slope_lanes(n);
     s.act = act;
     OIDN_TRY(ran(launch_slope(s, dtype, stream), "slope pass launch"));
+    if (dbias && b.chunks > 1) g.add_columns(b.sums, b.chunks, n, dbias);
+  } else if (dbias) {
+    g.sum_columns(dy, lddy, m, n, b.chunk, b.sums, dbias);
   }
   const void* dz = slope ? b.dz : dy;
   const long lddz = slope ? n : lddy;
-  Gradients g{dtype};
-  if (dbias && b.chunks > 1) g.add_columns(b.sums, b.chunks, n, dbias);
   if (dw) {
     if (x8) {
       OIDN_TRY(ran(launch_ckpt_unpack(x, m, k, b.x, k, dtype, stream), "checkpoint unpack launch"));
@@ -634,7 +663,8 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
   OIDN_TRY(check_workspace(workspace, ws_bytes, b.bytes));
 
   const long f2 = 2L * f;
-  Gradients g{dtype};
+  Gradients g{};
+  g.dtype = dtype;
   if (inner) {
     EpilogueArgs e{};
     e.y = b.dz;
@@ -649,18 +679,7 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
     OIDN_TRY(run_product(b.dh, dy, lddy, w_out, f, e, nullptr, stream, &groups));
     if (db_in) g.add_columns(e.part, groups, (int)f2, db_in);
   }
-  if (db_out) {
-    SlopeArgs s{};
-    s.dy = dy;
-    s.lddy = lddy;
-    s.part = b.chunks > 1 ? static_cast<float*>(b.out_sums) : db_out;
-    s.rows = m;
-    s.cols = d;
-    s.chunk = b.chunk;
-    s.act = OIDN_ACT_NONE;
-    OIDN_TRY(ran(launch_slope(s, dtype, stream), "column sum launch"));
-    if (b.chunks > 1) g.add_columns(b.out_sums, b.chunks, d, db_out);
-  }
+  if (db_out) g.sum_columns(dy, lddy, m, d, b.chunk, b.out_sums, db_out);
   // the longest sums first
   if (dw_in) {
     if (x8) {

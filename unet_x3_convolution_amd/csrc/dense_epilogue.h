@@ -80,9 +80,17 @@ __device__ __forceinline__ void store8(void* p, long i, const Eight& r, int n) {
       __builtin_memcpy(s, &t, 16);
     }
   } else {
+    // runs of four, two and one
+    T t[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < n) s[k] = (T)r.v[k];
+    for (int k = 0; k < 8; ++k) t[k] = (T)r.v[k];
+    const bool four = n & 4, two = n & 2;
+    if (four) __builtin_memcpy(s, t, 4 * sizeof(T));
+    if (two) {
+      const T p[2] = {four ? t[4] : t[0], four ? t[5] : t[1]};
+      __builtin_memcpy(s + (n & 4), p, 2 * sizeof(T));
+    }
+    if (n & 1) s[n - 1] = four ? (two ? t[6] : t[4]) : (two ? t[2] : t[0]);
   }
 }
 
@@ -308,12 +316,14 @@ struct RawCodes {
 template <int DT, bool Z8> struct RawFetched { Raw<DT> a, b; };
 template <int DT> struct RawFetched<DT, true> { RawCodes a, b; };
 
+// n of the elements are wanted; the rest may be anything, so that only where the
+// matrix ends within eight elements (`left` from here on) single ones are read.
 template <int DT>
-__device__ __forceinline__ Raw<DT> load_raw(const void* p, long i, int n) {
+__device__ __forceinline__ Raw<DT> load_raw(const void* p, long i, int n, long left) {
   typedef typename Storage<DT>::T T;
   const T* s = static_cast<const T*>(p) + i;
   Raw<DT> r;
-  if (n >= 8) {
+  if (left >= 8) {
     __builtin_memcpy(&r.e, s, sizeof(r.e));
   } else {
 #pragma unroll
@@ -329,20 +339,21 @@ __device__ __forceinline__ Eight ckpt_load8(const CkptAt& c, long i, int j) { re
 
 template <int DT, int EPI, bool WHOLE, bool Z8>
 __device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, RawFetched<DT, Z8>& f) {
-  const int n = WHOLE ? 8 : e.cols - j;     // columns that exist from j on
   if constexpr (EPI == kEpiPartial || EPI == kEpiGated) return;
-  if constexpr (WHOLE) i = i < e.rows ? i : e.rows - 1;
-  else if (i >= e.rows || n <= 0) return;
+  const int n = e.cols - j;                 // columns that exist from j on
+  if (!WHOLE && n <= 0) return;
+  i = i < e.rows ? i : e.rows - 1;
+  const long below = e.rows - 1 - i;        // rows after this one
   if constexpr (EPI == kEpiLinear || EPI == kEpiStore) {
-    if (e.res) f.a = load_raw<DT>(e.res, i * e.ldr + j, n);
+    if (e.res) f.a = load_raw<DT>(e.res, i * e.ldr + j, n, WHOLE ? 8 : below * e.ldr + n);
   }
   if constexpr (EPI == kEpiGatedBack) {
     if constexpr (Z8) {
       f.a = load_codes(ckpt_at(e.z, e.rows, e.cols), i, j);
       f.b = load_codes(ckpt_at(static_cast<char*>(e.z) + ckpt_size(e.rows, e.cols), e.rows, e.cols), i, j);
     } else {
-      f.a = load_raw<DT>(e.z, i * e.ldz + j, n);
-      f.b = load_raw<DT>(e.z, i * e.ldz + e.cols + j, n);
+      f.a = load_raw<DT>(e.z, i * e.ldz + j, n, WHOLE ? 8 : below * e.ldz + e.cols + n);
+      f.b = load_raw<DT>(e.z, i * e.ldz + e.cols + j, n, WHOLE ? 8 : below * e.ldz + n);
     }
   }
 }
@@ -466,10 +477,10 @@ __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const float
   const bool whole = j0 + 8 * kLanes <= e.cols;
   auto read = [&](long ir, int s) {
     if constexpr (kReads) {
-      if (whole || j + 8 <= e.cols) {
+      if (whole) {
 #pragma unroll
         for (int k = 0; k < kTogether; ++k) fetch<DT, EPI, true, Z8>(e, ir + (s + k) * kAtOnce, j, got[k]);
-      } else if (j < e.cols) {
+      } else {
 #pragma unroll
         for (int k = 0; k < kTogether; ++k) fetch<DT, EPI, false, Z8>(e, ir + (s + k) * kAtOnce, j, got[k]);
       }

@@ -28,6 +28,7 @@
 #pragma once
 
 #include "dense_gemm16.h"
+#include "dense_slope.h"
 
 namespace oidn {
 namespace {
@@ -284,6 +285,8 @@ __global__ __launch_bounds__(256, workgroups_per_cu(TR, TC)) void dense_gemm16(G
 template <bool BF, int T, bool DIRECT>
 __global__ __launch_bounds__(256, workgroups_per_cu(T, T)) void dense_gemm16_group(GemmGroup g) {
   __shared__ __attribute__((aligned(1024))) char lds[gemm16_lds<T, T>()];
+  if ((int)blockIdx.x >= g.sums_start)
+    return slope_rows<BF ? OIDN_BF16 : OIDN_F16>(g.sums, blockIdx.x - g.sums_start, reinterpret_cast<float*>(lds));
   int k = 0;
   while (k + 1 < g.count && (int)blockIdx.x >= g.start[k + 1]) ++k;
   const int block = blockIdx.x - g.start[k];

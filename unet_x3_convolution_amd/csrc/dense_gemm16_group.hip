@@ -6,7 +6,7 @@ namespace {
 
 template <bool BF, int T>
 hipError_t launch(const GemmGroup& g, const GemmPlan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)(g.start[g.count - 1] + gemm_blocks(g.a[g.count - 1])));
+  const dim3 grid((unsigned)g.blocks);
   if (p.direct)
     hipLaunchKernelGGL((dense_gemm16_group<BF, T, true>), grid, dim3(256), 0, stream, g);
   else if constexpr (T <= 128)

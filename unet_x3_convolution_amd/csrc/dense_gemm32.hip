@@ -9,6 +9,7 @@
 // and nothing is shuffled.  Strided operands are transposed by the LDS write:
 // eight neighbouring lanes read 128 contiguous bytes.
 #include "dense_gemm16.h"
+#include "dense_slope.h"
 
 namespace oidn {
 namespace {
@@ -136,6 +137,7 @@ __global__ __launch_bounds__(256, 2) void dense_gemm32(GemmArgs a) {
 template <int T>
 __global__ __launch_bounds__(256, 2) void dense_gemm32_group(GemmGroup g) {
   __shared__ __attribute__((aligned(16))) float lds[gemm32_lds<T, T>() / 4];
+  if ((int)blockIdx.x >= g.sums_start) return slope_rows<OIDN_F32>(g.sums, blockIdx.x - g.sums_start, lds);
   int k = 0;
   while (k + 1 < g.count && (int)blockIdx.x >= g.start[k + 1]) ++k;
   const int block = blockIdx.x - g.start[k];
@@ -164,7 +166,7 @@ hipError_t launch_gemm32(const GemmArgs& a, const GemmPlan& p, int epi, hipStrea
 }
 
 hipError_t launch_gemm32_group(const GemmGroup& g, const GemmPlan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)(g.start[g.count - 1] + gemm_blocks(g.a[g.count - 1]))), block(256);
+  const dim3 grid((unsigned)g.blocks), block(256);
   if (p.tile_r == 128) hipLaunchKernelGGL(dense_gemm32_group<128>, grid, block, 0, stream, g);
   else hipLaunchKernelGGL(dense_gemm32_group<64>, grid, block, 0, stream, g);
   return hipGetLastError();

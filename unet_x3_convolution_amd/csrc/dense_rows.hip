@@ -1,12 +1,10 @@
 // Memory-bound passes of the dense operators: the sum of a product's slices,
 // the slope pass dz = dy * act'(z) with column sums, column sums of partial
 // rows, 8-bit checkpoints of whole matrices, and zeros.
-#include "dense_epilogue.h"
+#include "dense_slope.h"
 
 namespace oidn {
 namespace {
-
-constexpr int kRowThreads = 256;
 
 // Sums of a product's slices: a workgroup takes 256 >> lg units of eight
 // columns, 1 << lg of its threads share a unit's slices, several reads in
@@ -95,55 +93,10 @@ __global__ __launch_bounds__(kRowThreads) void finish_sums(FinishArgs a, FinishP
   }
 }
 
-// A workgroup covers `chunk` rows by 8 << cs columns: 1 << cs units of eight
-// columns, the other threads are row lanes.
 template <int DT>
-__global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, int cs) {
-  const int u = threadIdx.x & ((1 << cs) - 1), rl = threadIdx.x >> cs, rows_at_once = kRowThreads >> cs;
-  const int j = (int)((blockIdx.y << cs) + u) * 8;
-  const int n = a.cols - j;
-  const long r0 = blockIdx.x * a.chunk, r1 = r0 + a.chunk < a.rows ? r0 + a.chunk : a.rows;
-  Eight sum{};
-  if (n > 0) {
-    // four rows' reads in flight
-    for (long i0 = r0 + rl; i0 < r1; i0 += 4 * rows_at_once) {
-      Eight d[4], z[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const long i = i0 + k * rows_at_once;
-        if (i >= r1) break;
-        d[k] = load8<DT>(a.dy, i * a.lddy + j, n);
-        if (a.act != OIDN_ACT_NONE)
-          z[k] = a.z8 ? ckpt_load8(ckpt_at(const_cast<void*>(a.z), a.rows, a.cols), i, j)
-                      : load8<DT>(a.z, i * a.ldz + j, n);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const long i = i0 + k * rows_at_once;
-        if (i >= r1) break;
-        if (a.act != OIDN_ACT_NONE) {
-          Eight value;
-          activate_slope8<DT>(a.act, z[k], value);
-#pragma unroll
-          for (int m = 0; m < 8; ++m) d[k].v[m] *= z[k].v[m];
-        }
-        if (a.dz) store8<DT>(a.dz, i * (long)a.cols + j, d[k], n);
-        add8(sum, d[k]);
-      }
-    }
-  }
-  if (!a.part) return;
-  // row lanes are added in order through LDS
-  __shared__ float lds[kRowThreads][9];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) lds[threadIdx.x][k] = sum.v[k];
-  __syncthreads();
-  for (int c = threadIdx.x; c < (8 << cs); c += kRowThreads) {
-    float s = 0.f;
-    for (int r = 0; r < rows_at_once; ++r) s += lds[(r << cs) + c / 8][c % 8];
-    const int col = (int)(blockIdx.y << cs) * 8 + c;
-    if (col < a.cols) a.part[(long)blockIdx.x * a.cols + col] = s;
-  }
+__global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a) {
+  __shared__ float lds[kSlopeLds / 4];
+  slope_rows<DT>(a, blockIdx.x, lds);
 }
 
 // A thread codes eight columns; four neighbouring lanes hold a block.
@@ -209,17 +162,21 @@ long slope_chunk(long rows) {
   return c < 32 ? 32 : c;
 }
 
-hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream) {
-  const int units = (a.cols + 7) / 8;
+int slope_lanes(int cols) {
+  const int units = (cols + 7) / 8;
   int cs = 0;
   while (cs < 5 && (1 << cs) < units) ++cs;
-  const dim3 grid((unsigned)((a.rows + a.chunk - 1) / a.chunk), (unsigned)((units + (1 << cs) - 1) >> cs));
-  if (dtype == OIDN_F32)
-    hipLaunchKernelGGL(slope_pass<OIDN_F32>, grid, dim3(kRowThreads), 0, stream, a, cs);
-  else if (dtype == OIDN_F16)
-    hipLaunchKernelGGL(slope_pass<OIDN_F16>, grid, dim3(kRowThreads), 0, stream, a, cs);
-  else
-    hipLaunchKernelGGL(slope_pass<OIDN_BF16>, grid, dim3(kRowThreads), 0, stream, a, cs);
+  return cs;
+}
+long slope_blocks(const SlopeArgs& a) {
+  return ((a.rows + a.chunk - 1) / a.chunk) * (((a.cols + 7) / 8 + (1 << a.lanes) - 1) >> a.lanes);
+}
+
+hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream) {
+  const dim3 grid((unsigned)slope_blocks(a)), block(kRowThreads);
+  if (dtype == OIDN_F32) hipLaunchKernelGGL(slope_pass<OIDN_F32>, grid, block, 0, stream, a);
+  else if (dtype == OIDN_F16) hipLaunchKernelGGL(slope_pass<OIDN_F16>, grid, block, 0, stream, a);
+  else hipLaunchKernelGGL(slope_pass<OIDN_BF16>, grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
