@@ -111,6 +111,21 @@ struct SlopeArgs {
   int act;
 };
 
+// A checkpoint read back beside another launch's work: blocks workgroups of
+// kUnpackRun * 256 units of eight columns each; y is contiguous.
+struct UnpackJob {
+  const void* ckpt;
+  long m;
+  int n;
+  void* y;
+  int blocks;              // 0: none
+};
+constexpr int kUnpackRun = 4;
+inline UnpackJob unpack_job(const void* ckpt, long m, int n, void* y) {
+  const long units = m * ((n + 7) / 8), per = kUnpackRun * 256;
+  return {ckpt, m, n, y, (int)((units + per - 1) / per)};
+}
+
 // Up to three gradients' products in one launch (kEpiStore), the ones with the
 // longest tiles first.
 struct GemmGroup {
@@ -125,11 +140,13 @@ struct GemmGroup {
 
 // 16-bit: kForward with kEpiLinear or kEpiGated, kInputGrad with kEpiGatedBack.
 hipError_t launch_gemm16_forward(const GemmArgs& a, const GemmPlan& p, int epi, bool bf16, hipStream_t stream);
-hipError_t launch_gemm16_gated_back(const GemmArgs& a, const GemmPlan& p, bool bf16, hipStream_t stream);
+// The latter, and the slope pass, take an unpack job along.
+hipError_t launch_gemm16_gated_back(const GemmArgs& a, const GemmPlan& p, bool bf16, const UnpackJob& job,
+                                    hipStream_t stream);
 // They also run a group's column sums, after its products.
 hipError_t launch_gemm16_group(const GemmGroup& g, const GemmPlan& p, bool bf16, hipStream_t stream);
 // fp32: the same.
-hipError_t launch_gemm32(const GemmArgs& a, const GemmPlan& p, int epi, hipStream_t stream);
+hipError_t launch_gemm32(const GemmArgs& a, const GemmPlan& p, int epi, const UnpackJob& job, hipStream_t stream);
 hipError_t launch_gemm32_group(const GemmGroup& g, const GemmPlan& p, hipStream_t stream);
 // Forward products (kEpiLinear, kEpiGated) of at most kFewRows rows, in one
 // launch without slices.
@@ -150,7 +167,7 @@ hipError_t launch_finish(const FinishArgs& a, int dtype, hipStream_t stream);
 long slope_chunk(long rows);
 int slope_lanes(int cols);
 long slope_blocks(const SlopeArgs& a);
-hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_slope(const SlopeArgs& a, const UnpackJob& job, int dtype, hipStream_t stream);
 hipError_t launch_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
                             hipStream_t stream);
 hipError_t launch_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ldy, int dtype,

@@ -154,16 +154,16 @@ void set_tiles(const Product& p, GemmArgs& a) {
   a.tiles_c = (int)((p.cols + c - 1) / c);
 }
 // A forward or gated backward product; `groups` receives the row groups of the
-// latter's column sums.
+// latter's column sums, and it takes `job` along.
 int run_product(Product p, const void* q, long ldq, const void* pm, long ldp, const EpilogueArgs& e,
-                void* slices, hipStream_t stream, long* groups = nullptr) {
+                void* slices, hipStream_t stream, long* groups = nullptr, const UnpackJob& job = {}) {
   GemmArgs a = gemm_args(p, q, ldq, pm, ldp, e, slices);
   set_tiles(p, a);
   if (groups) *groups = gated_back_groups(p.rows, p.plan.tile_r);
   hipError_t r;
   if (p.plan.few) r = launch_few(a, p.epi, p.dtype, stream);
-  else if (p.dtype == OIDN_F32) r = launch_gemm32(a, p.plan, p.epi, stream);
-  else if (p.epi == kEpiGatedBack) r = launch_gemm16_gated_back(a, p.plan, p.dtype == OIDN_BF16, stream);
+  else if (p.dtype == OIDN_F32) r = launch_gemm32(a, p.plan, p.epi, job, stream);
+  else if (p.epi == kEpiGatedBack) r = launch_gemm16_gated_back(a, p.plan, p.dtype == OIDN_BF16, job, stream);
   else r = launch_gemm16_forward(a, p.plan, p.epi, p.dtype == OIDN_BF16, stream);
   OIDN_TRY(ran(r, "matrix product launch"));
   if (p.plan.splits > 1)
@@ -239,7 +239,7 @@ struct Gradients {
                                      : launch_gemm16_group(g, plan, dtype == OIDN_BF16, stream),
                    "gradient products launch"));
     }
-    if (summing) OIDN_TRY(ran(launch_slope(sums, dtype, stream), "column sum launch"));
+    if (summing) OIDN_TRY(ran(launch_slope(sums, {}, dtype, stream), "column sum launch"));
     return ran(launch_finish(finish, dtype, stream), "sums launch");
   }
 };
@@ -553,7 +553,8 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
     s.chunk = b.chunk;
     s.lanes = slope_lanes(n);
     s.act = act;
-    OIDN_TRY(ran(launch_slope(s, dtype, stream), "slope pass launch"));
+    const UnpackJob job = dw && x8 ? unpack_job(x, m, k, b.x) : UnpackJob{};
+    OIDN_TRY(ran(launch_slope(s, job, dtype, stream), "slope pass launch"));
     if (dbias && b.chunks > 1) g.add_columns(b.sums, b.chunks, n, dbias);
   } else if (dbias) {
     g.sum_columns(dy, lddy, m, n, b.chunk, b.sums, dbias);
@@ -562,7 +563,7 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
   const long lddz = slope ? n : lddy;
   if (dw) {
     if (x8) {
-      OIDN_TRY(ran(launch_ckpt_unpack(x, m, k, b.x, k, dtype, stream), "checkpoint unpack launch"));
+      if (!slope) OIDN_TRY(ran(launch_ckpt_unpack(x, m, k, b.x, k, dtype, stream), "checkpoint unpack launch"));
       x = b.x;
       ldx = k;
     }
@@ -676,14 +677,14 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
     e.act = act;
     e.part = db_in ? static_cast<float*>(b.in_sums) : nullptr;
     long groups = 0;
-    OIDN_TRY(run_product(b.dh, dy, lddy, w_out, f, e, nullptr, stream, &groups));
+    const UnpackJob job = dw_in && x8 ? unpack_job(x, m, d, b.x) : UnpackJob{};
+    OIDN_TRY(run_product(b.dh, dy, lddy, w_out, f, e, nullptr, stream, &groups, job));
     if (db_in) g.add_columns(e.part, groups, (int)f2, db_in);
   }
   if (db_out) g.sum_columns(dy, lddy, m, d, b.chunk, b.out_sums, db_out);
   // the longest sums first
   if (dw_in) {
     if (x8) {
-      OIDN_TRY(ran(launch_ckpt_unpack(x, m, d, b.x, d, dtype, stream), "checkpoint unpack launch"));
       x = b.x;
       ldx = d;
     }

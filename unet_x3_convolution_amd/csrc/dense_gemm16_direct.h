@@ -280,6 +280,15 @@ __global__ __launch_bounds__(256, workgroups_per_cu(TR, TC)) void dense_gemm16(G
   gemm16<BF, LAYOUT, EPI, TR, TC, DIRECT>(a, blockIdx.x, lds);
 }
 
+// The gated block's dh with its epilogue; the first workgroups read a
+// checkpoint back for the products that follow.
+template <bool BF, int T, bool DIRECT>
+__global__ __launch_bounds__(256, workgroups_per_cu(T, T)) void dense_gemm16_gated_back(GemmArgs a, UnpackJob u) {
+  __shared__ __attribute__((aligned(1024))) char lds[gemm16_lds<T, T>()];
+  if ((int)blockIdx.x < u.blocks) return unpack_rows<BF ? OIDN_BF16 : OIDN_F16>(u, blockIdx.x);
+  gemm16<BF, kInputGrad, kEpiGatedBack, T, T, DIRECT>(a, blockIdx.x - u.blocks, lds);
+}
+
 // Several gradients' products in one launch: they fill the device together,
 // and the last tiles of one run beside the first of the next.
 template <bool BF, int T, bool DIRECT>

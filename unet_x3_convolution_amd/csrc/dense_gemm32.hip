@@ -128,9 +128,12 @@ __device__ __forceinline__ void gemm32(const GemmArgs& a, int block, float* lds)
 }
 
 template <int LAYOUT, int EPI, int TR, int TC>
-__global__ __launch_bounds__(256, 2) void dense_gemm32(GemmArgs a) {
+__global__ __launch_bounds__(256, 2) void dense_gemm32(GemmArgs a, UnpackJob u) {
   __shared__ __attribute__((aligned(16))) float lds[gemm32_lds<TR, TC>() / 4];
-  gemm32<LAYOUT, EPI, TR, TC>(a, blockIdx.x, lds);
+  if constexpr (EPI == kEpiGatedBack) {
+    if ((int)blockIdx.x < u.blocks) return unpack_rows<OIDN_F32>(u, blockIdx.x);
+  }
+  gemm32<LAYOUT, EPI, TR, TC>(a, blockIdx.x - (EPI == kEpiGatedBack ? u.blocks : 0), lds);
 }
 
 // Several gradients' products in one launch.
@@ -146,22 +149,22 @@ __global__ __launch_bounds__(256, 2) void dense_gemm32_group(GemmGroup g) {
 }
 
 template <int LAYOUT, int EPI>
-hipError_t launch_epi(const GemmArgs& a, const GemmPlan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)gemm_blocks(a)), block(256);
+hipError_t launch_epi(const GemmArgs& a, const GemmPlan& p, const UnpackJob& u, hipStream_t stream) {
+  const dim3 grid((unsigned)(gemm_blocks(a) + u.blocks)), block(256);
   constexpr int SC = EPI == kEpiGated ? 128 : 64;
   if (p.tile_r == 128)
-    hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 128, 128>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 128, 128>), grid, block, 0, stream, a, u);
   else
-    hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 64, SC>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 64, SC>), grid, block, 0, stream, a, u);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gemm32(const GemmArgs& a, const GemmPlan& p, int epi, hipStream_t stream) {
-  if (epi == kEpiLinear) return launch_epi<kForward, kEpiLinear>(a, p, stream);
-  if (epi == kEpiGated) return launch_epi<kForward, kEpiGated>(a, p, stream);
-  if (epi == kEpiGatedBack) return launch_epi<kInputGrad, kEpiGatedBack>(a, p, stream);
+hipError_t launch_gemm32(const GemmArgs& a, const GemmPlan& p, int epi, const UnpackJob& u, hipStream_t stream) {
+  if (epi == kEpiLinear) return launch_epi<kForward, kEpiLinear>(a, p, u, stream);
+  if (epi == kEpiGated) return launch_epi<kForward, kEpiGated>(a, p, u, stream);
+  if (epi == kEpiGatedBack) return launch_epi<kInputGrad, kEpiGatedBack>(a, p, u, stream);
   return hipErrorInvalidValue;
 }
 

@@ -94,9 +94,10 @@ __global__ __launch_bounds__(kRowThreads) void finish_sums(FinishArgs a, FinishP
 }
 
 template <int DT>
-__global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a) {
+__global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, UnpackJob u) {
   __shared__ float lds[kSlopeLds / 4];
-  slope_rows<DT>(a, blockIdx.x, lds);
+  if ((int)blockIdx.x < u.blocks) unpack_rows<DT>(u, blockIdx.x);
+  else slope_rows<DT>(a, blockIdx.x - u.blocks, lds);
 }
 
 // A thread codes eight columns; four neighbouring lanes hold a block.
@@ -172,11 +173,11 @@ long slope_blocks(const SlopeArgs& a) {
   return ((a.rows + a.chunk - 1) / a.chunk) * (((a.cols + 7) / 8 + (1 << a.lanes) - 1) >> a.lanes);
 }
 
-hipError_t launch_slope(const SlopeArgs& a, int dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)slope_blocks(a)), block(kRowThreads);
-  if (dtype == OIDN_F32) hipLaunchKernelGGL(slope_pass<OIDN_F32>, grid, block, 0, stream, a);
-  else if (dtype == OIDN_F16) hipLaunchKernelGGL(slope_pass<OIDN_F16>, grid, block, 0, stream, a);
-  else hipLaunchKernelGGL(slope_pass<OIDN_BF16>, grid, block, 0, stream, a);
+hipError_t launch_slope(const SlopeArgs& a, const UnpackJob& u, int dtype, hipStream_t stream) {
+  const dim3 grid((unsigned)(slope_blocks(a) + u.blocks)), block(kRowThreads);
+  if (dtype == OIDN_F32) hipLaunchKernelGGL(slope_pass<OIDN_F32>, grid, block, 0, stream, a, u);
+  else if (dtype == OIDN_F16) hipLaunchKernelGGL(slope_pass<OIDN_F16>, grid, block, 0, stream, a, u);
+  else hipLaunchKernelGGL(slope_pass<OIDN_BF16>, grid, block, 0, stream, a, u);
   return hipGetLastError();
 }
 

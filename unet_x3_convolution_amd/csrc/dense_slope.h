@@ -1,4 +1,5 @@
-// The pass dz = dy * act'(z) over rows, with column sums (SlopeArgs).
+// The pass dz = dy * act'(z) over rows, with column sums (SlopeArgs), and
+// checkpoints read back beside other work (UnpackJob).
 #pragma once
 
 #include "dense_epilogue.h"
@@ -57,6 +58,24 @@ __device__ __forceinline__ void slope_rows(const SlopeArgs& a, int block, float*
     for (int r = 0; r < rows_at_once; ++r) s += lds[((r << cs) + c / 8) * 9 + c % 8];
     const int col = (bc << cs) * 8 + c;
     if (col < a.cols) a.part[(long)chunk * a.cols + col] = s;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack_rows(const UnpackJob& u, int block) {
+  const long units = (u.n + 7) / 8, total = u.m * units;
+  const CkptAt at = ckpt_at(const_cast<void*>(u.ckpt), u.m, u.n);
+  RawCodes got[kUnpackRun];
+#pragma unroll
+  for (int k = 0; k < kUnpackRun; ++k) {
+    const long t = ((long)block * kUnpackRun + k) * kRowThreads + threadIdx.x, i = t / units;
+    if (t < total) got[k] = load_codes(at, i, (int)(t - i * units) * 8);
+  }
+#pragma unroll
+  for (int k = 0; k < kUnpackRun; ++k) {
+    const long t = ((long)block * kUnpackRun + k) * kRowThreads + threadIdx.x, i = t / units;
+    const int j = (int)(t - i * units) * 8;
+    if (t < total) store8<DT>(u.y, i * u.n + j, got[k].value(), u.n - j);
   }
 }
 
