@@ -153,13 +153,11 @@ __device__ __forceinline__ void activate_slope(int act, float z, float& a, float
 }
 
 // ------------------------------------------------------ 8-bit checkpoints
-// A block is 32 columns of a row: s = bf16(max|x| / 127), q = rint(x / s).
-// Taken as x * (1 / s): the code differs from rint(x / s) only where x / s is
-// within 2^-16 of a tie.  The error is at most half a step of s: the rounding
-// of s leaves max|x| / s at most 127.5, so the clamp to 127 costs no more.
-// Blocks whose scale falls below 2^-120 are stored as zeros; a block with an
-// infinity or a NaN gets the scale NaN, so all of it reads back as NaN and
-// the gradients it enters show it.
+// A block is 32 columns of a row: s = bf16(max|x| / 127), q = rint(x / s).  The
+// error is at most half a step of s: the rounding of s leaves max|x| / s at most
+// 127.5, so the clamp to 127 costs no more.  Blocks whose scale falls below
+// 2^-120 are stored as zeros; a block with an infinity or a NaN gets the scale
+// NaN, so all of it reads back as NaN and the gradients it enters show it.
 __device__ __forceinline__ float bf16_round(float v) { return (float)(__bf16)v; }
 
 struct CkptAt {
@@ -186,14 +184,17 @@ __device__ __forceinline__ float ckpt_scale(unsigned top) {
   const float s = bf16_round(__builtin_fmaf(__builtin_fmaf(-q, 127.f, t), r, q));
   return s < 7.52316385e-37f ? 0.f : s;
 }
-// Adding 1.5 * 2^23 rounds to a whole number, nearest even, and leaves its two's
-// complement in the low byte.
+// The quotient takes one correction step, so that ties are ties (common where x
+// has few bits); adding 1.5 * 2^23 rounds to a whole number, nearest even, and
+// leaves its two's complement in the low byte.
 __device__ __forceinline__ uint2 ckpt_codes(const Eight& x, float s) {
   const float inv = s > 0.f ? __builtin_amdgcn_rcpf(s) : 0.f, magic = 12582912.f;
   unsigned q[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    q[k] = __float_as_uint(__builtin_amdgcn_fmed3f(__builtin_fmaf(x.v[k], inv, magic), magic - 127.f, magic + 127.f));
+  for (int k = 0; k < 8; ++k) {
+    const float t = x.v[k] * inv, exact = __builtin_fmaf(__builtin_fmaf(-t, s, x.v[k]), inv, t);
+    q[k] = __float_as_uint(__builtin_amdgcn_fmed3f(exact + magic, magic - 127.f, magic + 127.f));
+  }
   auto four = [&](const unsigned* p) {        // low bytes of four values
     return __builtin_amdgcn_perm(__builtin_amdgcn_perm(p[3], p[2], 0x0c0c0400),
                                  __builtin_amdgcn_perm(p[1], p[0], 0x0c0c0400), 0x05040100);

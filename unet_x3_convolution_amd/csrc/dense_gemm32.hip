@@ -2,7 +2,7 @@
 // products, tiles of C and epilogues as the 16-bit form (dense_gemm16.h).
 //
 // 32 summed elements are staged at a time through registers into one of two
-// LDS buffers, as rows of 32 + 4 floats: the pad puts the 16 rows of a
+// LDS buffers, two or three tiles ahead, as rows of 32 + 4 floats: the pad puts the 16 rows of a
 // fragment's 16-byte reads on distinct banks.  A lane's 16 bytes are elements
 // 4 g .. 4 g + 3 (g = lane / 16) of 16; MFMA e takes element e of every lane,
 // in both operands, so the order of the sum is permuted within 16 elements
@@ -74,51 +74,70 @@ __device__ __forceinline__ void gemm32(const GemmArgs& a, int block, float* lds)
 #pragma unroll
     for (int r = 0; r < FR; ++r) acc[c][r] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  // Tiles in flight in registers; tile t waits in set (t - t0) % kAhead.
-  constexpr int kAhead = 2;
+  // Tile t is multiplied out of LDS buffer (t - t0) % 2 while tile t + 1 goes
+  // into the other one from register set (t + 1 - t0) % 2 and the loads of tile
+  // t + 3 leave for that set: the LDS writes and the second half's reads are
+  // issued between the MFMAs, which take 32 cycles each.
   Loader<4, TC, kDenseKF32, PS> from_p(a.p, a.ldp, j0, a.e.cols, t0 * kDenseKF32, a.len, half);
   Loader<4, TR, kDenseKF32, QS> from_q(a.q, a.ldq, i0, a.e.rows, t0 * kDenseKF32, a.len, 0);
-  uint4 up[kAhead][P::kUnits], uq[kAhead][Q::kUnits];
+  uint4 up[2][P::kUnits], uq[2][Q::kUnits];
   auto load = [&](long t, int set) {
+    if (t >= t1) return;
     from_p.load(up[set], t * kDenseKF32);
     from_q.load(uq[set], t * kDenseKF32);
   };
+  auto store = [&](long t, int set) {
+    if (t >= t1) return;
+    float* const l = lds + set * (P::kFloats + Q::kFloats);
+    P::store(up[set], l);
+    Q::store(uq[set], l + P::kFloats);
+  };
+  floatx4 fp[2][FC], fq[2][FR];          // [half of the tile][fragment]
+  auto read = [&](int set, int kk) {
+    const float* const lp = lds + set * (P::kFloats + Q::kFloats);
 #pragma unroll
-  for (int s = 0; s < kAhead; ++s)
-    if (t0 + s < t1) load(t0 + s, s);
-  for (long tt = t0; tt < t1; tt += kAhead) {
+    for (int c = 0; c < FC; ++c) {
+      const int pair = c / 2;
+      const int base = EPI == kEpiGated
+                           ? (pair < FC / 4 ? wc * (TC / 4) + 32 * pair
+                                            : TC / 2 + wc * (TC / 4) + 32 * (pair - FC / 4))
+                           : wc * (TC / 2) + 32 * pair;
+      fp[kk][c] = P::template fragment<true>(lp, base, c & 1, kk);
+    }
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
+    for (int r = 0; r < FR; ++r)
+      fq[kk][r] = Q::template fragment<false>(lp + P::kFloats, wr * (TR / 2), r, kk);
+  };
+  auto multiply = [&](int kk, int e0, int e1) {
+#pragma unroll
+    for (int e = e0; e < e1; ++e)
+#pragma unroll
+      for (int c = 0; c < FC; ++c)
+#pragma unroll
+        for (int r = 0; r < FR; ++r)
+          acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(fp[kk][c][e], fq[kk][r][e], acc[c][r], 0, 0, 0);
+  };
+  load(t0, 0);
+  load(t0 + 1, 1);
+  store(t0, 0);
+  load(t0 + 2, 0);
+  for (long tt = t0; tt < t1; tt += 2) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
       const long t = tt + s;
       if (t >= t1) break;
-      float* const lp = lds + ((t - t0) & 1) * (P::kFloats + Q::kFloats);
-      float* const lq = lp + P::kFloats;
-      P::store(up[s], lp);
-      Q::store(uq[s], lq);
-      __syncthreads();
-      if (t + kAhead < t1) load(t + kAhead, s);
-#pragma unroll
-      for (int kk = 0; kk < kDenseKF32 / 16; ++kk) {
-        floatx4 fp[FC], fq[FR];
-#pragma unroll
-        for (int c = 0; c < FC; ++c) {
-          const int pair = c / 2;
-          const int base = EPI == kEpiGated
-                               ? (pair < FC / 4 ? wc * (TC / 4) + 32 * pair
-                                                : TC / 2 + wc * (TC / 4) + 32 * (pair - FC / 4))
-                               : wc * (TC / 2) + 32 * pair;
-          fp[c] = P::template fragment<true>(lp, base, c & 1, kk);
-        }
-#pragma unroll
-        for (int r = 0; r < FR; ++r) fq[r] = Q::template fragment<false>(lq, wr * (TR / 2), r, kk);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int c = 0; c < FC; ++c)
-#pragma unroll
-            for (int r = 0; r < FR; ++r)
-              acc[c][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(fp[c][e], fq[r][e], acc[c][r], 0, 0, 0);
-      }
+      __syncthreads();                   // tile t is written, tile t - 1 has been read
+      read(s, 0);
+      read(s, 1);
+      multiply(0, 0, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      store(t + 1, 1 - s);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(0, 2, 4);
+      __builtin_amdgcn_sched_barrier(0);
+      load(t + 3, 1 - s);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(1, 0, 4);
     }
   }
   __syncthreads();                       // every wave has read its last fragments
