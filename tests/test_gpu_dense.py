@@ -554,3 +554,20 @@ def test_training_step_in_a_graph(precision):
         torch.cuda.synchronize()
         for o, e in zip(outs, eager):
             assert torch.equal(o, e)
+
+
+@pytest.mark.parametrize("precision", ["f16", "bf16"])
+@pytest.mark.parametrize("k, n", [(24, 40), (100, 64), (33, 128), (128, 97)])
+def test_narrow_linear_backward_of_many_rows(k, n, precision):
+    """More blocks of rows than workgroups: each takes several, the last block is ragged."""
+    m, dt, ty = 33333, DT[precision], TORCH[precision]
+    mk, kind = Maker(k * n, precision), "silu"
+    x, w, dy, z = mk.rows(m, k, 8), mk.rows(n, k, 0, k ** -0.5), mk.rows(m, n, 3), mk.rows(m, n)
+    dx, dw, db = Out(m, k, ty, 5), Out(n, k, ty, 1), Out(1, n, torch.float32)
+    ws = bytes_(U.oidn_linear_backward_workspace_bytes(m, k, n, ACT[kind], dt, 0))
+    U.oidn_linear_backward(dy, dy.stride(0), x, x.stride(0), z, n, w, k, dx.view, dx.ld, dw.view, dw.ld, db.view, m, k, n,
+                           ACT[kind], dt, 0, ws, ws.numel())
+    want = linear_backward(given(dy), given(x), given(z), given(w), kind, precision)
+    check(dx.get(), want[0], precision, "dx")
+    check(dw.get(), want[1], precision, "dw")
+    check(db.get()[0], want[2], "f32", "dbias")

@@ -16,7 +16,7 @@ OBJ_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "liboidn_mi355x.so")
 SOURCES = ["api.cpp", "conv_f16.hip", "conv_f32.hip", "elementwise.hip", "noalloc.hip",
            "calibrate.hip", "dense_api.cpp", "dense_rows.hip", "dense_gemm16_forward.hip",
-           "dense_gemm16_gated_back.hip", "dense_gemm16_group.hip", "dense_gemm32.hip", "dense_few.hip"]
+           "dense_gemm16_gated_back.hip", "dense_gemm16_group.hip", "dense_gemm32.hip", "dense_few.hip", "dense_narrow.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # Packed-fp32 ops are turned off for the device code: plain fp32 arithmetic only.

@@ -168,6 +168,37 @@ long slope_chunk(long rows);
 int slope_lanes(int cols);
 long slope_blocks(const SlopeArgs& a);
 hipError_t launch_slope(const SlopeArgs& a, const UnpackJob& job, int dtype, hipStream_t stream);
+// All gradients of a narrow 16-bit layer (n, k <= kNarrow) in one pass over its
+// rows; `grid` workgroups share the blocks of 64 rows.  dx, dw and sums may be
+// null.  With more than one workgroup dw goes to `slices` ([grid][n][k], fp32)
+// and the column sums to `sums` ([grid][n]).
+constexpr int kNarrow = 128;
+struct NarrowArgs {
+  const void* dy;
+  long lddy;
+  const void* z;
+  long ldz;
+  const void* x;
+  long ldx;
+  const void* w;
+  long ldw;
+  void* dx;
+  long lddx;
+  void* dw;
+  long lddw;
+  float* slices;
+  float* sums;
+  long rows;
+  int n, k;
+  int blocks;              // of 64 rows
+  int act;
+};
+inline int narrow_grid(long rows) {
+  const long b = (rows + 63) / 64;
+  return (int)(b < 512 ? b : 512);
+}
+hipError_t launch_narrow_back(const NarrowArgs& a, int grid, bool bf16, hipStream_t stream);
+
 hipError_t launch_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
                             hipStream_t stream);
 hipError_t launch_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ldy, int dtype,

@@ -188,6 +188,10 @@ struct Gradients {
     a[count] = gemm_args(p[count], q, ldq, pm, ldp, e, slices);
     ++count;
   }
+  void add_slices(const EpilogueArgs& e, int splits) {
+    finish.product[finish.products].e = e;
+    finish.product[finish.products++].splits = splits;
+  }
   void add_columns(const void* part, long groups, int cols, float* out) {
     auto& c = finish.column[finish.columns++];
     c.part = static_cast<const float*>(part);
@@ -224,10 +228,7 @@ struct Gradients {
         g.blocks += (int)gemm_blocks(a[k]);
         g.layout[g.count] = p[k].layout;
         g.a[g.count++] = a[k];
-        if (p[k].plan.splits > 1) {
-          finish.product[finish.products].e = a[k].e;
-          finish.product[finish.products++].splits = p[k].plan.splits;
-        }
+        if (p[k].plan.splits > 1) add_slices(a[k].e, p[k].plan.splits);
       }
       g.sums_start = g.blocks;
       if (summing) {
@@ -267,6 +268,7 @@ struct Regions {
 
 // ---------------------------------------------------------------- linear
 struct LinearBack {
+  bool narrow;             // one pass over the rows (launch_narrow_back)
   Product dx, dw;
   long chunk, chunks;
   void *dz, *x, *sums, *dx_slices, *dw_slices;
@@ -274,6 +276,15 @@ struct LinearBack {
 };
 LinearBack linear_back(long m, int k, int n, int act, int dtype, unsigned flags, void* ws) {
   LinearBack b{};
+  if (dtype != OIDN_F32 && flags == 0 && n <= kNarrow && k <= kNarrow) {
+    b.narrow = true;
+    const size_t grid = narrow_grid(m);
+    Regions r{static_cast<char*>(ws), 0};
+    b.sums = r.take(align256(grid * n * sizeof(float)));
+    b.dw_slices = grid > 1 ? r.take(align256(grid * n * k * sizeof(float))) : nullptr;
+    b.bytes = r.used;
+    return b;
+  }
   b.dx = Product{kInputGrad, kEpiStore, m, k, n, dtype, {}};
   b.dw = Product{kWeightGrad, kEpiStore, n, k, m, dtype, {}};
   Product* const both[] = {&b.dw, &b.dx};
@@ -539,6 +550,42 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
 
   Gradients g{};
   g.dtype = dtype;
+  if (b.narrow) {
+    const int grid = narrow_grid(m);
+    NarrowArgs a{};
+    a.dy = dy;
+    a.lddy = lddy;
+    a.z = z;
+    a.ldz = ldz;
+    a.x = x;
+    a.ldx = ldx;
+    a.w = w;
+    a.ldw = ldw;
+    a.dx = dx;
+    a.lddx = lddx;
+    a.dw = dw;
+    a.lddw = lddw;
+    a.slices = static_cast<float*>(b.dw_slices);
+    a.sums = dbias && grid > 1 ? static_cast<float*>(b.sums) : dbias;
+    a.rows = m;
+    a.n = n;
+    a.k = k;
+    a.blocks = (int)((m + 63) / 64);
+    a.act = act;
+    if (dx || dw || dbias) OIDN_TRY(ran(launch_narrow_back(a, grid, dtype == OIDN_BF16, stream), "gradients launch"));
+    if (grid > 1) {
+      if (dw) {
+        EpilogueArgs e = store_to(dw, lddw, nullptr, 0);
+        e.part = a.slices;
+        e.rows = n;
+        e.cols = k;
+        g.add_slices(e, grid);
+      }
+      if (dbias) g.add_columns(b.sums, grid, n, dbias);
+      OIDN_TRY(g.run(stream));
+    }
+    return clear_error();
+  }
   if (slope) {
     SlopeArgs s{};
     s.dy = dy;

@@ -39,10 +39,10 @@ __device__ __forceinline__ void sum_slices(const EpilogueArgs& e, int splits, in
 }
 constexpr int kSumLds = kRowThreads * 32;
 
-// Threads that share a unit: as many as have four slices each, at most 8.
+// Threads that share a unit: as many as have four slices each, at most 32.
 int slice_lanes(int splits) {
   int lg = 0;
-  while (lg < 3 && (8 << lg) <= splits) ++lg;
+  while (lg < 5 && (8 << lg) <= splits) ++lg;
   return lg;
 }
 long slice_blocks(const EpilogueArgs& e, int splits) {
@@ -56,28 +56,30 @@ __global__ __launch_bounds__(kRowThreads) void split_sum(EpilogueArgs e, int spl
   sum_slices<DT, kEpiLinear>(e, splits, lg, blockIdx.x, lds);
 }
 
-// 32 columns x 8 lanes over the groups of partial column sums.
+// Columns of partial sums, 256 / lanes of them a workgroup: each is shared by
+// `lanes` threads, eight reads in flight each, added in order.
 __device__ __forceinline__ void sum_columns(const float* __restrict__ part, long groups, int cols,
-                                            float* __restrict__ out, int block, char* mem) {
-  const int c = threadIdx.x & 31, l = threadIdx.x >> 5, j = block * 32 + c;
+                                            float* __restrict__ out, int block, int lanes, char* mem) {
+  const int across = kRowThreads / lanes, c = threadIdx.x % across, l = threadIdx.x / across, j = block * across + c;
   float s = 0.f;
   if (j < cols) {
 #pragma unroll 8
-    for (long g = l; g < groups; g += 8) s += part[g * cols + j];
+    for (long g = l; g < groups; g += lanes) s += part[g * cols + j];
   }
   float* const lds = reinterpret_cast<float*>(mem);
   lds[threadIdx.x] = s;
   __syncthreads();
   if (l == 0 && j < cols) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) s += lds[k * 32 + c];
+    for (int k = 1; k < lanes; ++k) s += lds[k * across + c];
     out[j] = s;
   }
 }
+int column_lanes(long groups) { return groups > 64 ? 32 : 8; }
 
 struct FinishPlan {
   int start[kMaxGroup + 2 + 1];     // first workgroup of each job, products first
   int lg[kMaxGroup];
+  int lanes[2];
 };
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void finish_sums(FinishArgs a, FinishPlan p) {
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(kRowThreads) void finish_sums(FinishArgs a, FinishP
     sum_slices<DT, kEpiStore>(a.product[k].e, a.product[k].splits, p.lg[k], block, lds);
   } else {
     const auto& c = a.column[k - a.products];
-    sum_columns(c.part, c.groups, c.cols, c.out, block, lds);
+    sum_columns(c.part, c.groups, c.cols, c.out, block, p.lanes[k - a.products], lds);
   }
 }
 
@@ -147,7 +149,11 @@ hipError_t launch_finish(const FinishArgs& a, int dtype, hipStream_t stream) {
     p.lg[k] = slice_lanes(a.product[k].splits);
     p.start[k + 1] = p.start[k] + (int)slice_blocks(a.product[k].e, a.product[k].splits);
   }
-  for (int c = 0; c < a.columns; ++c, ++k) p.start[k + 1] = p.start[k] + (a.column[c].cols + 31) / 32;
+  for (int c = 0; c < a.columns; ++c, ++k) {
+    p.lanes[c] = column_lanes(a.column[c].groups);
+    const int across = kRowThreads / p.lanes[c];
+    p.start[k + 1] = p.start[k] + (a.column[c].cols + across - 1) / across;
+  }
   if (k == 0) return hipSuccess;
   const dim3 grid((unsigned)p.start[k]), block(kRowThreads);
   if (dtype == OIDN_F32) hipLaunchKernelGGL(finish_sums<OIDN_F32>, grid, block, 0, stream, a, p);
