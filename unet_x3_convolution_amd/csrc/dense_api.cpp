@@ -375,20 +375,20 @@ namespace oidn {
 //   128 x 128   6.2 + 0.49 kt at q = 1,  15 + 1.6 kt at q = 4
 //   256 x 256   16 + 1.4 kt at q = 1,    19 + 2.9 kt at q = 2
 // that is, a start, a cost per tile, and per staged tile the larger of a
-// workgroup's own pace and its share of the compute unit's.  fp32 tiles hold
-// half as many summed elements at a sixteenth of the rate.  Summing slices
-// costs a launch and moves their bytes twice.
+// workgroup's own pace and its share of the compute unit's.  fp32 tiles (64 x
+// 64) hold half as many summed elements and take 0.8 us alone, 0.53 us of a
+// full unit.  Summing slices costs a launch and moves their bytes twice.
 struct TileCost { long tile; double start, each, own, share; };
 constexpr TileCost kCost16[] = {{64, 2.8, 0.7, 0.27, 0.17}, {128, 3.4, 2.9, 0.49, 0.40}, {256, 6.5, 9.0, 1.35, 1.40}};
 constexpr TileCost kCostGated = {64, 2.8, 1.3, 0.35, 0.30};      // a gated product's 64 x 128
-constexpr TileCost kCost32[] = {{64, 3.0, 1.0, 0.70, 0.55}, {128, 5.0, 4.0, 2.2, 2.0}};
+constexpr TileCost kCost32[] = {{64, 3.5, 1.0, 0.80, 0.53}};
 constexpr long kMaxSlices = 256;
 constexpr double kCus = 256, kSliceLaunch = 3.0, kSliceBytesPerUs = 4e6;
 
 void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, int dtype, bool direct) {
   const long bk = dtype == OIDN_F32 ? kDenseKF32 : kDenseK;
   const TileCost* const table = dtype == OIDN_F32 ? kCost32 : kCost16;
-  const int choices = dtype == OIDN_F32 || !direct ? 2 : 3;
+  const int choices = dtype == OIDN_F32 ? 1 : direct ? 3 : 2;
   double best = 0;
   for (int c = 0; c < choices; ++c) {
     const TileCost t = shapes[0].epi == kEpiGated && table[c].tile == 64 ? kCostGated : table[c];

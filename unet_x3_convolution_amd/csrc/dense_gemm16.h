@@ -114,17 +114,11 @@ struct Loader {
   long i0, rows, ld, len, half;
   bool columns;              // STRIDED: every column of the tile exists
 
-  // Row and unit in the row of unit k.  A strided fp32 tile deals its units so
-  // that a wave's LDS writes, which transpose, spread over the banks.
+  // Row and unit in the row of unit k.
   static __device__ __forceinline__ void place(int k, int& r, int& s) {
-    if constexpr (STRIDED && SIZE == 4) {
-      r = threadIdx.x >> 3;
-      s = (threadIdx.x & 7) + 8 * k;
-    } else {
-      const int t = threadIdx.x + k * 256;
-      r = t / kPerRow;
-      s = t % kPerRow;
-    }
+    const int t = threadIdx.x + k * 256;
+    r = t / kPerRow;
+    s = t % kPerRow;
   }
   // Tiles start at output row i0_ (of rows_) and summed element l0 (of len_).
   // half_: tile rows from T / 2 on come from `half` further matrix rows

@@ -1,13 +1,18 @@
 // fp32 matrix products on the matrix cores (v_mfma_f32_16x16x4), the same
 // products, tiles of C and epilogues as the 16-bit form (dense_gemm16.h).
 //
+// Tiles of C are 64 x 64 (gated: 64 x 128), several to a compute unit: 4096 x
+// 4096 x 1024 runs at 120 TFLOP/s, 128 x 128 tiles at 105, one or two to a unit
+// with their registers full.
+//
 // 32 summed elements are staged at a time through registers into one of two
-// LDS buffers, two or three tiles ahead, as rows of 32 + 4 floats: the pad puts the 16 rows of a
-// fragment's 16-byte reads on distinct banks.  A lane's 16 bytes are elements
+// LDS buffers, two or three tiles ahead, as rows of 32 + 4 floats: the pad puts
+// the 16 rows of a fragment's 16-byte reads on distinct banks.  A lane's 16 bytes are elements
 // 4 g .. 4 g + 3 (g = lane / 16) of 16; MFMA e takes element e of every lane,
 // in both operands, so the order of the sum is permuted within 16 elements
-// and nothing is shuffled.  Strided operands are transposed by the LDS write:
-// eight neighbouring lanes read 128 contiguous bytes.
+// and nothing is shuffled.  Strided operands keep rows of T + 4 floats, one per
+// summed element, and are read float by float: the pad puts the rows of the
+// four lane groups on distinct banks.
 #include "dense_gemm16.h"
 #include "dense_slope.h"
 
@@ -18,34 +23,36 @@ constexpr int kPad32 = kDenseKF32 + 4;
 
 template <int T, bool STRIDED>
 struct Stage32 {
-  static constexpr int kUnits = T * kDenseKF32 / 4 / 256;
-  static constexpr int kFloats = T * kPad32;
+  typedef Loader<4, T, kDenseKF32, STRIDED> From;
+  static constexpr int kUnits = From::kUnits;
+  static constexpr int kPitch = STRIDED ? T + 4 : kPad32;
+  static constexpr int kFloats = (STRIDED ? kDenseKF32 : T) * kPitch;
 
   static __device__ __forceinline__ void store(const uint4 (&u)[kUnits], float* lds) {
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
-      if constexpr (!STRIDED) {
-        const int t = threadIdx.x + k * 256;
-        *reinterpret_cast<uint4*>(lds + (t >> 3) * kPad32 + 4 * (t & 7)) = u[k];
-      } else {
-        float* p = lds + (32 * k + 4 * (threadIdx.x & 7)) * kPad32 + (threadIdx.x >> 3);
-        p[0] = __uint_as_float(u[k].x);
-        p[kPad32] = __uint_as_float(u[k].y);
-        p[2 * kPad32] = __uint_as_float(u[k].z);
-        p[3 * kPad32] = __uint_as_float(u[k].w);
-      }
+      int r, s;
+      From::place(k, r, s);
+      *reinterpret_cast<uint4*>(lds + r * kPitch + 4 * s) = u[k];
     }
   }
   template <bool PAIR>
   static __device__ __forceinline__ floatx4 fragment(const float* lds, int base, int q, int kk) {
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int row = base + (PAIR ? 8 * (r >> 2) + 4 * q + (r & 3) : 16 * q + r);
-    return *reinterpret_cast<const floatx4*>(lds + row * kPad32 + 16 * kk + 4 * g);
+    if constexpr (!STRIDED) {
+      return *reinterpret_cast<const floatx4*>(lds + row * kPitch + 16 * kk + 4 * g);
+    } else {
+      floatx4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = lds[(16 * kk + 4 * g + e) * kPitch + row];
+      return v;
+    }
   }
 };
 
 template <int TR, int TC>
-constexpr int gemm32_lds() { return 2 * (TR + TC) * kPad32 * 4; }
+constexpr int gemm32_lds() { return 2 * (TR + TC) * kPad32 * 4; }    // strided tiles take less
 
 template <int LAYOUT, int EPI, int TR, int TC>
 __device__ __forceinline__ void gemm32(const GemmArgs& a, int block, float* lds) {
@@ -78,8 +85,8 @@ __device__ __forceinline__ void gemm32(const GemmArgs& a, int block, float* lds)
   // into the other one from register set (t + 1 - t0) % 2 and the loads of tile
   // t + 3 leave for that set: the LDS writes and the second half's reads are
   // issued between the MFMAs, which take 32 cycles each.
-  Loader<4, TC, kDenseKF32, PS> from_p(a.p, a.ldp, j0, a.e.cols, t0 * kDenseKF32, a.len, half);
-  Loader<4, TR, kDenseKF32, QS> from_q(a.q, a.ldq, i0, a.e.rows, t0 * kDenseKF32, a.len, 0);
+  typename P::From from_p(a.p, a.ldp, j0, a.e.cols, t0 * kDenseKF32, a.len, half);
+  typename Q::From from_q(a.q, a.ldq, i0, a.e.rows, t0 * kDenseKF32, a.len, 0);
   uint4 up[2][P::kUnits], uq[2][Q::kUnits];
   auto load = [&](long t, int set) {
     if (t >= t1) return;
@@ -171,10 +178,8 @@ template <int LAYOUT, int EPI>
 hipError_t launch_epi(const GemmArgs& a, const GemmPlan& p, const UnpackJob& u, hipStream_t stream) {
   const dim3 grid((unsigned)(gemm_blocks(a) + u.blocks)), block(256);
   constexpr int SC = EPI == kEpiGated ? 128 : 64;
-  if (p.tile_r == 128)
-    hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 128, 128>), grid, block, 0, stream, a, u);
-  else
-    hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 64, SC>), grid, block, 0, stream, a, u);
+  if (p.tile_r != 64 || p.tile_c != SC) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 64, SC>), grid, block, 0, stream, a, u);
   return hipGetLastError();
 }
 
@@ -189,8 +194,8 @@ hipError_t launch_gemm32(const GemmArgs& a, const GemmPlan& p, int epi, const Un
 
 hipError_t launch_gemm32_group(const GemmGroup& g, const GemmPlan& p, hipStream_t stream) {
   const dim3 grid((unsigned)g.blocks), block(256);
-  if (p.tile_r == 128) hipLaunchKernelGGL(dense_gemm32_group<128>, grid, block, 0, stream, g);
-  else hipLaunchKernelGGL(dense_gemm32_group<64>, grid, block, 0, stream, g);
+  if (p.tile_r != 64) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(dense_gemm32_group<64>, grid, block, 0, stream, g);
   return hipGetLastError();
 }
 
