@@ -180,20 +180,24 @@ def _check(rc: int):
 
 def _p(t):
     """Device address of a tensor (or int / None)."""
-    try:
-        return t.data_ptr()
-    except AttributeError:
-        return t
+    return t if t is None or t.__class__ is int else t.data_ptr()
+
+
+_current_stream = None
 
 
 def _s(stream):
+    global _current_stream
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:   # a CPU-only torch, or one without it: the stream object, which costs 3 us to make
-            return torch.cuda.current_stream().cuda_stream
-        return raw(torch.cuda.current_device())
-    if isinstance(stream, int):
+        if _current_stream is None:
+            import torch
+            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            if raw is None:   # a torch without it: the stream object, which costs 3 us to make
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+            else:
+                _current_stream = lambda: raw(device())  # noqa: E731
+        return _current_stream()
+    if stream.__class__ is int:
         return stream
     return stream.cuda_stream
 
