@@ -65,7 +65,9 @@ __device__ __forceinline__ Eight load8(const void* p, long i, int n) {
   return r;
 }
 
-template <int DT>
+// STREAM: whole units are not kept in the caches (results of a size that the
+// next reader does not find there anyway).
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ void store8(void* p, long i, const Eight& r, int n) {
   typedef typename Storage<DT>::T T;
   T* s = static_cast<T*>(p) + i;
@@ -77,7 +79,12 @@ __device__ __forceinline__ void store8(void* p, long i, const Eight& r, int n) {
       T8 t;
 #pragma unroll
       for (int k = 0; k < 8; ++k) t[k] = (T)r.v[k];
-      __builtin_memcpy(s, &t, 16);
+      if constexpr (STREAM) {
+        typedef unsigned int u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, t), reinterpret_cast<u32x4*>(s));
+      } else {
+        __builtin_memcpy(s, &t, 16);
+      }
     }
   } else {
     // runs of four, two and one
@@ -372,7 +379,7 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
       store8<OIDN_F32>(e.part, ((long)slice * e.rows + i) * e.cols + j, x, n);
   } else if constexpr (EPI == kEpiStore) {
     if (e.res) add8(x, f.a.value());
-    if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
+    if (ok) store8<DT, WHOLE>(e.y, i * e.ldy + j, x, n);
   } else if constexpr (EPI == kEpiLinear) {
     add8(x, bias.a);
     if (e.z) {
@@ -385,7 +392,7 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
     }
     activate8<DT>(e.act, x);
     if (e.res) add8(x, f.a.value());
-    if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
+    if (ok) store8<DT, WHOLE>(e.y, i * e.ldy + j, x, n);
   } else if constexpr (EPI == kEpiGated) {
     add8(x, bias.a);
     add8(u, bias.b);
