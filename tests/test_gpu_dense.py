@@ -571,3 +571,21 @@ def test_narrow_linear_backward_of_many_rows(k, n, precision):
     check(dx.get(), want[0], precision, "dx")
     check(dw.get(), want[1], precision, "dw")
     check(db.get()[0], want[2], "f32", "dbias")
+
+
+@pytest.mark.parametrize("precision", ["f16", "bf16"])
+@pytest.mark.parametrize("m, k, n", [(8191, 65, 96), (8192, 65, 96), (8193, 128, 128), (16385, 112, 72),
+                                     (20001, 40, 64), (20001, 70, 64)])
+def test_narrow_linear_backward_around_its_limits(m, k, n, precision):
+    """Either side of the row count from which wide ones take one pass, of one and of two blocks a workgroup."""
+    dt, ty = DT[precision], TORCH[precision]
+    mk, kind = Maker(m + k * n, precision), "gelu"
+    x, w, dy, z = mk.rows(m, k, 3), mk.rows(n, k, 0, k ** -0.5), mk.rows(m, n, 8), mk.rows(m, n)
+    dx, dw, db = Out(m, k, ty, 1), Out(n, k, ty, 5), Out(1, n, torch.float32)
+    ws = bytes_(U.oidn_linear_backward_workspace_bytes(m, k, n, ACT[kind], dt, 0))
+    U.oidn_linear_backward(dy, dy.stride(0), x, x.stride(0), z, n, w, k, dx.view, dx.ld, dw.view, dw.ld, db.view, m, k, n,
+                           ACT[kind], dt, 0, ws, ws.numel())
+    want = linear_backward(given(dy), given(x), given(z), given(w), kind, precision)
+    check(dx.get(), want[0], precision, "dx")
+    check(dw.get(), want[1], precision, "dw")
+    check(db.get()[0], want[2], "f32", "dbias")

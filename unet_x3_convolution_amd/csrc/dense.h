@@ -193,9 +193,22 @@ struct NarrowArgs {
   int blocks;              // of 64 rows
   int act;
 };
-inline int narrow_grid(long rows) {
+// Whether a layer is narrow.  Where n and k are both over 64 the pass pays from
+// 8192 rows on (us, bf16, gelu, 128 x 128: 17 against 14 in separate launches at
+// 2040 rows, 20 against 19 at 8160, 26 against 26 at 16320, 54 against 114 at
+// 130560); narrower layers gain at any length (32 -> 64: 10 against 14 at 510
+// rows, 25 against 61 at 130560).
+inline bool narrow_layer(long rows, int n, int k) {
+  return n <= kNarrow && k <= kNarrow && (n <= 64 || k <= 64 || rows >= 8192);
+}
+// Workgroups: one per block while units are free for them, then 256 with at
+// least two blocks each, for a slice of dw less to write and add (64 x 64, 510
+// blocks: 15.9 us against 18.7 with 510), then 512 that hide each other's
+// barriers (2040 blocks: 26 against 27, 96 x 48 34 against 44).  128 x 128 takes
+// a unit's registers, so there 256 remain (54 against 64).
+inline int narrow_grid(long rows, int n, int k) {
   const long b = (rows + 63) / 64;
-  return (int)(b < 512 ? b : 512);
+  return (int)(b <= 256 ? b : b <= 512 || (n > 64 && k > 64) ? 256 : 512);
 }
 hipError_t launch_narrow_back(const NarrowArgs& a, int grid, bool bf16, hipStream_t stream);
 

@@ -276,9 +276,9 @@ struct LinearBack {
 };
 LinearBack linear_back(long m, int k, int n, int act, int dtype, unsigned flags, void* ws) {
   LinearBack b{};
-  if (dtype != OIDN_F32 && flags == 0 && n <= kNarrow && k <= kNarrow) {
+  if (dtype != OIDN_F32 && flags == 0 && narrow_layer(m, n, k)) {
     b.narrow = true;
-    const size_t grid = narrow_grid(m);
+    const size_t grid = narrow_grid(m, n, k);
     Regions r{static_cast<char*>(ws), 0};
     b.sums = r.take(align256(grid * n * sizeof(float)));
     b.dw_slices = grid > 1 ? r.take(align256(grid * n * k * sizeof(float))) : nullptr;
@@ -551,7 +551,7 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
   Gradients g{};
   g.dtype = dtype;
   if (b.narrow) {
-    const int grid = narrow_grid(m);
+    const int grid = narrow_grid(m, n, k);
     NarrowArgs a{};
     a.dy = dy;
     a.lddy = lddy;

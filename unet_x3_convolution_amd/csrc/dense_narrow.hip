@@ -43,8 +43,11 @@ struct Rows16 {
   }
 };
 
+// 128 x 128 needs more than the 256 registers that two workgroups a unit would
+// leave each thread: within them it spilled and took 98 us at 130560 rows, now 54.
 template <bool BF, int NP, int KP>
-__global__ __launch_bounds__(256, NP * KP > 64 * 64 ? 2 : 3) void narrow_back(NarrowArgs a) {
+__global__ __launch_bounds__(256, NP * KP == 128 * 128 ? 1 : NP * KP > 64 * 64 ? 2 : 3)
+void narrow_back(NarrowArgs a) {
   constexpr int DT = BF ? OIDN_BF16 : OIDN_F16;
   constexpr int FC = KP / 32;              // column fragments of a wave, of dx and of dw
   constexpr int FN = NP / 32;              // row fragments of a wave's dw
