@@ -589,3 +589,16 @@ def test_narrow_linear_backward_around_its_limits(m, k, n, precision):
     check(dx.get(), want[0], precision, "dx")
     check(dw.get(), want[1], precision, "dw")
     check(db.get()[0], want[2], "f32", "dbias")
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("m, k, n", [(2, 264, 4096), (3, 264, 4095), (3, 267, 4096), (4, 1032, 4099), (4, 72, 4090), (5, 72, 4096)])
+def test_few_rows_of_many_columns(m, k, n, precision):
+    """Either side of the column and row counts between the two kernels of few rows."""
+    mk, kind = Maker(m + k + n, precision), "silu"
+    x, w, bias, r = mk.rows(m, k, 3), mk.rows(n, k, 0, k ** -0.5), mk.vec(n), mk.rows(m, n, 1)
+    z = Out(m, n, TORCH[precision], 5)
+    y = run_linear(x, w, bias, r, kind, precision, z, pad=3, shift=1)
+    want, want_z = linear(given(x), given(w), given(bias), given(r), kind)
+    check(y.get(), want, precision, "y")
+    check(z.get(), want_z, precision, "z")

@@ -28,7 +28,15 @@ template <int DT>
 hipError_t launch_type(const GemmArgs& a, int epi, hipStream_t stream) {
   // 16 columns a workgroup, unless an 8-bit block of 32 has to be in one
   const bool block32 = a.e.z && a.e.z8;
-  if (a.e.rows <= 4 && !block32) {
+  // Dot instructions, or matrix fragments (us a call, weights cold).  One and two
+  // rows: dots (bf16 4096 -> 4096 7.6 against 8.4).  Three and four: a plain
+  // product's dots read four rows of x for one of w, and where the fragments'
+  // workgroups of 16 columns fill the 256 units they are ahead (bf16 4096 -> 4096
+  // 8.8 against 11.5, fp32 2048 -> 8192 15.1 against 20.6), else not (bf16 5632 ->
+  // 2048 10.7 against 8.6).  A gated product reads two rows of w with them: dots
+  // (block of 2048 x 5632 21.5 against 25.6).
+  const bool wide = epi == kEpiLinear && a.e.cols >= 16 * 256;
+  if (a.e.rows <= (wide ? 2 : 4) && !block32) {
     if (epi == kEpiLinear) return launch_dot<DT, kEpiLinear>(a, stream);
     if (epi == kEpiGated) return launch_dot<DT, kEpiGated>(a, stream);
   }
