@@ -602,3 +602,21 @@ def test_few_rows_of_many_columns(m, k, n, precision):
     want, want_z = linear(given(x), given(w), given(bias), given(r), kind)
     check(y.get(), want, precision, "y")
     check(z.get(), want_z, precision, "z")
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("m, k, n", [(33, 64, 64), (95, 67, 63), (97, 515, 300), (512, 512, 520), (1021, 128, 771),
+                                     (2041, 112, 97)])
+def test_linear_of_few_tiles(m, k, n, precision):
+    """Rows that end inside 32-row and 64-row tiles, sums without and with slices, z in both forms."""
+    mk, kind = Maker(m + 3 * k + n, precision), "gelu"
+    x, w, bias, r = mk.rows(m, k, 1), mk.rows(n, k, 0, k ** -0.5), mk.vec(n), mk.rows(m, n, 3)
+    z = Out(m, n, TORCH[precision], 2)
+    y = run_linear(x, w, bias, r, kind, precision, z, pad=1)
+    want, want_z = linear(given(x), given(w), given(bias), given(r), kind)
+    check(y.get(), want, precision, "y")
+    check(z.get(), want_z, precision, "z")
+    kept = bytes_(U.oidn_ckpt_bytes(m, n))
+    y8 = run_linear(x, w, bias, r, kind, precision, kept, U.OIDN_Z_CKPT8, pad=1)
+    assert torch.equal(y8.get(), y.get())
+    check_codes(kept, want_z, m, n, "z in 8 bits")

@@ -377,18 +377,19 @@ namespace oidn {
 // that is, a start, a cost per tile, and per staged tile the larger of a
 // workgroup's own pace and its share of the compute unit's.  fp32 tiles (64 x
 // 64) hold half as many summed elements and take 0.8 us alone, 0.53 us of a
-// full unit.  Summing slices costs a launch and moves their bytes twice.
+// full unit; 32 x 64 ones, for a lone plain product, give two workgroups to a unit
+// that would hold one.  Summing slices costs a launch and moves their bytes twice.
 struct TileCost { long tile; double start, each, own, share; };
 constexpr TileCost kCost16[] = {{64, 2.8, 0.7, 0.27, 0.17}, {128, 3.4, 2.9, 0.49, 0.40}, {256, 6.5, 9.0, 1.35, 1.40}};
 constexpr TileCost kCostGated = {64, 2.8, 1.3, 0.35, 0.30};      // a gated product's 64 x 128
-constexpr TileCost kCost32[] = {{64, 3.5, 1.0, 0.80, 0.53}};
+constexpr TileCost kCost32[] = {{64, 3.5, 1.0, 0.80, 0.53}, {32, 3.0, 0.7, 0.50, 0.30}};
 constexpr long kMaxSlices = 256;
 constexpr double kCus = 256, kSliceLaunch = 3.0, kSliceBytesPerUs = 4e6;
 
 void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, int dtype, bool direct) {
   const long bk = dtype == OIDN_F32 ? kDenseKF32 : kDenseK;
   const TileCost* const table = dtype == OIDN_F32 ? kCost32 : kCost16;
-  const int choices = dtype == OIDN_F32 ? 1 : direct ? 3 : 2;
+  const int choices = dtype == OIDN_F32 ? (shapes[0].epi == kEpiLinear ? 2 : 1) : direct ? 3 : 2;
   double best = 0;
   for (int c = 0; c < choices; ++c) {
     const TileCost t = shapes[0].epi == kEpiGated && table[c].tile == 64 ? kCostGated : table[c];
@@ -396,7 +397,7 @@ void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, i
     for (int k = 0; k < count; ++k) {
       const PlanShape& s = shapes[k];
       // a gated tile holds half its columns of each projection, 64 at least
-      const long tc = s.epi == kEpiGated ? (t.tile < 128 ? 64 : t.tile / 2) : t.tile;
+      const long tc = s.epi == kEpiGated ? (t.tile < 128 ? 64 : t.tile / 2) : t.tile < 64 ? 64 : t.tile;
       tiles[k] = ((s.rows + t.tile - 1) / t.tile) * ((s.cols + tc - 1) / tc);
       kt[k] = (s.len + bk - 1) / bk;
       if (kt[k] > longest) longest = kt[k];
@@ -408,7 +409,7 @@ void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, i
       for (int k = 0; k < count; ++k) {
         const PlanShape& s = shapes[k];
         GemmPlan& p = tried[k];
-        p = GemmPlan{(int)t.tile, s.epi == kEpiGated && t.tile < 128 ? 128 : (int)t.tile, false, false, 1, kt[k]};
+        p = GemmPlan{(int)t.tile, s.epi == kEpiGated && t.tile < 128 ? 128 : t.tile < 64 ? 64 : (int)t.tile, false, false, 1, kt[k]};
         if ((s.epi == kEpiLinear || s.epi == kEpiStore) && kt[k] > cap && cap >= 2) {
           long n = (kt[k] + cap - 1) / cap;
           if (n > kMaxSlices) n = kMaxSlices;

@@ -3,7 +3,11 @@
 //
 // Tiles of C are 64 x 64 (gated: 64 x 128), several to a compute unit: 4096 x
 // 4096 x 1024 runs at 120 TFLOP/s, 128 x 128 tiles at 105, one or two to a unit
-// with their registers full.
+// with their registers full.  Plain forward products of few tiles take 32 x 64,
+// whose second workgroup on a unit works while the first one waits (us a call,
+// gelu and residual, 64 x 64 against 32 x 64): 2040 x 112 -> 96 8.0 and 6.0, 510
+// x 128 -> 512 7.4 and 5.7, 1021 x 515 -> 771 19.1 and 18.2; with many tiles the
+// larger ones' fewer loads win: 4096 x 1024 -> 4096 293 and 322.
 //
 // 32 summed elements are staged at a time through registers into one of two
 // LDS buffers, two or three tiles ahead, as rows of 32 + 4 floats: the pad puts
@@ -178,6 +182,12 @@ template <int LAYOUT, int EPI>
 hipError_t launch_epi(const GemmArgs& a, const GemmPlan& p, const UnpackJob& u, hipStream_t stream) {
   const dim3 grid((unsigned)(gemm_blocks(a) + u.blocks)), block(256);
   constexpr int SC = EPI == kEpiGated ? 128 : 64;
+  if constexpr (EPI == kEpiLinear) {
+    if (p.tile_r == 32 && p.tile_c == 64) {
+      hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 32, 64>), grid, block, 0, stream, a, u);
+      return hipGetLastError();
+    }
+  }
   if (p.tile_r != 64 || p.tile_c != SC) return hipErrorInvalidValue;
   hipLaunchKernelGGL((dense_gemm32<LAYOUT, EPI, 64, SC>), grid, block, 0, stream, a, u);
   return hipGetLastError();
