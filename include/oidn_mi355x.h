@@ -399,7 +399,8 @@ int oidn_unet_forward_timed(const void* d_weights, int in_channels, const float*
  * Layout of an m x n checkpoint: m rows of int8 codes, padded to whole blocks
  * (padding holds 0), then one bf16 scale per row and block.  Blocks with
  * s < 2^-120 are stored as zeros; a block with an infinity or a NaN reads back
- * as NaN.  The buffer is 16-byte aligned. */
+ * as NaN.  A finite value of a 16-bit type reads back finite in it: one that the
+ * rounding of s carries past the range becomes the largest.  The buffer is 16-byte aligned. */
 int oidn_ckpt_bytes(long m, long n, size_t* bytes);
 int oidn_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
                    hipStream_t stream);

@@ -35,3 +35,52 @@ def test_gradients_of_the_narrowest_layers(m, k, n, precision):
     check(dx, want[0], precision, "dx")
     check(dw, want[1], precision, "dw")
     check(db, want[2], "f32", "dbias")
+
+
+def last_values(precision):
+    """Blocks whose largest magnitudes are the type's last finite values, a few steps below, and of both signs."""
+    top = torch.tensor(torch.finfo(TORCH[precision]).max, dtype=torch.float64)
+    down = torch.linspace(0, 0.01, 33, dtype=torch.float64).view(-1, 1)
+    x = (top * (1 - down)).repeat(1, 64)
+    x[:, 1::3] *= -1
+    x[:, 2::3] *= 0.25
+    return x.to(TORCH[precision])
+
+
+@pytest.mark.parametrize("precision", ["f32", "f16", "bf16"])
+def test_checkpoints_of_the_largest_values_stay_finite(precision):
+    """A finite value reads back within half a step of its block's scale, and a step is max / 127 and its rounding."""
+    x = last_values(precision)
+    m, n = x.shape
+    blob, y = bytes_(U.oidn_ckpt_bytes(m, n)), torch.empty_like(x, device="cuda")
+    U.oidn_ckpt_pack(x.cuda(), n, m, n, blob, DT[precision])
+    U.oidn_ckpt_unpack(blob, m, n, y, n, DT[precision])
+    y, x = y.cpu().double(), x.double()
+    assert y.isfinite().all()
+    step = x.abs().amax(1, keepdim=True) / 127 * (1 + 2.0 ** -8)
+    assert ((y - x).abs() <= (0.5 + 2.0 ** -14) * step + torch.finfo(TORCH[precision]).eps / 2 * x.abs()).all()
+
+
+@pytest.mark.parametrize("precision", ["f32", "f16", "bf16"])
+def test_weight_gradients_from_checkpoints_of_the_largest_values(precision):
+    """x from 8 bits beside the slope pass and beside the block's backward product: one row in, so dw is x scaled."""
+    ty, dt = TORCH[precision], DT[precision]
+    x = last_values(precision)[:1]
+    n = x.shape[1]
+    x8 = bytes_(U.oidn_ckpt_bytes(1, n))
+    U.oidn_ckpt_pack(x.cuda(), n, 1, n, x8, dt)
+    small = torch.full((1, 1), 2.0 ** -12, dtype=ty, device="cuda")
+    one, dw = torch.ones(1, 1, dtype=ty, device="cuda"), torch.empty(1, n, dtype=ty, device="cuda")
+    ws = bytes_(U.oidn_linear_backward_workspace_bytes(1, n, 1, U.OIDN_ACT_RELU, dt, U.OIDN_X_CKPT8))
+    U.oidn_linear_backward(small, 1, x8, 0, one, 1, None, n, None, n, dw, n, None, 1, n, 1, U.OIDN_ACT_RELU, dt,
+                           U.OIDN_X_CKPT8, ws, ws.numel())
+    want, bound = x.double() * 2.0 ** -12, x.double().abs().max() * 2.0 ** -12 / 127
+    assert ((dw.cpu().double() - want).abs() <= bound).all()
+    dy = torch.zeros(1, n, dtype=ty, device="cuda")
+    dy[0, 0] = 2.0 ** -12
+    z, w_out = torch.ones(1, 2, dtype=ty, device="cuda"), torch.ones(n, 1, dtype=ty, device="cuda")
+    dw_in = torch.empty(2, n, dtype=ty, device="cuda")
+    ws = bytes_(U.oidn_ffn_backward_workspace_bytes(1, n, 1, dt, U.OIDN_X_CKPT8))
+    U.oidn_ffn_backward(dy, n, x8, 0, z, None, w_out, None, 0, None, n, dw_in, None, None, None, 1, n, 1,
+                        U.OIDN_ACT_RELU, dt, U.OIDN_X_CKPT8, ws, ws.numel())
+    assert ((dw_in.cpu().double() - want).abs() <= bound).all()

@@ -345,6 +345,23 @@ __device__ __forceinline__ RawCodes load_codes(const CkptAt& c, long i, int j) {
 
 __device__ __forceinline__ Eight ckpt_load8(const CkptAt& c, long i, int j) { return load_codes(c, i, j).value(); }
 
+// Values that go back to type DT.  The rounding of a block's scale can carry its
+// largest value past the type's range (fp16: 127 x 516 = 65532); up to the scale
+// that the type's largest value gets, such a value is that largest one, beyond
+// (sums that were kept in 8 bits) it is infinite.  NaN, the scale of a block with
+// no finite maximum, stays.  In fp32 127 times the largest scale is finite.
+template <int DT>
+__device__ __forceinline__ Eight ckpt_stored(const RawCodes& c) {
+  Eight r = c.value();
+  if constexpr (DT != OIDN_F32) {
+    const float top = DT == OIDN_F16 ? 0x1.02p9f : 0x1.02p121f, most = DT == OIDN_F16 ? 65504.f : 0x1.fep127f;
+    const float s = (float)c.s, limit = s <= top ? most : s * __builtin_inff();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r.v[k] = __builtin_amdgcn_fmed3f(r.v[k], -limit, limit);
+  }
+  return r;
+}
+
 template <int DT, int EPI, bool WHOLE, bool Z8>
 __device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, RawFetched<DT, Z8>& f) {
   if constexpr (EPI == kEpiPartial || EPI == kEpiGated) return;

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kRowThreads) void ckpt_unpack(void* ckpt, long m, l
   const long i = t / units, j = (t - i * units) * 8;
   const int left = n - j < 8 ? (int)(n - j) : 8;
   if (t >= total || left <= 0) return;
-  store8<DT>(y, i * ldy + j, ckpt_load8(ckpt_at(ckpt, m, n), i, (int)j), left);
+  store8<DT>(y, i * ldy + j, ckpt_stored<DT>(load_codes(ckpt_at(ckpt, m, n), i, (int)j)), left);
 }
 
 __global__ __launch_bounds__(kRowThreads) void zero_bytes(unsigned char* p, size_t n) {

@@ -80,7 +80,7 @@ __device__ __forceinline__ void unpack_rows(const UnpackJob& u, int block) {
   for (int k = 0; k < kUnpackRun; ++k) {
     const long t = ((long)block * kUnpackRun + k) * kRowThreads + threadIdx.x, i = t / units;
     const int j = (int)(t - i * units) * 8;
-    if (t < total) store8<DT>(u.y, i * u.n + j, got[k].value(), u.n - j);
+    if (t < total) store8<DT>(u.y, i * u.n + j, ckpt_stored<DT>(got[k]), u.n - j);
   }
 }
 
