@@ -1,10 +1,12 @@
 """Dense operators at their edges: the narrowest operands, whose 16-byte loads
 span several rows, as dense as they can lie."""
+import math
+
 import pytest
 import torch
 
 import unet_x3_convolution_amd as U
-from dense_reference import TORCH, check, given, linear_backward
+from dense_reference import HALF, TINY, TORCH, check, given, linear_backward
 from helpers import DT, torch_cuda
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +86,32 @@ def test_weight_gradients_from_checkpoints_of_the_largest_values(precision):
     U.oidn_ffn_backward(dy, n, x8, 0, z, None, w_out, None, 0, None, n, dw_in, None, None, None, 1, n, 1,
                         U.OIDN_ACT_RELU, dt, U.OIDN_X_CKPT8, ws, ws.numel())
     assert ((dw_in.cpu().double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("precision", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_activations_keep_their_relative_accuracy_where_they_vanish(kind, precision):
+    """act(z) and act'(z) of negative z against 64 bits, off by a part of their own magnitude: fp32 by the exponential's
+    argument (half a step of z^2 / 2 or of z, twice) and 16 units of erfc, the 16-bit gelu by its formula (2^-15, and
+    2^-11 past the range of fp16); then the output's rounding."""
+    ty, dt, act = TORCH[precision], DT[precision], U.OIDN_ACT_GELU if kind == "gelu" else U.OIDN_ACT_SILU
+    x = (-torch.linspace(0, 13 if kind == "gelu" else 80, 5003)).to(ty).cuda().view(-1, 1)
+    m, one = x.shape[0], torch.ones(1, 1, dtype=ty, device="cuda")
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    ws = bytes_(max(U.oidn_linear_workspace_bytes(m, 1, 1, dt), U.oidn_linear_backward_workspace_bytes(m, 1, 1, act, dt, 0)))
+    U.oidn_linear(x, 1, one, 1, None, None, 0, y, 1, None, 0, m, 1, 1, act, dt, 0, ws, ws.numel())
+    U.oidn_linear_backward(torch.ones_like(x), 1, x, 1, x, 1, one, 1, dx, 1, None, 1, None, m, 1, 1, act, dt, 0, ws, ws.numel())
+    z = x.cpu().double()
+    if kind == "gelu":
+        p, d = torch.special.erfc(-z / math.sqrt(2)) / 2, torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        part = 2.0 ** -19 + z * z * 2.0 ** -22
+        if precision != "f32":
+            part = part + torch.where(z > -5.75, 2.0 ** -15, 2.0 ** -11)
+    else:
+        p = 1 / (1 + torch.exp(-z))
+        d, part = p * (1 - p), 2.0 ** -20 - z * 2.0 ** -22
+    for got, want, size in ((y, z * p, z.abs() * p), (dx, p + z * d, p + z.abs() * d)):
+        bound = part * size
+        bound = bound + HALF[precision] * (want.abs() + bound) + TINY[precision]
+        bad = ~((got.cpu().double() - want).abs() <= bound)
+        assert not bad.any(), (int(bad.sum()), float(z[bad][0]), float(got.cpu()[bad][0]), float(want[bad][0]))
