@@ -180,7 +180,7 @@ def _check(rc: int):
 
 def _p(t):
     """Device address of a tensor (or int / None)."""
-    return t if t is None or t.__class__ is int else t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 _current_stream = None
@@ -197,7 +197,7 @@ def _s(stream):
             else:
                 _current_stream = lambda: raw(device())  # noqa: E731
         return _current_stream()
-    if stream.__class__ is int:
+    if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
