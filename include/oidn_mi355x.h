@@ -386,7 +386,9 @@ int oidn_unet_forward_timed(const void* d_weights, int in_channels, const float*
  * are 0, nothing else is written).  Outputs must not overlap inputs, except
  * that `residual` may be y and `add` may be dx (same pitch).  Columns between
  * a row's end and its pitch are neither read nor written.  Column counts
- * above 2^24 and matrices above 2^38 elements: OIDN_E_UNSUPPORTED.
+ * above 2^24, matrices above 2^38 elements and products of more tiles than a
+ * launch holds (about 2^24; of 64 x 64 where a side is short):
+ * OIDN_E_UNSUPPORTED.
  *
  * The workspace (16-byte aligned, the size the matching *_workspace_bytes
  * call gives) holds nothing between calls.

@@ -115,3 +115,21 @@ def test_activations_keep_their_relative_accuracy_where_they_vanish(kind, precis
         bound = bound + HALF[precision] * (want.abs() + bound) + TINY[precision]
         bad = ~((got.cpu().double() - want).abs() <= bound)
         assert not bad.any(), (int(bad.sum()), float(z[bad][0]), float(got.cpu()[bad][0]), float(want[bad][0]))
+
+
+def test_checkpoint_of_more_units_than_a_launch_has_threads():
+    """2^30 rows of one column take 2^32 units of eight codes.  Each value is its block's largest: q = +-127."""
+    m, part = 2 ** 30 + 3, 2 ** 27
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, y = torch.empty(m, 1, dtype=torch.float16, device="cuda"), torch.full((m, 1), float("nan"), dtype=torch.float16, device="cuda")
+    for i in range(0, m, part):
+        x[i:i + part].normal_(generator=g)
+    blob = bytes_(U.oidn_ckpt_bytes(m, 1))
+    U.oidn_ckpt_pack(x, 1, m, 1, blob, U.OIDN_F16)
+    U.oidn_ckpt_unpack(blob, m, 1, y, 1, U.OIDN_F16)
+    del blob
+    for i in range(0, m, part):
+        a, b = x[i:i + part].float(), y[i:i + part].float()
+        step = a.abs() / 127 * (1 + 2.0 ** -8)
+        assert ((b - a).abs() <= (0.5 + 2.0 ** -13) * step + a.abs() * 2.0 ** -11 + 2.0 ** -25).all()
+    torch.cuda.empty_cache()

@@ -90,9 +90,10 @@ constexpr int kMinTile = 64;
 
 // Workgroups of a product: its tiles, rounded up so that every slice starts on
 // the first XCD, times its slices.
-inline long gemm_blocks(const GemmArgs& a) {
-  return ((long)a.tiles_r * a.tiles_c + 7) / 8 * 8 * a.splits;
-}
+inline long gemm_blocks(long tiles_r, long tiles_c, int splits) { return (tiles_r * tiles_c + 7) / 8 * 8 * splits; }
+inline long gemm_blocks(const GemmArgs& a) { return gemm_blocks(a.tiles_r, a.tiles_c, a.splits); }
+// A launch holds less than 2^32 work items, here in workgroups of 256.
+constexpr long kMaxWorkgroups = 0xffffffffL / 256;
 
 // dz = dy * act'(z) (dz may be null: column sums alone; act none: z unused)
 // and, with part, partial column sums of dz over `chunk` rows: part[r / chunk][n].
@@ -163,6 +164,10 @@ struct FinishArgs {
   struct { const float* part; long groups; int cols; float* out; } column[2];
 };
 hipError_t launch_finish(const FinishArgs& a, int dtype, hipStream_t stream);
+
+// Workgroups that the sum of a product's slices takes, and that of partial columns.
+long slice_blocks(long rows, int cols, int splits);
+long column_blocks(long groups, int cols);
 
 long slope_chunk(long rows);
 int slope_lanes(int cols);

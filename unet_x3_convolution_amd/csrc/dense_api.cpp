@@ -1,6 +1,7 @@
 // Host side of the dense operators' C ABI: argument checks, launch plans,
 // workspace layout and the launch sequences.  Nothing here allocates device
 // memory, waits for the device or throws.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 
@@ -23,8 +24,9 @@ int ran(hipError_t e, const char* what) {
   return e == hipSuccess ? OIDN_OK : fail(OIDN_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-// Limits: columns index with 32-bit ints, and tiles and 8-column units of one
-// matrix have to fit a launch's grid.
+// Limits: columns index with 32-bit ints, rows count with them where tiles do.
+// Whether a call's products fit a launch's grid is a matter of its plan
+// (check_launch).
 constexpr long kMaxColumns = 1L << 24;
 constexpr long kMaxRows = (1L << 31) - 1;
 constexpr long kMaxElements = 1L << 38;
@@ -118,6 +120,30 @@ Product product(int layout, int epi, long rows, long cols, long len, int dtype) 
 }
 size_t product_bytes(const Product& p) {
   return p.plan.splits > 1 ? align256((size_t)p.plan.splits * p.rows * p.cols * sizeof(float)) : 0;
+}
+// Workgroups of a product's launch at most: where operands cannot go straight to
+// LDS, the largest tiles give way to the next smaller ones.
+long most_blocks(const Product& p) {
+  if (p.plan.few) return 0;
+  const bool staged = p.dtype != OIDN_F32 && p.plan.tile_r > 128;
+  const long r = staged ? 128 : p.plan.tile_r, t = staged ? 128 : p.plan.tile_c, c = p.epi == kEpiGated ? t / 2 : t;
+  return gemm_blocks((p.rows + r - 1) / r, (p.cols + c - 1) / c, p.plan.splits);
+}
+long sum_blocks(const Product& p) {
+  return p.plan.splits > 1 ? slice_blocks(p.rows, (int)p.cols, p.plan.splits) : 0;
+}
+long slope_blocks(long rows, int cols, long chunk) {
+  SlopeArgs s{};
+  s.rows = rows;
+  s.cols = cols;
+  s.chunk = chunk;
+  s.lanes = slope_lanes(cols);
+  return slope_blocks(s);
+}
+// `blocks`: of the largest launch of a call.
+int check_launch(long blocks) {
+  if (blocks <= kMaxWorkgroups) return OIDN_OK;
+  return fail(OIDN_E_UNSUPPORTED, "%ld workgroups are more than the %ld of a launch", blocks, kMaxWorkgroups);
 }
 // Whether a 16-bit operand can go straight to LDS in 16-byte units: `extent`
 // is what its rows hold of (the summed length, or the output's rows or columns
@@ -313,6 +339,7 @@ struct Ffn {
   Product in, out;
   void *h, *slices;
   size_t bytes;
+  long launch;             // workgroups of the largest launch, at most
 };
 Ffn ffn_plan(long m, int d, int f, int dtype, void* ws) {
   Ffn p{};
@@ -322,6 +349,7 @@ Ffn ffn_plan(long m, int d, int f, int dtype, void* ws) {
   p.h = r.take(bytes_of(m, f, dtype));
   p.slices = r.take(product_bytes(p.out));
   p.bytes = r.used;
+  p.launch = std::max({most_blocks(p.in), most_blocks(p.out), sum_blocks(p.out)});
   return p;
 }
 
@@ -475,7 +503,12 @@ int oidn_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ldy, int dt
 int oidn_linear_workspace_bytes(long m, int k, int n, int dtype, size_t* bytes) {
   if (!bytes) return fail(OIDN_E_INVALID, "null bytes pointer");
   OIDN_TRY(check_linear(m, k, n, dtype));
-  *bytes = m ? product_bytes(product(kForward, kEpiLinear, m, n, k, dtype)) : 0;
+  *bytes = 0;
+  if (m) {
+    const Product p = product(kForward, kEpiLinear, m, n, k, dtype);
+    OIDN_TRY(check_launch(std::max(most_blocks(p), sum_blocks(p))));
+    *bytes = product_bytes(p);
+  }
   return clear_error();
 }
 
@@ -496,6 +529,7 @@ int oidn_linear(const void* x, long ldx, const void* w, long ldw, const float* b
   if (z8) OIDN_TRY(check_blob("z", z));
   else OIDN_TRY(check_matrix("z", z, ldz, n, dtype, true));
   const Product p = product(kForward, kEpiLinear, m, n, k, dtype);
+  OIDN_TRY(check_launch(std::max(most_blocks(p), sum_blocks(p))));
   OIDN_TRY(check_workspace(workspace, ws_bytes, product_bytes(p)));
   EpilogueArgs e = store_to(y, ldy, residual, ldr);
   e.bias = bias;
@@ -547,6 +581,12 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
   if (dx) OIDN_TRY(check_matrix("w", w, ldw, k, dtype, false));
   OIDN_TRY(check_matrix("dx", dx, lddx, k, dtype, true));
   LinearBack b = linear_back(m, k, n, act, dtype, flags, workspace);
+  const UnpackJob job = dw && x8 && slope ? unpack_job(x, m, k, b.x) : UnpackJob{};
+  if (!b.narrow) {
+    const long pass = slope_blocks(m, n, b.chunk);
+    OIDN_TRY(check_launch(std::max({job.blocks + pass, (dx ? most_blocks(b.dx) : 0) + (dw ? most_blocks(b.dw) : 0) + pass,
+                                    sum_blocks(b.dx) + sum_blocks(b.dw) + column_blocks(b.chunks, n)})));
+  }
   OIDN_TRY(check_workspace(workspace, ws_bytes, b.bytes));
 
   Gradients g{};
@@ -601,7 +641,6 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
     s.chunk = b.chunk;
     s.lanes = slope_lanes(n);
     s.act = act;
-    const UnpackJob job = dw && x8 ? unpack_job(x, m, k, b.x) : UnpackJob{};
     OIDN_TRY(ran(launch_slope(s, job, dtype, stream), "slope pass launch"));
     if (dbias && b.chunks > 1) g.add_columns(b.sums, b.chunks, n, dbias);
   } else if (dbias) {
@@ -626,7 +665,12 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
 int oidn_ffn_workspace_bytes(long m, int d, int f, int dtype, size_t* bytes) {
   if (!bytes) return fail(OIDN_E_INVALID, "null bytes pointer");
   OIDN_TRY(check_ffn(m, d, f, dtype));
-  *bytes = m ? ffn_plan(m, d, f, dtype, nullptr).bytes : 0;
+  *bytes = 0;
+  if (m) {
+    const Ffn b = ffn_plan(m, d, f, dtype, nullptr);
+    OIDN_TRY(check_launch(b.launch));
+    *bytes = b.bytes;
+  }
   return clear_error();
 }
 
@@ -649,6 +693,7 @@ int oidn_ffn(const void* x, long ldx, const void* w_in, const float* b_in, const
   if (z8) OIDN_TRY(check_blob("z", z));
   else OIDN_TRY(check_matrix("z", z, 2L * f, 2L * f, dtype, true));
   const Ffn p = ffn_plan(m, d, f, dtype, workspace);
+  OIDN_TRY(check_launch(p.launch));
   OIDN_TRY(check_workspace(workspace, ws_bytes, p.bytes));
 
   EpilogueArgs e = store_to(p.h, f, nullptr, 0);
@@ -709,6 +754,12 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
   OIDN_TRY(check_matrix("dx", dx, lddx, d, dtype, true));
   OIDN_TRY(check_matrix("add", add, ldadd, d, dtype, true));
   const FfnBack b = ffn_back(m, d, f, dtype, flags, workspace);
+  const UnpackJob job = dw_in && x8 ? unpack_job(x, m, d, b.x) : UnpackJob{};
+  OIDN_TRY(check_launch(std::max({(inner ? most_blocks(b.dh) : 0) + job.blocks,
+                                  (dx ? most_blocks(b.dx) : 0) + (dw_in ? most_blocks(b.dw_in) : 0) +
+                                      (dw_out ? most_blocks(b.dw_out) : 0) + slope_blocks(m, d, b.chunk),
+                                  sum_blocks(b.dx) + sum_blocks(b.dw_in) + sum_blocks(b.dw_out) +
+                                      column_blocks(b.groups, 2 * f) + column_blocks(b.chunks, d)})));
   OIDN_TRY(check_workspace(workspace, ws_bytes, b.bytes));
 
   const long f2 = 2L * f;
@@ -725,7 +776,6 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
     e.act = act;
     e.part = db_in ? static_cast<float*>(b.in_sums) : nullptr;
     long groups = 0;
-    const UnpackJob job = dw_in && x8 ? unpack_job(x, m, d, b.x) : UnpackJob{};
     OIDN_TRY(run_product(b.dh, dy, lddy, w_out, f, e, nullptr, stream, &groups, job));
     if (db_in) g.add_columns(e.part, groups, (int)f2, db_in);
   }

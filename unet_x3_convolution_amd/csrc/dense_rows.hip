@@ -48,10 +48,6 @@ int slice_lanes(int splits) {
   while (lg < 5 && (8 << lg) <= splits) ++lg;
   return lg;
 }
-long slice_blocks(const EpilogueArgs& e, int splits) {
-  const long per = kRowThreads >> slice_lanes(splits);
-  return (e.rows * ((e.cols + 31) / 32 * 4) + per - 1) / per;
-}
 
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void split_sum(EpilogueArgs e, int splits, int lg) {
@@ -105,11 +101,21 @@ __global__ __launch_bounds__(kRowThreads) void slope_pass(SlopeArgs a, UnpackJob
   else slope_rows<DT>(a, blockIdx.x - u.blocks, lds);
 }
 
+// Thread of a launch over `row_grid`: one dimension, or two where a matrix has more
+// units than the work items that one holds.
+__device__ __forceinline__ long unit_index() {
+  return ((long)blockIdx.y * gridDim.x + blockIdx.x) * kRowThreads + threadIdx.x;
+}
+dim3 row_grid(long units) {
+  const long blocks = (units + kRowThreads - 1) / kRowThreads, most = 1L << 23;
+  return blocks <= most ? dim3((unsigned)blocks) : dim3((unsigned)most, (unsigned)((blocks + most - 1) / most));
+}
+
 // A thread codes eight columns; four neighbouring lanes hold a block.
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void ckpt_pack(const void* __restrict__ x, long ldx, long m,
                                                          long n, void* ckpt, long units, long total) {
-  const long t = (long)blockIdx.x * kRowThreads + threadIdx.x;
+  const long t = unit_index();
   const long i = t / units, j = (t - i * units) * 8;
   Eight v{};
   const int left = n - j < 8 ? (int)(n - j) : 8;
@@ -120,7 +126,7 @@ __global__ __launch_bounds__(kRowThreads) void ckpt_pack(const void* __restrict_
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void ckpt_unpack(void* ckpt, long m, long n, void* __restrict__ y,
                                                            long ldy, long units, long total) {
-  const long t = (long)blockIdx.x * kRowThreads + threadIdx.x;
+  const long t = unit_index();
   const long i = t / units, j = (t - i * units) * 8;
   const int left = n - j < 8 ? (int)(n - j) : 8;
   if (t >= total || left <= 0) return;
@@ -132,13 +138,20 @@ __global__ __launch_bounds__(kRowThreads) void zero_bytes(unsigned char* p, size
   for (size_t i = (size_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += step) p[i] = 0;
 }
 
-unsigned blocks_of(long n) { return (unsigned)((n + kRowThreads - 1) / kRowThreads); }
-
 }  // namespace
+
+long slice_blocks(long rows, int cols, int splits) {
+  const long per = kRowThreads >> slice_lanes(splits);
+  return (rows * ((cols + 31) / 32 * 4) + per - 1) / per;
+}
+long column_blocks(long groups, int cols) {
+  const int across = kRowThreads / column_lanes(groups);
+  return (cols + across - 1) / across;
+}
 
 hipError_t launch_split_sum(const EpilogueArgs& e, int splits, int dtype, hipStream_t stream) {
   const int lg = slice_lanes(splits);
-  const dim3 grid((unsigned)slice_blocks(e, splits)), block(kRowThreads);
+  const dim3 grid((unsigned)slice_blocks(e.rows, e.cols, splits)), block(kRowThreads);
   if (dtype == OIDN_F32) hipLaunchKernelGGL(split_sum<OIDN_F32>, grid, block, 0, stream, e, splits, lg);
   else if (dtype == OIDN_F16) hipLaunchKernelGGL(split_sum<OIDN_F16>, grid, block, 0, stream, e, splits, lg);
   else hipLaunchKernelGGL(split_sum<OIDN_BF16>, grid, block, 0, stream, e, splits, lg);
@@ -149,13 +162,13 @@ hipError_t launch_finish(const FinishArgs& a, int dtype, hipStream_t stream) {
   FinishPlan p{};
   int k = 0;
   for (; k < a.products; ++k) {
-    p.lg[k] = slice_lanes(a.product[k].splits);
-    p.start[k + 1] = p.start[k] + (int)slice_blocks(a.product[k].e, a.product[k].splits);
+    const auto& s = a.product[k];
+    p.lg[k] = slice_lanes(s.splits);
+    p.start[k + 1] = p.start[k] + (int)slice_blocks(s.e.rows, s.e.cols, s.splits);
   }
   for (int c = 0; c < a.columns; ++c, ++k) {
     p.lanes[c] = column_lanes(a.column[c].groups);
-    const int across = kRowThreads / p.lanes[c];
-    p.start[k + 1] = p.start[k] + (a.column[c].cols + across - 1) / across;
+    p.start[k + 1] = p.start[k] + (int)column_blocks(a.column[c].groups, a.column[c].cols);
   }
   if (k == 0) return hipSuccess;
   const dim3 grid((unsigned)p.start[k]), block(kRowThreads);
@@ -193,7 +206,7 @@ hipError_t launch_slope(const SlopeArgs& a, const UnpackJob& u, int dtype, hipSt
 hipError_t launch_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt, int dtype,
                             hipStream_t stream) {
   const long units = ckpt_cols(n) / 8, total = m * units;
-  const dim3 grid(blocks_of(total)), block(kRowThreads);
+  const dim3 grid = row_grid(total), block(kRowThreads);
   if (dtype == OIDN_F32)
     hipLaunchKernelGGL(ckpt_pack<OIDN_F32>, grid, block, 0, stream, x, ldx, m, n, ckpt, units, total);
   else if (dtype == OIDN_F16)
@@ -207,7 +220,7 @@ hipError_t launch_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ld
                               hipStream_t stream) {
   void* const c = const_cast<void*>(ckpt);
   const long units = (n + 7) / 8, total = m * units;
-  const dim3 grid(blocks_of(total)), block(kRowThreads);
+  const dim3 grid = row_grid(total), block(kRowThreads);
   if (dtype == OIDN_F32)
     hipLaunchKernelGGL(ckpt_unpack<OIDN_F32>, grid, block, 0, stream, c, m, n, y, ldy, units, total);
   else if (dtype == OIDN_F16)
