@@ -1,5 +1,6 @@
 """Dense operators at their edges: the narrowest operands, whose 16-byte loads
 span several rows, as dense as they can lie."""
+import ctypes
 import math
 
 import pytest
@@ -133,3 +134,27 @@ def test_checkpoint_of_more_units_than_a_launch_has_threads():
         step = a.abs() / 127 * (1 + 2.0 ** -8)
         assert ((b - a).abs() <= (0.5 + 2.0 ** -13) * step + a.abs() * 2.0 ** -11 + 2.0 ** -25).all()
     torch.cuda.empty_cache()
+
+
+def recorded(call):
+    """Nodes of a graph that records the call."""
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    count = ctypes.c_size_t()
+    assert U.lib().hipGraphGetNodes(ctypes.c_void_p(graph.raw_cuda_graph()), None, ctypes.byref(count)) == 0
+    return count.value
+
+
+def test_gradients_of_no_rows_take_one_launch_each():
+    """dw inside a wider buffer too: 300 rows of 7 of its 9 columns are zeros, the others as they were."""
+    k, n, ld = 7, 300, 9
+    dw, db = torch.full((n, ld), 3.0, device="cuda"), torch.full((n,), 3.0, device="cuda")
+
+    def call():
+        U.oidn_linear_backward(None, n, None, k, None, n, None, k, None, k, dw, ld, db, 0, k, n, U.OIDN_ACT_GELU, U.OIDN_F32,
+                               0, None, 0)
+
+    call()
+    assert not dw[:, :k].any() and (dw[:, k:] == 3).all() and not db.any()
+    assert recorded(call) == 2

@@ -221,7 +221,8 @@ hipError_t launch_ckpt_pack(const void* x, long ldx, long m, long n, void* ckpt,
                             hipStream_t stream);
 hipError_t launch_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ldy, int dtype,
                               hipStream_t stream);
-// Zeros (a plain store kernel, so that a captured graph holds no memset node).
-hipError_t launch_zero(void* p, size_t bytes, hipStream_t stream);
+// Zeros in rows of `width` bytes (a plain store kernel, so that a captured graph
+// holds no memset node).
+hipError_t launch_zero(void* p, long rows, size_t width, size_t pitch, hipStream_t stream);
 
 }  // namespace oidn

@@ -563,10 +563,9 @@ int oidn_linear_backward(const void* dy, long lddy, const void* x, long ldx, con
   OIDN_TRY(check_aligned("dbias", dbias, 4));
   if (m == 0) {
     // sums over no rows
-    for (long i = 0; dw && lddw != k && i < n; ++i)
-      OIDN_TRY(ran(launch_zero(static_cast<char*>(dw) + i * lddw * esize(dtype), k * esize(dtype), stream), "zero launch"));
-    if (dw && lddw == k) OIDN_TRY(ran(launch_zero(dw, (size_t)n * k * esize(dtype), stream), "zero launch"));
-    if (dbias) OIDN_TRY(ran(launch_zero(dbias, n * sizeof(float), stream), "zero launch"));
+    const size_t es = esize(dtype);
+    if (dw) OIDN_TRY(ran(launch_zero(dw, n, k * es, lddw * es, stream), "zero launch"));
+    if (dbias) OIDN_TRY(ran(launch_zero(dbias, 1, n * sizeof(float), 0, stream), "zero launch"));
     return clear_error();
   }
   OIDN_TRY(check_matrix("dy", dy, lddy, n, dtype, false));
@@ -733,10 +732,10 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
   OIDN_TRY(check_aligned("db_out", db_out, 4));
   if (m == 0) {
     // sums over no rows
-    if (dw_in) OIDN_TRY(ran(launch_zero(dw_in, 2 * (size_t)f * d * es, stream), "zero launch"));
-    if (dw_out) OIDN_TRY(ran(launch_zero(dw_out, (size_t)f * d * es, stream), "zero launch"));
-    if (db_in) OIDN_TRY(ran(launch_zero(db_in, 2 * (size_t)f * sizeof(float), stream), "zero launch"));
-    if (db_out) OIDN_TRY(ran(launch_zero(db_out, d * sizeof(float), stream), "zero launch"));
+    if (dw_in) OIDN_TRY(ran(launch_zero(dw_in, 1, 2 * (size_t)f * d * es, 0, stream), "zero launch"));
+    if (dw_out) OIDN_TRY(ran(launch_zero(dw_out, 1, (size_t)f * d * es, 0, stream), "zero launch"));
+    if (db_in) OIDN_TRY(ran(launch_zero(db_in, 1, 2 * (size_t)f * sizeof(float), 0, stream), "zero launch"));
+    if (db_out) OIDN_TRY(ran(launch_zero(db_out, 1, d * sizeof(float), 0, stream), "zero launch"));
     return clear_error();
   }
   const bool inner = dx || dw_in || db_in || dw_out;     // what needs dh

@@ -133,9 +133,10 @@ __global__ __launch_bounds__(kRowThreads) void ckpt_unpack(void* ckpt, long m, l
   store8<DT>(y, i * ldy + j, ckpt_stored<DT>(load_codes(ckpt_at(ckpt, m, n), i, (int)j)), left);
 }
 
-__global__ __launch_bounds__(kRowThreads) void zero_bytes(unsigned char* p, size_t n) {
+__global__ __launch_bounds__(kRowThreads) void zero_rows(unsigned char* p, size_t width, size_t pitch, size_t total) {
   const size_t step = (size_t)gridDim.x * kRowThreads;
-  for (size_t i = (size_t)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += step) p[i] = 0;
+  for (size_t i = (size_t)blockIdx.x * kRowThreads + threadIdx.x; i < total; i += step)
+    p[i / width * pitch + i % width] = 0;
 }
 
 }  // namespace
@@ -230,10 +231,10 @@ hipError_t launch_ckpt_unpack(const void* ckpt, long m, long n, void* y, long ld
   return hipGetLastError();
 }
 
-hipError_t launch_zero(void* p, size_t bytes, hipStream_t stream) {
-  const size_t b = (bytes + kRowThreads - 1) / kRowThreads;
-  hipLaunchKernelGGL(zero_bytes, dim3((unsigned)(b < 2048 ? b : 2048)), dim3(kRowThreads), 0, stream,
-                     static_cast<unsigned char*>(p), bytes);
+hipError_t launch_zero(void* p, long rows, size_t width, size_t pitch, hipStream_t stream) {
+  const size_t total = rows * width, b = (total + kRowThreads - 1) / kRowThreads;
+  hipLaunchKernelGGL(zero_rows, dim3((unsigned)(b < 2048 ? b : 2048)), dim3(kRowThreads), 0, stream,
+                     static_cast<unsigned char*>(p), width, pitch, total);
   return hipGetLastError();
 }
 
