@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import unet_x3_convolution_amd as U
-from dense_reference import HALF, TINY, TORCH, check, given, linear_backward
+from dense_reference import HALF, TINY, TORCH, check, given, linear, linear_backward
 from helpers import DT, torch_cuda
 
 pytestmark = pytest.mark.gpu
@@ -158,3 +158,41 @@ def test_gradients_of_no_rows_take_one_launch_each():
     call()
     assert not dw[:, :k].any() and (dw[:, k:] == 3).all() and not db.any()
     assert recorded(call) == 2
+
+
+# the largest subnormal, and weights that bring its multiples back into the middle of the range
+SUBNORMAL = {"f32": (2.0 ** -127, 2.0 ** 100), "f16": (2.0 ** -15, 2.0 ** 12), "bf16": (2.0 ** -127, 2.0 ** 100)}
+
+
+@pytest.mark.parametrize("precision", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m, k, n", [(1, 72, 48), (2, 515, 48), (3, 72, 48), (4, 1040, 48), (3, 72, 4104), (5, 72, 48), (33, 72, 48), (300, 129, 200)])
+def test_subnormal_inputs_count(m, k, n, precision):
+    """Every kernel of a forward product takes subnormals as what they are."""
+    size, scale = SUBNORMAL[precision]
+    ty, dt = TORCH[precision], DT[precision]
+    g = torch.Generator().manual_seed(m + k + n)
+    x = ((torch.rand(m, k, generator=g, dtype=torch.float64) * 2 - 1) * size).to(ty)
+    w = (torch.randn(n, k, generator=g, dtype=torch.float64) * scale * k ** -0.5).to(ty)
+    assert x.any() and x.abs().max().double() <= size
+    y = torch.empty(m, n, dtype=ty, device="cuda")
+    ws = bytes_(U.oidn_linear_workspace_bytes(m, k, n, dt))
+    U.oidn_linear(x.cuda(), k, w.cuda(), k, None, None, 0, y, n, None, 0, m, k, n, U.OIDN_ACT_NONE, dt, 0, ws, ws.numel())
+    check(y, linear(given(x), given(w), None, None, "none")[0], precision, "y")
+
+
+@pytest.mark.parametrize("precision", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m, k, n", [(50, 40, 24), (50, 136, 144), (9000, 24, 40)])
+def test_subnormal_gradients_count(m, k, n, precision):
+    """dy subnormal, in one pass and in separate products."""
+    size, scale = SUBNORMAL[precision]
+    ty, dt = TORCH[precision], DT[precision]
+    g = torch.Generator().manual_seed(m + k + n)
+    dy = ((torch.rand(m, n, generator=g, dtype=torch.float64) * 2 - 1) * size).to(ty)
+    x, w = ((torch.randn(r, k, generator=g, dtype=torch.float64) * scale * 2.0 ** -6).to(ty) for r in (m, n))
+    dx, dw = torch.empty(m, k, dtype=ty, device="cuda"), torch.empty(n, k, dtype=ty, device="cuda")
+    ws = bytes_(U.oidn_linear_backward_workspace_bytes(m, k, n, U.OIDN_ACT_NONE, dt, 0))
+    U.oidn_linear_backward(dy.cuda(), n, x.cuda(), k, None, n, w.cuda(), k, dx, k, dw, k, None, m, k, n, U.OIDN_ACT_NONE, dt,
+                           0, ws, ws.numel())
+    want = linear_backward(given(dy), given(x), None, given(w), "none", precision)
+    check(dx, want[0], precision, "dx")
+    check(dw, want[1], precision, "dw")
