@@ -35,8 +35,8 @@ class KernelNode(ctypes.Structure):
                 ("args", ctypes.c_void_p), ("lds", ctypes.c_uint)]
 
 
-def launches(call):
-    """What `call` launches: (kernel, tile, straight to LDS) of its 16-bit tile kernels."""
+def names(call):
+    """The kernels that `call` launches, by their mangled names."""
     graph = torch.cuda.CUDAGraph(keep_graph=True)
     with torch.cuda.graph(graph):
         call()
@@ -49,7 +49,14 @@ def launches(call):
     for node in nodes:
         params = KernelNode()
         assert hip.hipGraphKernelNodeGetParams(ctypes.c_void_p(node), ctypes.byref(params)) == 0
-        name = hip.hipKernelNameRefByPtr(ctypes.c_void_p(params.func), None).decode()
+        found.append(hip.hipKernelNameRefByPtr(ctypes.c_void_p(params.func), None).decode())
+    return found
+
+
+def launches(call):
+    """(kernel, tile, straight to LDS) of the 16-bit tile kernels that `call` launches."""
+    found = []
+    for name in names(call):
         m = re.search(r"dense_gemm16(_gated_back|_group)?ILb[01]E(?:Li0ELi([02])E)?Li(\d+)E(?:Li\d+E)?Lb([01])E", name)
         if m:
             kind = {"_gated_back": "gated back", "_group": "group"}.get(m[1]) or ("linear" if m[2] == "0" else "gated")
@@ -118,7 +125,8 @@ def agree8(blob, want, label):
 # m, k, n, the tile, and the one where rows lie at odd pitches
 LINEAR = [(3001, 264, 1030, (128, True), (128, False)), (6150, 264, 2054, (256, True), (128, False)),
           (6145, 320, 2049, (256, True), (128, False)), (1030, 8192, 1030, (128, True), (128, False)),
-          (3001, 263, 1030, (128, False), (128, False))]
+          (3001, 263, 1030, (128, False), (128, False)), (8001, 1032, 510, (128, True), (128, False)),
+          (13101, 264, 4102, (256, True), (128, False))]
 
 
 @pytest.mark.parametrize("precision", ["f16", "bf16"])
@@ -181,7 +189,7 @@ def test_ffn(m, d, f, gated, second, pad, precision):
 
 
 # m, k, n and the tile of both products
-LINEAR_BACK = [(2051, 4104, 2056, 256), (8201, 520, 1032, 128), (521, 4104, 520, 128)]
+LINEAR_BACK = [(2051, 4104, 2056, 256), (12301, 4104, 2056, 256), (8201, 520, 1032, 128), (521, 4104, 520, 128)]
 
 
 @pytest.mark.parametrize("precision", ["f16", "bf16"])
@@ -248,3 +256,14 @@ def test_ffn_backward(m, d, f, back, tile, eight, pad, precision):
     agree(dw_out, want[2], precision, "dw_out")
     agree(db_in, want[3], "f32", "db_in")
     agree(db_out, want[4], "f32", "db_out")
+
+
+@pytest.mark.parametrize("m, n, streamed", [(529, 2048, False), (16401, 192, True), (174737, 192, False), (4113, 2048, False),
+                                            (49169, 1024, True), (2048, 513, False), (2048, 512, True)])
+def test_which_results_go_past_the_caches(m, n, streamed):
+    """Those that the next reader is better off without in them: narrow ones of up to 18 MB, all from 96 MB on."""
+    x, w, y = (torch.empty(r, c, dtype=torch.bfloat16, device="cuda") for r, c in ((m, 64), (n, 64), (m, n)))
+    ws = bytes_(U.oidn_linear_workspace_bytes(m, 64, n, U.OIDN_BF16))
+    called = names(lambda: U.oidn_linear(x, 64, w, 64, None, None, 0, y, n, None, 0, m, 64, n, U.OIDN_ACT_RELU, U.OIDN_BF16, 0,
+                                         ws, ws.numel()))
+    assert len(called) == 1 and re.search(r"CachingE([01])E", called[0])[1] == str(int(streamed))

@@ -49,9 +49,23 @@ struct EpilogueArgs {
   float* part;             // kEpiPartial: [slice][rows][cols]; kEpiGatedBack: column sums or null
   int act;
   int z8;                  // z is held in 8 bits
+  int stream;              // kEpiLinear, kEpiStore: stream_result
   long rows;
   int cols;
 };
+// Whether a 16-bit result goes past the caches.  Two layers one after the other
+// (bf16, 32 to 2048 columns, 2 to 160 MB a result; streamed against kept, us): up to
+// 18 MB in at most 512 columns 2% slower to 14% faster (64 columns, 16 MB 17.9 and
+// 19.6); in 1024 and more, whose rows several tiles read again, 5% faster to 14%
+// slower (2048 columns, 2 MB 41 and 36); 20 to 80 MB mostly slower, up to 24% (192
+// columns, 64 MB 88 and 71); from 96 MB on 3% slower to 10% faster (1024 columns,
+// 112 MB 266 and 278) but for 96 columns (9% slower).  A call by itself may gain by
+// it where the next reader loses: 8192 x 4096 -> 4096 231 and 234 alone, 402 and 397
+// twice in a row.
+inline bool stream_result(long rows, long cols) {
+  const long bytes = 2 * rows * cols;
+  return (bytes <= 18L << 20 && cols <= 512) || bytes >= 96L << 20;
+}
 
 struct GemmArgs {
   const void* q;

@@ -171,6 +171,7 @@ GemmArgs gemm_args(Product& p, const void* q, long ldq, const void* pm, long ldp
   a.e = e;
   a.e.rows = p.rows;
   a.e.cols = (int)p.cols;
+  a.e.stream = stream_result(p.rows, p.cols);
   if (p.plan.splits > 1) a.e.part = static_cast<float*>(slices);
   return a;
 }

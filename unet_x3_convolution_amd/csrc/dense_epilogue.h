@@ -65,8 +65,7 @@ __device__ __forceinline__ Eight load8(const void* p, long i, int n) {
   return r;
 }
 
-// STREAM: whole units are not kept in the caches (results of a size that the
-// next reader does not find there anyway).
+// STREAM: whole units are not kept in the caches (stream_result).
 template <int DT, bool STREAM = false>
 __device__ __forceinline__ void store8(void* p, long i, const Eight& r, int n) {
   typedef typename Storage<DT>::T T;
@@ -389,7 +388,7 @@ __device__ __forceinline__ void fetch(const EpilogueArgs& e, long i, int j, RawF
 // x: the sums (kEpiGated: the gate's, u the up projection's); bias: that of
 // the same columns, zeros if there is none.  kEpiGatedBack adds da and db to
 // sums.
-template <int DT, int EPI, bool WHOLE, bool Z8>
+template <int DT, int EPI, bool WHOLE, bool Z8, bool STREAM = false>
 __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i, int j, Eight x, Eight u,
                                        const Fetched& bias, const RawFetched<DT, Z8>& f, Fetched& sums) {
   const int n = WHOLE ? 8 : e.cols - j;
@@ -399,7 +398,7 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
       store8<OIDN_F32>(e.part, ((long)slice * e.rows + i) * e.cols + j, x, n);
   } else if constexpr (EPI == kEpiStore) {
     if (e.res) add8(x, f.a.value());
-    if (ok) store8<DT, WHOLE>(e.y, i * e.ldy + j, x, n);
+    if (ok) store8<DT, WHOLE && STREAM>(e.y, i * e.ldy + j, x, n);
   } else if constexpr (EPI == kEpiLinear) {
     add8(x, bias.a);
     if (e.z) {
@@ -412,7 +411,7 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
     }
     activate8<DT>(e.act, x);
     if (e.res) add8(x, f.a.value());
-    if (ok) store8<DT, WHOLE>(e.y, i * e.ldy + j, x, n);
+    if (ok) store8<DT, WHOLE && STREAM>(e.y, i * e.ldy + j, x, n);
   } else if constexpr (EPI == kEpiGated) {
     add8(x, bias.a);
     add8(u, bias.b);
@@ -471,11 +470,18 @@ constexpr int epilogue_rows() { return FR * FC > 32 ? 8 * FR : 16 * FR; }
 template <int FR, int FC>
 constexpr int epilogue_bytes() { return epilogue_rows<FR, FC>() * 64 * FC; }
 
-template <int DT, int EPI, int FR, int FC, bool Z8 = false>
+// Results kept in the caches, past them, or as e.stream has it.
+enum Caching { kKept, kStreamed, kEither };
+
+template <int DT, int EPI, int FR, int FC, bool Z8 = false, Caching WHERE = kKept>
 __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const floatx4 (&acc)[FC][FR], char* lds,
                                               long i0, int j0, int slice, long group) {
   if constexpr (EPI == kEpiLinear || EPI == kEpiStore) {
     if (slice >= 0) return tile_epilogue<DT, kEpiPartial, FR, FC>(e, acc, lds, i0, j0, slice, group);
+    if constexpr (WHERE == kEither) {
+      if (e.stream) return tile_epilogue<DT, EPI, FR, FC, Z8, kStreamed>(e, acc, lds, i0, j0, slice, group);
+      return tile_epilogue<DT, EPI, FR, FC, Z8, kKept>(e, acc, lds, i0, j0, slice, group);
+    }
   }
   if constexpr (EPI == kEpiGatedBack && !Z8) {
     if (e.z8) return tile_epilogue<DT, EPI, FR, FC, true>(e, acc, lds, i0, j0, slice, group);
@@ -529,7 +535,7 @@ __device__ __forceinline__ void tile_epilogue(const EpilogueArgs& e, const float
         for (int m = 0; m < 4; ++m) u.v[4 * h + m] = w[m];
       }
     }
-    finish<DT, EPI, kWhole, Z8>(e, slice, ir + s * kAtOnce, j, x, u, bias, f, sums);
+    finish<DT, EPI, kWhole, Z8, WHERE == kStreamed>(e, slice, ir + s * kAtOnce, j, x, u, bias, f, sums);
   };
   constexpr int kRounds = 16 * FR / kRows;
 #pragma unroll 1

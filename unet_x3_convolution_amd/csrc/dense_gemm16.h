@@ -83,7 +83,7 @@ template <int TR, int TC>
 constexpr int gemm16_lds() { return 2 * (TR + TC) * kDenseK * 2; }
 
 // Workgroup `block` of the product; lds: gemm16_lds<TR, TC>() bytes.
-template <bool BF, int LAYOUT, int EPI, int TR, int TC>
+template <bool BF, int LAYOUT, int EPI, int TR, int TC, Caching WHERE>
 __device__ __forceinline__ void gemm16_staged(const GemmArgs& a, int block, char* lds) {
   constexpr int DT = BF ? OIDN_BF16 : OIDN_F16;
   constexpr bool PS = LAYOUT != kForward, QS = LAYOUT == kWeightGrad;
@@ -158,7 +158,7 @@ __device__ __forceinline__ void gemm16_staged(const GemmArgs& a, int block, char
     }
   }
   __syncthreads();                       // every wave has read its last fragments
-  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, lds + wave * epilogue_bytes<FR, FC>(), i0 + wr * (TR / 2),
+  tile_epilogue<DT, EPI, FR, FC, false, WHERE>(a.e, acc, lds + wave * epilogue_bytes<FR, FC>(), i0 + wr * (TR / 2),
                                  (int)j0 + wc * (C / 2), a.splits > 1 ? slice : -1, (long)tr * 2 + wr);
 }
 

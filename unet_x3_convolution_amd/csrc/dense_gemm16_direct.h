@@ -132,7 +132,7 @@ struct Direct16 {
 
 // Workgroup `block` of the product; lds: gemm16_lds<TR, TC>() bytes, two
 // buffers of a P and a Q tile.
-template <bool BF, int LAYOUT, int EPI, int TR, int TC>
+template <bool BF, int LAYOUT, int EPI, int TR, int TC, Caching WHERE>
 __device__ __forceinline__ void gemm16_direct(const GemmArgs& a, int block, char* lds) {
   constexpr int DT = BF ? OIDN_BF16 : OIDN_F16;
   constexpr bool PS = LAYOUT != kForward, QS = LAYOUT == kWeightGrad;
@@ -269,22 +269,22 @@ __device__ __forceinline__ void gemm16_direct(const GemmArgs& a, int block, char
            acc[(n + 3) / FR][(n + 3) % FR]);
   }
   __syncthreads();                       // every wave has read its last fragments
-  tile_epilogue<DT, EPI, FR, FC>(a.e, acc, lds + wave * epilogue_bytes<FR, FC>(), i0 + wr * (TR / 2),
+  tile_epilogue<DT, EPI, FR, FC, false, WHERE>(a.e, acc, lds + wave * epilogue_bytes<FR, FC>(), i0 + wr * (TR / 2),
                                  (int)j0 + wc * (C / 2), a.splits > 1 ? slice : -1, (long)tr * 2 + wr);
 }
 
 // The kernels.  DIRECT: operands go straight to LDS, else through registers.
-template <bool BF, int LAYOUT, int EPI, int TR, int TC, bool DIRECT>
+template <bool BF, int LAYOUT, int EPI, int TR, int TC, bool DIRECT, Caching WHERE = kKept>
 __device__ __forceinline__ void gemm16(const GemmArgs& a, int block, char* lds) {
-  if constexpr (DIRECT) gemm16_direct<BF, LAYOUT, EPI, TR, TC>(a, block, lds);
-  else gemm16_staged<BF, LAYOUT, EPI, TR, TC>(a, block, lds);
+  if constexpr (DIRECT) gemm16_direct<BF, LAYOUT, EPI, TR, TC, WHERE>(a, block, lds);
+  else gemm16_staged<BF, LAYOUT, EPI, TR, TC, WHERE>(a, block, lds);
 }
 constexpr int workgroups_per_cu(int tr, int tc) { return tr * tc >= 256 * 256 ? 1 : 2; }
 
-template <bool BF, int LAYOUT, int EPI, int TR, int TC, bool DIRECT>
+template <bool BF, int LAYOUT, int EPI, int TR, int TC, bool DIRECT, Caching WHERE>
 __global__ __launch_bounds__(256, workgroups_per_cu(TR, TC)) void dense_gemm16(GemmArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[gemm16_lds<TR, TC>()];
-  gemm16<BF, LAYOUT, EPI, TR, TC, DIRECT>(a, blockIdx.x, lds);
+  gemm16<BF, LAYOUT, EPI, TR, TC, DIRECT, WHERE>(a, blockIdx.x, lds);
 }
 
 // The gated block's dh with its epilogue; the first workgroups read a
@@ -306,8 +306,8 @@ __global__ __launch_bounds__(256, workgroups_per_cu(T, T)) void dense_gemm16_gro
   int k = 0;
   while (k + 1 < g.count && (int)blockIdx.x >= g.start[k + 1]) ++k;
   const int block = blockIdx.x - g.start[k];
-  if (g.layout[k] == kInputGrad) gemm16<BF, kInputGrad, kEpiStore, T, T, DIRECT>(g.a[k], block, lds);
-  else gemm16<BF, kWeightGrad, kEpiStore, T, T, DIRECT>(g.a[k], block, lds);
+  if (g.layout[k] == kInputGrad) gemm16<BF, kInputGrad, kEpiStore, T, T, DIRECT, kEither>(g.a[k], block, lds);
+  else gemm16<BF, kWeightGrad, kEpiStore, T, T, DIRECT, kEither>(g.a[k], block, lds);
 }
 
 }  // namespace
