@@ -104,11 +104,13 @@ __device__ __forceinline__ void store8(void* p, long i, const Eight& r, int n) {
 // silu(z) = z p with p = 1 / (1 + e^-z); gelu(z) = z Phi(z), Phi the normal
 // distribution function.  Phi is formed from Phi(-|z|), which is small where z is
 // negative, so gelu keeps its relative accuracy there: (1 + erf) / 2 would leave
-// what two numbers near 1/2 differ by (18% off at z = -5.25).  fp32 uses erfcf.
-// The 16-bit types use Phi(-|z|) = e^(-z^2 / 2) P(t), t = 1 / (1 + 0.29 |z|), with a
-// P of degree 6 fitted to the formula by minimax: to 5e-8 absolute and 2e-5 of the
-// value up to |z| = 5.8 (where fp16 ends; half its step is 4.9e-4), 3.3e-4 of it to
-// 13.5 (where bf16 ends; half its step is 3.9e-3).
+// what two numbers near 1/2 differ by (18% off at z = -5.25).  Phi(-|z|) is
+// e^(-z^2 / 2) P(t), t = 1 / (1 + c |z|), with a P fitted to it by minimax of the
+// relative error up to |z| = 13.5, where fp32 ends.  fp32: c = 0.35, degree 9, to 3e-8
+// (3e-7 with the roundings of fp32, which the exponential's argument adds z^2 6e-8
+// to); erfcf took 5% longer on a whole block's gradients.  16 bits: c = 0.29, degree
+// 6, to 5e-8 absolute and 2e-5 of the value up to |z| = 5.8 (where fp16 ends; half its
+// step is 4.9e-4), 3.3e-4 of it beyond (half a step of bf16 is 3.9e-3).
 __device__ __forceinline__ float logistic(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
 }
@@ -116,14 +118,17 @@ __device__ __forceinline__ float logistic(float z) {
 template <int DT>
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
   e = __builtin_amdgcn_exp2f(-0.72134752f * z * z);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(DT == OIDN_F32 ? 0.35f : 0.29f, __builtin_fabsf(z), 1.f));
+  float p;
   if constexpr (DT == OIDN_F32) {
-    return 0.5f * erfcf(-0.70710678f * z);
+    p = 0.139621571f + t * (0.13985908f + t * (0.119852439f + t * (0.105432935f + t * (-0.0229371302f +
+        t * (0.158929259f + t * (-0.255504519f + t * (0.143872216f + t * -0.02912586f)))))));
   } else {
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.29f, __builtin_fabsf(z), 1.f));
-    const float q = e * t * (0.117000229f + t * (0.0996669881f + t * (0.182742287f + t * (-0.097846044f +
-                    t * (0.288142841f + t * -0.0897063499f)))));
-    return z < 0.f ? q : 1.f - q;
+    p = 0.117000229f + t * (0.0996669881f + t * (0.182742287f + t * (-0.097846044f + t * (0.288142841f +
+        t * -0.0897063499f))));
   }
+  const float q = e * (t * p);
+  return z < 0.f ? q : 1.f - q;
 }
 
 // Past |z| = 100 (silu) and 30 (gelu) the functions have reached 0, z and the
