@@ -378,14 +378,16 @@ int oidn_unet_forward_timed(const void* d_weights, int in_channels, const float*
  * row per output channel, in dtype; biases and their gradients are float32.
  * Sums, activations and slopes are fp32; every output is rounded once, to
  * nearest even, where it is stored.  fp16 outputs beyond 65504 become
- * infinite.  Results do not depend on timing: a call with the same arguments
+ * infinite, and so do what passes from one product to the next in fp16 (h, dz,
+ * da, db); with OIDN_F32 nothing is rounded on the way.  Results do not depend on timing: a call with the same arguments
  * gives the same bits.
  *
  * Any size and pitch works and any element-aligned base; bases and pitches
  * that are multiples of 16 bytes are fastest.  m may be 0 (sums over no rows
  * are 0, nothing else is written).  Outputs must not overlap inputs, except
  * that `residual` may be y and `add` may be dx (same pitch).  Columns between
- * a row's end and its pitch are neither read nor written.  Column counts
+ * a row's end and its pitch are never written; they may be read, and what they
+ * hold does not matter.  Column counts
  * above 2^24, matrices above 2^38 elements and products of more tiles than a
  * launch holds (about 2^24; of 64 x 64 where a side is short):
  * OIDN_E_UNSUPPORTED.

@@ -214,9 +214,11 @@ struct NarrowArgs {
 };
 // Whether a layer is narrow.  Where n and k are both over 64 the pass pays from
 // 8192 rows on (us, bf16, gelu, 128 x 128: 17 against 14 in separate launches at
-// 2040 rows, 20 against 19 at 8160, 26 against 26 at 16320, 54 against 114 at
-// 130560); narrower layers gain at any length (32 -> 64: 10 against 14 at 510
-// rows, 25 against 61 at 130560).
+// 2040 rows, 20 against 19 at 8160, 26 against 26 at 16320, 55 against 115 at
+// 130560); where one is 64 or less it was ahead at every length measured, 64 to
+// 130560 rows of 3 -> 32, 8 -> 8, 32 -> 64, 64 -> 16, 64 -> 64, 96 -> 48, 48 -> 96,
+// 128 -> 32 and 32 -> 128 (32 -> 64: 10 against 14 at 510 rows, 25 against 61 at
+// 130560; the least, 48 -> 96 at 2040 rows, 12.6 against 13.3).
 inline bool narrow_layer(long rows, int n, int k) {
   return n <= kNarrow && k <= kNarrow && (n <= 64 || k <= 64 || rows >= 8192);
 }

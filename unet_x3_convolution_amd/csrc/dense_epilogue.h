@@ -435,6 +435,9 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
       }
     }
     activate8<DT>(e.act, x);
+    // h is rounded to the storage type, as the second product's matrix cores take it
+    // (y of a block is off by 0.0019 in bf16 and 0.00023 in fp16, where an fp32 h
+    // would leave 0.0017 and 0.00021, its own rounding)
 #pragma unroll
     for (int k = 0; k < 8; ++k) x.v[k] *= u.v[k];
     if (ok) store8<DT>(e.y, i * e.ldy + j, x, n);
@@ -453,6 +456,9 @@ __device__ __forceinline__ void finish(const EpilogueArgs& e, int slice, long i,
         sums.b.v[k] += db.v[k];
       }
     }
+    // rounded to what the gradients' products read, 16-bit operands of the matrix
+    // cores: dx and both dw then carry two roundings, sqrt 2 of the output's own; the
+    // column sums above are of the unrounded values
     store8<DT>(e.h, i * (long)e.cols + j, h, n);
     store8<DT>(e.y, i * e.ldy + j, da, n);
     store8<DT>(e.y, i * e.ldy + e.cols + j, db, n);

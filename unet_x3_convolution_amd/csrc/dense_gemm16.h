@@ -21,8 +21,8 @@
 // never stored; elements past the summed length are zeros in both operands.
 // Loads are 16 bytes wide at any 2-byte alignment.  This form is for operands
 // that the direct one (dense_gemm16_direct.h) does not take: odd pitches, bases
-// and sizes.  4096 x 4096 x 2048 takes 82 us (838 TFLOP/s; direct 67), with odd
-// pitches, whose loads straddle lines, 105.
+// and sizes.  4096 x 4096 x 2048 takes 82 to 91 us (838 to 758 TFLOP/s; direct 57 to
+// 67, by the card), with odd pitches, whose loads straddle lines, 100 to 105.
 #pragma once
 
 #include "dense_epilogue.h"

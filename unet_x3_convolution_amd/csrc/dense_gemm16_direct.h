@@ -28,9 +28,9 @@
 // of reads, two workgroups to a unit; 64 x 64: launches that would leave units
 // idle otherwise.
 //
-// Measured (bf16, one MI355X): 8192 x 4096 x 4096 in 205 us (1340 TFLOP/s),
-// through registers 331; 8192^3 at 1351, 1349 and 1324 TFLOP/s in the three
-// layouts.  Power bounds it: the same instructions on zeros ran at 1835.  A
+// Measured (bf16, one MI355X): 8192 x 4096 x 4096 in 205 us (1340 TFLOP/s), a call
+// among others 212, through registers 331; 8192^3 at 1351, 1349 and 1324 TFLOP/s in
+// the three layouts.  Power bounds it: the same instructions on zeros ran at 1835.  A
 // 256 x 256 tile costs 9 us besides its loop and its launch's start, as fitted over sizes.
 #pragma once
 

@@ -5,9 +5,9 @@
 // 4096 x 1024 runs at 120 TFLOP/s, 128 x 128 tiles at 105, one or two to a unit
 // with their registers full.  Plain forward products of few tiles take 32 x 64,
 // whose second workgroup on a unit works while the first one waits (us a call,
-// gelu and residual, 64 x 64 against 32 x 64): 2040 x 112 -> 96 8.0 and 6.0, 510
-// x 128 -> 512 7.4 and 5.7, 1021 x 515 -> 771 19.1 and 18.2; with many tiles the
-// larger ones' fewer loads win: 4096 x 1024 -> 4096 293 and 322.
+// gelu and residual, 64 x 64 against 32 x 64): 2040 x 112 -> 96 7.8 and 6.0, 510
+// x 128 -> 512 7.3 and 5.7, 1021 x 515 -> 771 18.8 and 18.3; with many tiles the
+// larger ones' fewer loads win: 4096 x 1024 -> 4096 298 and 325.
 //
 // 32 summed elements are staged at a time through registers into one of two
 // LDS buffers, two or three tiles ahead, as rows of 32 + 4 floats: the pad puts

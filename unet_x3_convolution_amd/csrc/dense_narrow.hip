@@ -117,7 +117,7 @@ void narrow_back(NarrowArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           v.v[k] *= s.v[k];
-          r[k] = (T)v.v[k];                // as the products read it
+          r[k] = (T)v.v[k];                // rounded as the products read it; the sums are not
         }
         kept = __builtin_bit_cast(uint4, r);
       }

@@ -2,8 +2,9 @@
 // the slope pass dz = dy * act'(z) with column sums, column sums of partial
 // rows, 8-bit checkpoints of whole matrices, and zeros.
 //
-// Small ones take a launch's 2 to 3 us; 32640 x 112 fp16 goes to 8 bits in 5.3 us
-// and back in 3.9, 16384 x 2048 bf16 (103 MB) in 22 us (4.7 TB/s) and 20.
+// Small ones take a launch's 2 to 3 us; 32640 x 112 fp16 goes to 8 bits in 5.2 us
+// and back in 4.0, 16384 x 2048 bf16 (103 MB) in 22.6 us (4.6 TB/s), there and back
+// in 40.
 #include "dense_slope.h"
 
 namespace oidn {
