@@ -62,6 +62,11 @@ extern "C" {
                                  OIDN_E_UNSUPPORTED                                   */
 #define OIDN_TRANSFER_LOG  1  /* F(x) = ln(1 + x), F^-1(y) = exp(y) - 1 (reading)    */
 
+/* ---- norms around a block ------------------------------------------------ */
+#define OIDN_NORM_NONE   0  /* the row itself                                  */
+#define OIDN_NORM_RMS    1  /* x / sqrt(mean(x^2) + eps)                       */
+#define OIDN_NORM_LAYER  2  /* (x - mean) / sqrt(mean((x - mean)^2) + eps)     */
+
 /* ---- activations of the dense operators ---------------------------------- */
 #define OIDN_ACT_NONE  0
 #define OIDN_ACT_RELU  1   /* max(z, 0), slope 0 at 0                          */
@@ -461,6 +466,81 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
                       long lddx, void* dw_in, float* db_in, void* dw_out, float* db_out, long m, int d,
                       int f, int act, int dtype, unsigned flags, void* workspace, size_t ws_bytes,
                       hipStream_t stream);
+
+/* ========================================================================
+ * What stands around a block over activation rows: the norm before it, and the
+ * residual sum after it with a norm, a gate, a residual scale and dropout.
+ * Matrices, pitches and types are as above; weights, shifts, gates and their
+ * gradients are float32.  Statistics and sums are fp32; every output is rounded
+ * once.  Rows of n columns, each by itself: a NaN or an infinity stays in its row.
+ * A row whose sum of squares passes the range of float32 becomes zeros or NaN; so
+ * does a row of equal values (of zeros, with OIDN_NORM_RMS) where eps is 0.
+ * In place: y of oidn_norm may be x, u may be x or o, y of oidn_dropout may be x
+ * or the residual, add may be dx (same pitch).
+ * ======================================================================== */
+
+/* Before a block:  y = norm(x) weight + shift.  weight and shift (n floats) may
+ * be NULL: 1 and 0.  norm: OIDN_NORM_RMS or OIDN_NORM_LAYER. */
+int oidn_norm(const void* x, long ldx, const float* weight, const float* shift, void* y, long ldy, long m,
+              int n, int norm, float eps, int dtype, hipStream_t stream);
+
+/* Its gradients, from dy: with hat = norm(x) = (x - mean) r and g = dy weight,
+ *   dx = r (g - mean(g) - hat mean(g hat)) + add     (OIDN_NORM_RMS: mean(g) left out)
+ *   dweight = sum of dy hat over the rows,  dshift = sum of dy
+ * add (m x n or NULL) is what else reaches x.  dx, dweight and dshift may each
+ * be NULL.  Nothing is kept from the forward pass but x. */
+int oidn_norm_backward_workspace_bytes(long m, int n, int dtype, size_t* bytes);
+int oidn_norm_backward(const void* dy, long lddy, const void* x, long ldx, const float* weight,
+                       const void* add, long ldadd, void* dx, long lddx, float* dweight, float* dshift,
+                       long m, int n, int norm, float eps, int dtype, void* workspace, size_t ws_bytes,
+                       hipStream_t stream);
+
+/* After a block with the output o, and before the next one:
+ *   u = scale x + gate drop(norm(o) weight + shift)
+ *   v = next_norm(u) next_weight + next_shift        (of u as stored)
+ * gate: NULL (1), or a row of n floats at pitch ldg for every gate_rows rows (an
+ * image, a sequence; the last may be short).  drop: oidn_dropout's with p and rng
+ * (p = 0: none; rng unused).  norm may be OIDN_NORM_NONE (a block that norms only
+ * its input); next_norm too, with v NULL.  Vectors may be NULL: 1 and 0. */
+int oidn_norm_residual(const void* o, long ldo, const float* weight, const float* shift, const float* gate,
+                       long ldg, long gate_rows, const void* x, long ldx, float scale, float p,
+                       const unsigned long long* rng, void* u, long ldu, const float* next_weight,
+                       const float* next_shift, void* v, long ldv, long m, int n, int norm, int next_norm,
+                       float eps, int dtype, hipStream_t stream);
+
+/* Its gradients, from dv and from du, what else reaches u (NULL: nothing):
+ *   D = du + next_norm'(dv; u),  dx = scale D,
+ *   dgate = sum of D drop(norm(o) weight + shift) over the gate's rows,
+ *   h = drop(D gate),  dweight = sum of h norm(o),  dshift = sum of h,
+ *   d_o = norm'(h weight; o),
+ *   dnext_weight = sum of dv next_norm(u),  dnext_shift = sum of dv
+ * D is not rounded on the way.  u as oidn_norm_residual stored it (unused with
+ * next_norm OIDN_NORM_NONE, where dv is NULL and du is not); o, vectors, gate, p and
+ * rng's contents as given to it: the mask is formed again, not stored.  Any result
+ * may be NULL.  gate_rows of the size call: 0 without a gate. */
+int oidn_norm_residual_backward_workspace_bytes(long m, int n, long gate_rows, int dtype, size_t* bytes);
+int oidn_norm_residual_backward(const void* du, long lddu, const void* dv, long lddv, const void* o,
+                                long ldo, const float* weight, const float* shift, const float* gate,
+                                long ldg, long gate_rows, const void* u, long ldu, float scale, float p,
+                                const unsigned long long* rng, const float* next_weight, void* dx, long lddx,
+                                void* d_o, long lddo, float* dgate, long lddg, float* dweight, float* dshift,
+                                float* dnext_weight, float* dnext_shift, long m, int n, int norm,
+                                int next_norm, float eps, int dtype, void* workspace, size_t ws_bytes,
+                                hipStream_t stream);
+
+/* Dropout:  y = drop(x) + residual  (residual m x n or NULL).  Its gradient is
+ * the same call on dy without the residual.  The mask is never stored: with
+ * t = rint(65536 p), element (i, j) is kept, times 65536 / (65536 - t), where its 16
+ * bits are >= t, else 0 whatever it holds.  The bits are those of Philox4x32-10 with
+ * the 64-bit key rng[0] (the seed) and the counter (i ceil(n / 8) + j / 8, rng[1]),
+ * both 64 bits, low words first: element j % 8 = 2 w + b takes half b of word w
+ * (0: low).  So they depend on the element's place, seed and offset alone, not on
+ * pitch or type.  rng: two 64-bit words in device memory, read by the kernel, so
+ * that a captured graph drops other elements at each replay if the program (or a node of
+ * the graph) changes rng[1] in between; calls that are to be independent take
+ * different offsets.  p in [0, 1]; p = 0: nothing is dropped and rng may be NULL. */
+int oidn_dropout(const void* x, long ldx, const void* residual, long ldr, void* y, long ldy, long m, int n,
+                 float p, const unsigned long long* rng, int dtype, hipStream_t stream);
 
 /* Measurement helper, not part of the denoise path: `blocks` workgroups of
  * 4 waves, each wave issuing iters x 8 independent 16x16x32 MFMAs (fp16, or

@@ -36,6 +36,10 @@ OIDN_ACT_RELU = 1
 OIDN_ACT_SILU = 2
 OIDN_ACT_GELU = 3
 
+OIDN_NORM_NONE = 0
+OIDN_NORM_RMS = 1
+OIDN_NORM_LAYER = 2
+
 OIDN_X_CKPT8 = 1
 OIDN_Z_CKPT8 = 2
 
@@ -56,6 +60,8 @@ EXPORTS = (
     "oidn_ckpt_bytes", "oidn_ckpt_pack", "oidn_ckpt_unpack",
     "oidn_linear_workspace_bytes", "oidn_linear", "oidn_linear_backward_workspace_bytes", "oidn_linear_backward",
     "oidn_ffn_workspace_bytes", "oidn_ffn", "oidn_ffn_backward_workspace_bytes", "oidn_ffn_backward",
+    "oidn_norm", "oidn_norm_backward_workspace_bytes", "oidn_norm_backward", "oidn_norm_residual",
+    "oidn_norm_residual_backward_workspace_bytes", "oidn_norm_residual_backward", "oidn_dropout",
     "oidn_calibrate_mfma", "oidn_calibrate_read", "oidn_event_create", "oidn_event_destroy", "oidn_event_elapsed_ms",
 )
 
@@ -129,6 +135,17 @@ _SIGS = {
     "oidn_ffn_backward_workspace_bytes": ([_l, _i, _i, _i, _u, ctypes.POINTER(_sz)], _i),
     "oidn_ffn_backward": ([_vp, _l, _vp, _l, _vp, _vp, _vp, _vp, _l, _vp, _l, _vp, _vp, _vp, _vp, _l, _i, _i,
                            _i, _i, _u, _vp, _sz, _vp], _i),
+    "oidn_norm": ([_vp, _l, _vp, _vp, _vp, _l, _l, _i, _i, _f, _i, _vp], _i),
+    "oidn_norm_backward_workspace_bytes": ([_l, _i, _i, ctypes.POINTER(_sz)], _i),
+    "oidn_norm_backward": ([_vp, _l, _vp, _l, _vp, _vp, _l, _vp, _l, _vp, _vp, _l, _i, _i, _f, _i, _vp, _sz,
+                            _vp], _i),
+    "oidn_norm_residual": ([_vp, _l, _vp, _vp, _vp, _l, _l, _vp, _l, _f, _f, _vp, _vp, _l, _vp, _vp, _vp, _l, _l,
+                            _i, _i, _i, _f, _i, _vp], _i),
+    "oidn_norm_residual_backward_workspace_bytes": ([_l, _i, _l, _i, ctypes.POINTER(_sz)], _i),
+    "oidn_norm_residual_backward": ([_vp, _l, _vp, _l, _vp, _l, _vp, _vp, _vp, _l, _l, _vp, _l, _f, _f, _vp, _vp,
+                                     _vp, _l, _vp, _l, _vp, _l, _vp, _vp, _vp, _vp, _l, _i, _i, _i, _f, _i, _vp,
+                                     _sz, _vp], _i),
+    "oidn_dropout": ([_vp, _l, _vp, _l, _vp, _l, _l, _i, _f, _vp, _i, _vp], _i),
     "oidn_calibrate_mfma": ([_i, ctypes.c_long, _i, _vp, ctypes.POINTER(ctypes.c_longlong), _vp], _i),
     "oidn_calibrate_read": ([_vp, _sz, _vp, _vp], _i),
     "oidn_event_create": ([ctypes.POINTER(_vp)], _i),
@@ -488,6 +505,52 @@ def oidn_ffn_backward(dy, lddy: int, x, ldx: int, z, w_in, w_out, add, ldadd: in
     _check(lib().oidn_ffn_backward(_p(dy), lddy, _p(x), ldx, _p(z), _p(w_in), _p(w_out), _p(add), ldadd,
                                    _p(dx), lddx, _p(dw_in), _p(db_in), _p(dw_out), _p(db_out), m, d, f,
                                    act, dtype, flags, _p(workspace), ws_bytes, _s(stream)))
+
+
+# ------------------------------------------------- around a block over rows
+def oidn_norm(x, ldx: int, weight, shift, y, ldy: int, m: int, n: int, norm: int, eps: float, dtype: int,
+              stream=None):
+    _check(lib().oidn_norm(_p(x), ldx, _p(weight), _p(shift), _p(y), ldy, m, n, norm, eps, dtype, _s(stream)))
+
+
+def oidn_norm_backward_workspace_bytes(m: int, n: int, dtype: int) -> int:
+    return _size(lib().oidn_norm_backward_workspace_bytes, m, n, dtype)
+
+
+def oidn_norm_backward(dy, lddy: int, x, ldx: int, weight, add, ldadd: int, dx, lddx: int, dweight, dshift, m: int,
+                       n: int, norm: int, eps: float, dtype: int, workspace, ws_bytes: int, stream=None):
+    _check(lib().oidn_norm_backward(_p(dy), lddy, _p(x), ldx, _p(weight), _p(add), ldadd, _p(dx), lddx, _p(dweight),
+                                    _p(dshift), m, n, norm, eps, dtype, _p(workspace), ws_bytes, _s(stream)))
+
+
+def oidn_norm_residual(o, ldo: int, weight, shift, gate, ldg: int, gate_rows: int, x, ldx: int, scale: float,
+                       p: float, rng, u, ldu: int, next_weight, next_shift, v, ldv: int, m: int, n: int, norm: int,
+                       next_norm: int, eps: float, dtype: int, stream=None):
+    """rng: two 64-bit words in device memory (an int64 tensor of seed and offset)."""
+    _check(lib().oidn_norm_residual(_p(o), ldo, _p(weight), _p(shift), _p(gate), ldg, gate_rows, _p(x), ldx, scale,
+                                    p, _p(rng), _p(u), ldu, _p(next_weight), _p(next_shift), _p(v), ldv, m, n, norm,
+                                    next_norm, eps, dtype, _s(stream)))
+
+
+def oidn_norm_residual_backward_workspace_bytes(m: int, n: int, gate_rows: int, dtype: int) -> int:
+    return _size(lib().oidn_norm_residual_backward_workspace_bytes, m, n, gate_rows, dtype)
+
+
+def oidn_norm_residual_backward(du, lddu: int, dv, lddv: int, o, ldo: int, weight, shift, gate, ldg: int,
+                                gate_rows: int, u, ldu: int, scale: float, p: float, rng, next_weight, dx, lddx: int,
+                                d_o, lddo: int, dgate, lddg: int, dweight, dshift, dnext_weight, dnext_shift, m: int,
+                                n: int, norm: int, next_norm: int, eps: float, dtype: int, workspace, ws_bytes: int,
+                                stream=None):
+    _check(lib().oidn_norm_residual_backward(
+        _p(du), lddu, _p(dv), lddv, _p(o), ldo, _p(weight), _p(shift), _p(gate), ldg, gate_rows, _p(u), ldu, scale, p,
+        _p(rng), _p(next_weight), _p(dx), lddx, _p(d_o), lddo, _p(dgate), lddg, _p(dweight), _p(dshift),
+        _p(dnext_weight), _p(dnext_shift), m, n, norm, next_norm, eps, dtype, _p(workspace), ws_bytes, _s(stream)))
+
+
+def oidn_dropout(x, ldx: int, residual, ldr: int, y, ldy: int, m: int, n: int, p: float, rng, dtype: int,
+                 stream=None):
+    """rng: two 64-bit words in device memory (an int64 tensor of seed and offset)."""
+    _check(lib().oidn_dropout(_p(x), ldx, _p(residual), ldr, _p(y), ldy, m, n, p, _p(rng), dtype, _s(stream)))
 
 
 def oidn_calibrate_mfma(dtype: int, iters: int, blocks: int, sink, stream=None) -> int:

@@ -2,87 +2,12 @@
 // workspace layout and the launch sequences.  Nothing here allocates device
 // memory, waits for the device or throws.
 #include <algorithm>
-#include <cstdarg>
-#include <cstdio>
 
-#include "../../include/oidn_mi355x.h"
-#include "dense.h"
+#include "dense_checks.h"
 
 using namespace oidn;
 
 namespace {
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  return set_error(code, buf);
-}
-int ran(hipError_t e, const char* what) {
-  return e == hipSuccess ? OIDN_OK : fail(OIDN_E_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-// Limits: columns index with 32-bit ints, rows count with them where tiles do.
-// Whether a call's products fit a launch's grid is a matter of its plan
-// (check_launch).
-constexpr long kMaxColumns = 1L << 24;
-constexpr long kMaxRows = (1L << 31) - 1;
-constexpr long kMaxElements = 1L << 38;
-
-size_t esize(int dtype) { return dtype == OIDN_F32 ? 4 : 2; }
-size_t bytes_of(long rows, long cols, int dtype) {
-  return align256((size_t)rows * (size_t)cols * esize(dtype));
-}
-
-int check_type(int dtype) {
-  if (dtype == OIDN_F32 || dtype == OIDN_F16 || dtype == OIDN_BF16) return OIDN_OK;
-  return fail(OIDN_E_INVALID, "unknown dtype %d", dtype);
-}
-int check_size(const char* name, long rows, long cols) {
-  if (rows < 0 || cols < 1) return fail(OIDN_E_INVALID, "%s: %ld x %ld is not a size", name, rows, cols);
-  if (rows > kMaxRows || cols > kMaxColumns || rows > kMaxElements / cols)
-    return fail(OIDN_E_UNSUPPORTED, "%s: %ld x %ld is larger than the kernels index", name, rows, cols);
-  return OIDN_OK;
-}
-int check_act(int act) {
-  if (act >= OIDN_ACT_NONE && act <= OIDN_ACT_GELU) return OIDN_OK;
-  return fail(OIDN_E_INVALID, "unknown activation %d", act);
-}
-int check_flags(unsigned flags, unsigned known) {
-  if ((flags & ~known) == 0) return OIDN_OK;
-  return fail(OIDN_E_INVALID, "unknown flags 0x%x", flags & ~known);
-}
-int check_aligned(const char* name, const void* p, size_t to) {
-  if (reinterpret_cast<uintptr_t>(p) % to == 0) return OIDN_OK;
-  return fail(OIDN_E_INVALID, "%s must be aligned to %zu bytes", name, to);
-}
-// A matrix of `cols` columns at row pitch ld; may_be_null: absent is fine.
-int check_matrix(const char* name, const void* p, long ld, long cols, int dtype, bool may_be_null) {
-  if (!p) return may_be_null ? OIDN_OK : fail(OIDN_E_INVALID, "null pointer: %s", name);
-  if (ld < cols) return fail(OIDN_E_INVALID, "row pitch %ld of %s is less than its %ld columns", ld, name, cols);
-  if (ld > (1L << 32)) return fail(OIDN_E_UNSUPPORTED, "row pitch %ld of %s is above 2^32", ld, name);
-  return check_aligned(name, p, esize(dtype));
-}
-int check_blob(const char* name, const void* p) {
-  if (!p) return fail(OIDN_E_INVALID, "null pointer: %s", name);
-  return check_aligned(name, p, 16);
-}
-int check_workspace(const void* ws, size_t have, size_t need) {
-  if (need == 0) return OIDN_OK;
-  if (!ws) return fail(OIDN_E_INVALID, "null pointer: workspace");
-  const int rc = check_aligned("workspace", ws, 16);
-  if (rc) return rc;
-  if (have < need)
-    return fail(OIDN_E_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", have, need);
-  return OIDN_OK;
-}
-#define OIDN_TRY(expr)        \
-  do {                        \
-    const int rc_ = (expr);   \
-    if (rc_) return rc_;      \
-  } while (0)
 
 // One product: bytes of the workspace its slices take, and its launch.
 struct Product {
@@ -139,11 +64,6 @@ long slope_blocks(long rows, int cols, long chunk) {
   s.chunk = chunk;
   s.lanes = slope_lanes(cols);
   return slope_blocks(s);
-}
-// `blocks`: of the largest launch of a call.
-int check_launch(long blocks) {
-  if (blocks <= kMaxWorkgroups) return OIDN_OK;
-  return fail(OIDN_E_UNSUPPORTED, "%ld workgroups are more than the %ld of a launch", blocks, kMaxWorkgroups);
 }
 // Whether a 16-bit operand can go straight to LDS in 16-byte units: `extent`
 // is what its rows hold of (the summed length, or the output's rows or columns
@@ -269,27 +189,6 @@ struct Gradients {
     }
     if (summing) OIDN_TRY(ran(launch_slope(sums, {}, dtype, stream), "column sum launch"));
     return ran(launch_finish(finish, dtype, stream), "sums launch");
-  }
-};
-
-// The plain epilogue: store, with `add` (may be null) added.
-EpilogueArgs store_to(void* y, long ldy, const void* add, long ldadd) {
-  EpilogueArgs e{};
-  e.y = y;
-  e.ldy = ldy;
-  e.res = add;
-  e.ldr = ldadd;
-  return e;
-}
-
-// Workspace regions, handed out in order.
-struct Regions {
-  char* base;
-  size_t used;
-  void* take(size_t bytes) {
-    void* p = base ? base + used : nullptr;
-    used += bytes;
-    return p;
   }
 };
 

@@ -1,0 +1,88 @@
+// Internal declarations of what stands around a block over activation rows:
+// the norms before and after it with its gate and residual scale, and dropout.
+#pragma once
+
+#include "internal.h"
+
+namespace oidn {
+
+// Dropout: which elements are kept follows from the generator's state alone
+// (norm_rows.h).  threshold 0: nothing is dropped, the state is not read.
+struct Dropout {
+  unsigned threshold;              // of 65536: an element is kept where its 16 bits are not below
+  float gain;                      // of a kept element
+  const unsigned long long* rng;   // seed, offset
+};
+
+// u = scale x + gate drop(norm(o) weight + shift),  v = next_norm(u) next_weight + next_shift
+struct NormArgs {
+  const void* o;                   // null: u is x and is not stored
+  long ldo;
+  const float *weight, *shift;     // may be null
+  const float* gate;               // a row for every gate_rows rows, may be null
+  long ldg, gate_rows;
+  const void* x;
+  long ldx;
+  float scale;
+  Dropout drop;
+  void* u;
+  long ldu;
+  const float *next_weight, *next_shift;
+  void* v;                         // null: next_norm is OIDN_NORM_NONE
+  long ldv;
+  long m;
+  int n;
+  int norm, next_norm;
+  float eps;
+};
+
+// Rows in chunks that a workgroup goes through, such that a chunk either holds
+// whole gate groups or lies in one.
+struct NormChunks {
+  long rows;               // of a chunk
+  long per_group;          // chunks of a gate group; 0: a chunk holds whole groups
+  long group_rows;         // rows that share a gate, all of them without one
+  long count;
+};
+constexpr int kNormSums = 4;       // dweight, dshift, dnext_weight, dnext_shift
+// D = du + next_norm'(dv; u),  dx = scale D, and the branch's gradients
+struct NormBackArgs {
+  const void* du;                  // may be null
+  long lddu;
+  const void* dv;                  // null: next_norm is OIDN_NORM_NONE
+  long lddv;
+  const void* o;                   // null: no branch
+  long ldo;
+  const float *weight, *shift, *gate;
+  long ldg;
+  const void* u;                   // read where dv is
+  long ldu;
+  float scale;
+  Dropout drop;
+  const float* next_weight;
+  void* dx;                        // may be null, as the other results
+  long lddx;
+  void* d_o;
+  long lddo;
+  float* dgate;
+  long lddg;
+  float* sums[kNormSums];
+  float* rows;                     // workspace: kRowFloats of every row (wide rows)
+  float* part;                     // workspace: [chunk][kNormSums][n]
+  float* gate_part;                // workspace: [chunk][n]
+  NormChunks chunks;
+  long m;
+  int n;
+  int norm, next_norm;
+  float eps;
+};
+constexpr int kRowFloats = 8;
+
+NormChunks norm_chunks(long m, int n, long gate_rows);
+hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_norm_back(const NormBackArgs& a, int dtype, hipStream_t stream);
+// y = drop(x) + residual
+hipError_t launch_dropout(const void* x, long ldx, const void* residual, long ldr, void* y, long ldy, long m, int n,
+                          const Dropout& d, int dtype, hipStream_t stream);
+
+}  // namespace oidn

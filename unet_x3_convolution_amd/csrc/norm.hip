@@ -1,0 +1,50 @@
+// The norms before and after a block, forward, and dropout.
+#include "norm_wide.h"
+
+namespace oidn {
+namespace {
+
+// A thread takes eight columns.
+template <int DT>
+__global__ __launch_bounds__(kNormThreads) void dropout_rows(const void* x, long ldx, const void* residual, long ldr,
+                                                             void* y, long ldy, long m, int n, long units, Dropout d) {
+  const Generator random(d);
+  const long total = m * units, step = (long)gridDim.x * kNormThreads;
+  for (long t = (long)blockIdx.x * kNormThreads + threadIdx.x; t < total; t += step) {
+    const long i = t / units;
+    const int j = (int)(t - i * units) * 8;
+    Eight v = row8<DT>(x, ldx, i, j, m, n);
+    if (d.threshold) drop8(v, random.words(t), d);
+    if (residual) add8(v, row8<DT>(residual, ldr, i, j, m, n));
+    store8<DT>(y, i * ldy + j, v, n - j);
+  }
+}
+
+template <int DT>
+hipError_t launch_type(const NormArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.m < 65536 ? a.m : 65536));
+  hipLaunchKernelGGL(norm_wide<DT>, grid, dim3(kNormThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t stream) {
+  if (dtype == OIDN_F32) return launch_type<OIDN_F32>(a, stream);
+  return dtype == OIDN_F16 ? launch_type<OIDN_F16>(a, stream) : launch_type<OIDN_BF16>(a, stream);
+}
+
+hipError_t launch_dropout(const void* x, long ldx, const void* residual, long ldr, void* y, long ldy, long m, int n,
+                          const Dropout& d, int dtype, hipStream_t stream) {
+  const long units = (n + 7l) / 8, blocks = (m * units + kNormThreads - 1) / kNormThreads;
+  const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536)), block(kNormThreads);
+  if (dtype == OIDN_F32)
+    hipLaunchKernelGGL(dropout_rows<OIDN_F32>, grid, block, 0, stream, x, ldx, residual, ldr, y, ldy, m, n, units, d);
+  else if (dtype == OIDN_F16)
+    hipLaunchKernelGGL(dropout_rows<OIDN_F16>, grid, block, 0, stream, x, ldx, residual, ldr, y, ldy, m, n, units, d);
+  else
+    hipLaunchKernelGGL(dropout_rows<OIDN_BF16>, grid, block, 0, stream, x, ldx, residual, ldr, y, ldy, m, n, units, d);
+  return hipGetLastError();
+}
+
+}  // namespace oidn
