@@ -76,6 +76,8 @@ extern "C" {
 /* ---- flags of the dense operators ---------------------------------------- */
 #define OIDN_X_CKPT8  1u   /* x is a checkpoint (oidn_ckpt_pack), its pitch unused */
 #define OIDN_Z_CKPT8  2u   /* z is held in 8 bits                              */
+#define OIDN_FP8_SQUARE  4u  /* a scale for 128 x 128 values (weights)          */
+#define OIDN_X_FP8    8u   /* x is packed (oidn_fp8_pack), its pitch unused    */
 
 /* ---- limits ------------------------------------------------------------ */
 #define OIDN_MAX_SOURCE_CHANNELS 256   /* logical channels per conv source */
@@ -466,6 +468,51 @@ int oidn_ffn_backward(const void* dy, long lddy, const void* x, long ldx, const 
                       long lddx, void* dw_in, float* db_in, void* dw_out, float* db_out, long m, int d,
                       int f, int act, int dtype, unsigned flags, void* workspace, size_t ws_bytes,
                       hipStream_t stream);
+
+/* Dense layer in 8-bit floating point, with a scale for each block of 128 summed
+ * values.  Packed form of an m x n matrix: e4m3 codes (4 exponent bits, 3 mantissa
+ * bits, largest 448), then a scale 2^e per row and block of 128 columns,
+ *   e the least whole number with max|x| <= 448 2^e, held in [-120, 120],
+ *   code = x 2^-e rounded to nearest even, value = code 2^e.
+ * The scale is a power of two: it costs no precision, and the matrix cores apply it.
+ * Infinities and NaN become NaN, and the scale is that of the finite values.
+ * Layout: m rows of codes, padded with zeros to whole blocks; then for each row a
+ * byte e + 127 per block, padded to whole words of four bytes.  16-byte aligned.
+ * oidn_fp8_pack makes the packed form of x (m x n) and / or of its transpose (n x m,
+ * blocks of 128 rows of x): one of the two may be NULL.  With OIDN_FP8_SQUARE each
+ * 128 x 128 values share a scale, so that both hold the same values: for weights,
+ * which a forward pass sums over one way and a backward pass the other.
+ * oidn_fp8_unpack gives the values; a finite one that the rounding carried past the
+ * range of dtype becomes the largest. */
+int oidn_fp8_bytes(long m, long n, size_t* bytes);
+int oidn_fp8_pack(const void* x, long ldx, long m, long n, void* packed, void* packed_t, int dtype,
+                  unsigned flags, hipStream_t stream);
+int oidn_fp8_unpack(const void* packed, long m, long n, void* y, long ldy, int dtype, hipStream_t stream);
+
+/* The layer of oidn_linear on packed values:
+ *   z = [x] [w]^T + bias,  y = act(z) + residual,  [.] the packed form's values
+ * w8: the packed weights (n x k).  x: m x k of dtype, packed inside, or with
+ * OIDN_X_FP8 a packed matrix.  dtype: OIDN_F16 or OIDN_BF16.  The products of codes
+ * are added eight at a time with 13 bits below the largest, those sums in fp32:
+ * 1e-5 to 4e-5 of the result, far below the storage type's rounding.
+ * k, n <= 2^23.  The rest is as for oidn_linear. */
+int oidn_linear_fp8_workspace_bytes(long m, int k, int n, int dtype, unsigned flags, size_t* bytes);
+int oidn_linear_fp8(const void* x, long ldx, const void* w8, const float* bias, const void* residual,
+                    long ldr, void* y, long ldy, void* z, long ldz, long m, int k, int n, int act,
+                    int dtype, unsigned flags, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Its gradients, with dz = dy act'(z) not rounded before it is coded:
+ *   dx = [dz] [w],  dw = [dz^T] [x^T]^T,  dbias = sum of dz's rows
+ * [dz]: blocks of 128 along a row; [dz^T], [x^T]: blocks of 128 rows of a column.
+ * w8t: the packed transpose of w (k x n), of the same call with OIDN_FP8_SQUARE as the
+ * forward pass's w8.  x: m x k of dtype, or with OIDN_X_FP8 its packed transpose
+ * (k x m), which a forward pass may keep in place of x.  m <= 2^23. */
+int oidn_linear_fp8_backward_workspace_bytes(long m, int k, int n, int act, int dtype, unsigned flags,
+                                             size_t* bytes);
+int oidn_linear_fp8_backward(const void* dy, long lddy, const void* x, long ldx, const void* z, long ldz,
+                             const void* w8t, void* dx, long lddx, void* dw, long lddw, float* dbias,
+                             long m, int k, int n, int act, int dtype, unsigned flags, void* workspace,
+                             size_t ws_bytes, hipStream_t stream);
 
 /* ========================================================================
  * What stands around a block over activation rows: the norm before it, and the

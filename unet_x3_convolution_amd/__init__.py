@@ -42,6 +42,8 @@ OIDN_NORM_LAYER = 2
 
 OIDN_X_CKPT8 = 1
 OIDN_Z_CKPT8 = 2
+OIDN_FP8_SQUARE = 4
+OIDN_X_FP8 = 8
 
 OIDN_TILE_ALIGN = 16
 OIDN_DEFAULT_OVERLAP = 96
@@ -60,6 +62,8 @@ EXPORTS = (
     "oidn_ckpt_bytes", "oidn_ckpt_pack", "oidn_ckpt_unpack",
     "oidn_linear_workspace_bytes", "oidn_linear", "oidn_linear_backward_workspace_bytes", "oidn_linear_backward",
     "oidn_ffn_workspace_bytes", "oidn_ffn", "oidn_ffn_backward_workspace_bytes", "oidn_ffn_backward",
+    "oidn_fp8_bytes", "oidn_fp8_pack", "oidn_fp8_unpack", "oidn_linear_fp8_workspace_bytes", "oidn_linear_fp8",
+    "oidn_linear_fp8_backward_workspace_bytes", "oidn_linear_fp8_backward",
     "oidn_norm", "oidn_norm_backward_workspace_bytes", "oidn_norm_backward", "oidn_norm_residual",
     "oidn_norm_residual_backward_workspace_bytes", "oidn_norm_residual_backward", "oidn_dropout",
     "oidn_calibrate_mfma", "oidn_calibrate_read", "oidn_event_create", "oidn_event_destroy", "oidn_event_elapsed_ms",
@@ -135,6 +139,14 @@ _SIGS = {
     "oidn_ffn_backward_workspace_bytes": ([_l, _i, _i, _i, _u, ctypes.POINTER(_sz)], _i),
     "oidn_ffn_backward": ([_vp, _l, _vp, _l, _vp, _vp, _vp, _vp, _l, _vp, _l, _vp, _vp, _vp, _vp, _l, _i, _i,
                            _i, _i, _u, _vp, _sz, _vp], _i),
+    "oidn_fp8_bytes": ([_l, _l, ctypes.POINTER(_sz)], _i),
+    "oidn_fp8_pack": ([_vp, _l, _l, _l, _vp, _vp, _i, _u, _vp], _i),
+    "oidn_fp8_unpack": ([_vp, _l, _l, _vp, _l, _i, _vp], _i),
+    "oidn_linear_fp8_workspace_bytes": ([_l, _i, _i, _i, _u, ctypes.POINTER(_sz)], _i),
+    "oidn_linear_fp8": ([_vp, _l, _vp, _vp, _vp, _l, _vp, _l, _vp, _l, _l, _i, _i, _i, _i, _u, _vp, _sz, _vp], _i),
+    "oidn_linear_fp8_backward_workspace_bytes": ([_l, _i, _i, _i, _i, _u, ctypes.POINTER(_sz)], _i),
+    "oidn_linear_fp8_backward": ([_vp, _l, _vp, _l, _vp, _l, _vp, _vp, _l, _vp, _l, _vp, _l, _i, _i, _i, _i, _u,
+                                  _vp, _sz, _vp], _i),
     "oidn_norm": ([_vp, _l, _vp, _vp, _vp, _l, _l, _i, _i, _f, _i, _vp], _i),
     "oidn_norm_backward_workspace_bytes": ([_l, _i, _i, ctypes.POINTER(_sz)], _i),
     "oidn_norm_backward": ([_vp, _l, _vp, _l, _vp, _vp, _l, _vp, _l, _vp, _vp, _l, _i, _i, _f, _i, _vp, _sz,
@@ -505,6 +517,40 @@ def oidn_ffn_backward(dy, lddy: int, x, ldx: int, z, w_in, w_out, add, ldadd: in
     _check(lib().oidn_ffn_backward(_p(dy), lddy, _p(x), ldx, _p(z), _p(w_in), _p(w_out), _p(add), ldadd,
                                    _p(dx), lddx, _p(dw_in), _p(db_in), _p(dw_out), _p(db_out), m, d, f,
                                    act, dtype, flags, _p(workspace), ws_bytes, _s(stream)))
+
+
+def oidn_fp8_bytes(m: int, n: int) -> int:
+    return _size(lib().oidn_fp8_bytes, m, n)
+
+
+def oidn_fp8_pack(x, ldx: int, m: int, n: int, packed, packed_t, dtype: int, flags: int, stream=None):
+    _check(lib().oidn_fp8_pack(_p(x), ldx, m, n, _p(packed), _p(packed_t), dtype, flags, _s(stream)))
+
+
+def oidn_fp8_unpack(packed, m: int, n: int, y, ldy: int, dtype: int, stream=None):
+    _check(lib().oidn_fp8_unpack(_p(packed), m, n, _p(y), ldy, dtype, _s(stream)))
+
+
+def oidn_linear_fp8_workspace_bytes(m: int, k: int, n: int, dtype: int, flags: int) -> int:
+    return _size(lib().oidn_linear_fp8_workspace_bytes, m, k, n, dtype, flags)
+
+
+def oidn_linear_fp8(x, ldx: int, w8, bias, residual, ldr: int, y, ldy: int, z, ldz: int, m: int, k: int, n: int,
+                    act: int, dtype: int, flags: int, workspace, ws_bytes: int, stream=None):
+    _check(lib().oidn_linear_fp8(_p(x), ldx, _p(w8), _p(bias), _p(residual), ldr, _p(y), ldy, _p(z), ldz, m, k, n,
+                                 act, dtype, flags, _p(workspace), ws_bytes, _s(stream)))
+
+
+def oidn_linear_fp8_backward_workspace_bytes(m: int, k: int, n: int, act: int, dtype: int, flags: int) -> int:
+    return _size(lib().oidn_linear_fp8_backward_workspace_bytes, m, k, n, act, dtype, flags)
+
+
+def oidn_linear_fp8_backward(dy, lddy: int, x, ldx: int, z, ldz: int, w8t, dx, lddx: int, dw, lddw: int, dbias,
+                             m: int, k: int, n: int, act: int, dtype: int, flags: int, workspace, ws_bytes: int,
+                             stream=None):
+    _check(lib().oidn_linear_fp8_backward(_p(dy), lddy, _p(x), ldx, _p(z), ldz, _p(w8t), _p(dx), lddx, _p(dw), lddw,
+                                          _p(dbias), m, k, n, act, dtype, flags, _p(workspace), ws_bytes,
+                                          _s(stream)))
 
 
 # ------------------------------------------------- around a block over rows
