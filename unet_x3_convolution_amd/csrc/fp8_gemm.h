@@ -41,17 +41,43 @@ __device__ __forceinline__ void mfma8_acc(floatx4& c, const intx8& a, const intx
         : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb));
 }
 
-// Workgroup `block` of the product; lds: gemm16_lds<T, T>() bytes, two buffers of a P
-// and a Q tile.  Slices begin at multiples of four staged tiles, whose scales are a
-// word.
+// LDS: two buffers of a P tile, two of a Q tile, then two of the rows' scales, a word
+// of each for four staged tiles.  (In this order a fragment's place in either buffer
+// is an immediate offset of one address.)
+template <int T>
+constexpr int gemm8_lds() { return 4 * T * kFp8Block + 2 * 2 * T * 4; }
+
+// 4 bytes per lane to LDS byte address `lds` + 4 * lane from base + off; as copy16.
+__device__ __forceinline__ void copy4(const void* base, unsigned off, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory");
+}
+
+// Workgroup `block` of the product; lds: gemm8_lds<T>() bytes.  Slices begin at
+// multiples of four staged tiles.
+//
+// A wave's F x F fragments are multiplied in four quarters, P's halves by Q's, such
+// that what a quarter needs is read from LDS a quarter earlier and only F + F
+// fragments' registers are held:
+//   A  P0 Q0   reads Q1
+//   B  P0 Q1   reads P1; then a wait for the copies of tile t + 1 and a barrier: all
+//              of tile t is in registers
+//   C  P1 Q1   reads P0 of tile t + 1; copies of tile t + 2 over tile t
+//   D  P1 Q0   reads Q0 of tile t + 1 in Q1's place; copies
+// (every fourth tile C and D read the next word of scales too)
+// so that Q's halves change places from tile to tile, and a copy has a whole tile's
+// multiplications to arrive.  Within a quarter the order is fixed (sched_barrier): a
+// fragment's reads and some copies, then a row of multiplications.
 template <bool BF, int EPI, int T, Caching WHERE>
 __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds) {
   const GemmArgs& a = a8.g;
   constexpr int DT = BF ? OIDN_BF16 : OIDN_F16;
-  constexpr int F = T / 32;                      // 16-wide fragments per wave, each way
+  constexpr int F = T / 32, H = F / 2;           // 16-wide fragments per wave each way, half of them
   typedef Direct16<T, false> D;
   typedef typename D::S S;
-  constexpr unsigned kBuf = 2 * S::kBytes;
+  constexpr unsigned kBuf = S::kBytes;           // from one buffer of an operand to the other
+  constexpr unsigned kScales = 4 * S::kBytes, kScaleBuf = 2 * T * 4;
+  constexpr int kCopiesAStep = D::kCopies / H;
 
   int tc, tr, slice;
   if (!tile_and_slice(a, block, tc, tr, slice)) return;
@@ -63,18 +89,36 @@ __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds)
   const unsigned lds_at = (unsigned)(unsigned long)(__attribute__((address_space(3))) void*)lds;
   D p, q;
   p.init(a.p, a.ldp, j0, a.e.cols, t0 * kDenseK, 0, lds_at);
-  q.init(a.q, a.ldq, i0, a.e.rows, t0 * kDenseK, 0, lds_at + S::kBytes);
+  q.init(a.q, a.ldq, i0, a.e.rows, t0 * kDenseK, 0, lds_at + 2 * S::kBytes);
 
-  // this lane's rows' scales, four staged tiles a word
-  const unsigned char *sp[F], *sq[F];
+  // The scales' copies: 64 rows of an operand each, shared by the waves.
+  constexpr int kScaleCopies = 2 * T / 64, kScaleTurns = (kScaleCopies + 3) / 4;
+  unsigned scale_off[kScaleTurns];
 #pragma unroll
-  for (int f = 0; f < F; ++f) {
-    const long j = j0 + wc * (T / 2) + 32 * (f / 2) + 8 * (r >> 2) + 4 * (f & 1) + (r & 3), last = a.e.cols - 1l;
-    sp[f] = a8.ps + (j < last ? j : last) * a8.pn;
-    const long i = i0 + wr * (T / 2) + 16 * f + r;
-    sq[f] = a8.qs + (i < a.e.rows - 1 ? i : a.e.rows - 1) * a8.qn;
+  for (int k = 0; k < kScaleTurns; ++k) {
+    const int c = wave + 4 * k, row = 64 * (c % (T / 64)) + lane;
+    const bool of_p = c < T / 64;
+    const long last = of_p ? a.e.cols - 1 - j0 : a.e.rows - 1 - i0;
+    scale_off[k] = (unsigned)((row < last ? row : last) * (of_p ? a8.pn : a8.qn));
   }
+  const unsigned char* const ps = a8.ps + j0 * a8.pn;
+  const unsigned char* const qs = a8.qs + i0 * a8.qn;
+  // the word of tiles t .. t + 3 (t a multiple of 4)
+  auto copy_scales = [&](long t, unsigned buf) {
+#pragma unroll
+    for (int k = 0; k < kScaleTurns; ++k) {
+      const int c = __builtin_amdgcn_readfirstlane(wave + 4 * k);
+      if (c < kScaleCopies) copy4((c < T / 64 ? ps : qs) + t, scale_off[k], lds_at + kScales + buf + 256 * c);
+    }
+  };
   unsigned up[F], uq[F];
+  auto read_up = [&](int f, unsigned buf) {
+    up[f] = *reinterpret_cast<const unsigned*>(lds + kScales + buf + 4 * (wc * (T / 2) + 32 * (f / 2) + 8 * (r >> 2) +
+                                                                       4 * (f & 1) + (r & 3)));
+  };
+  auto read_uq = [&](int f, unsigned buf) {
+    uq[f] = *reinterpret_cast<const unsigned*>(lds + kScales + buf + 4 * T + 4 * (wr * (T / 2) + 16 * f + r));
+  };
 
   floatx4 acc[F][F];
 #pragma unroll
@@ -82,6 +126,87 @@ __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds)
 #pragma unroll
     for (int k = 0; k < F; ++k) acc[c][k] = floatx4{0.f, 0.f, 0.f, 0.f};
 
+  intx8 fp[F], fq[F];
+  auto both = [](uint4 lo, uint4 hi) {
+    return intx8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  };
+  auto read_p = [&](int c, unsigned buf) {
+    const int base = wc * (T / 2) + 32 * (c / 2);
+    fp[c] = both(S::template fragment<true>(lds + buf, base, c & 1, 0), S::template fragment<true>(lds + buf, base, c & 1, 1));
+  };
+  auto read_q = [&](int place, int k, unsigned buf) {
+    const char* const l = lds + buf + 2 * S::kBytes;
+    fq[place] = both(S::template fragment<false>(l, wr * (T / 2), k, 0), S::template fragment<false>(l, wr * (T / 2), k, 1));
+  };
+  auto wait_all = [&] {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Tile t of a word's four: its scales are in byte `byte`, Q's first half in
+  // fq[byte % 2 * H ..].  full: tiles t + 1 and t + 2 exist; cur, scales: their buffers.
+  auto tile = [&](auto byte, auto full, long t, unsigned cur, unsigned scales) {
+    constexpr int kByte = decltype(byte)::value, X = kByte % 2 * H, Y = H - X;
+    constexpr bool kFull = decltype(full)::value;
+    const bool one_more = kFull || t + 1 < t1, two_more = kFull || t + 2 < t1;
+    const unsigned next = kBuf - cur;
+    auto row = [&](int c, int place, int k0) {       // H multiplications
+#pragma unroll
+      for (int k = 0; k < H; ++k) mfma8_acc<kByte>(acc[c][k0 + k], fp[c], fq[place + k], up[c], uq[k0 + k]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < H; ++s) {
+      read_q(Y + s, H + s, cur);
+      row(s, X, 0);
+    }
+#pragma unroll
+    for (int s = 0; s < H; ++s) {
+      read_p(H + s, cur);
+      row(s, Y, H);
+    }
+    wait_all();
+    if constexpr (kByte == 0) {
+      // read three tiles on; what it overwrites was read at the end of the last word
+      if (t + 4 < t1) copy_scales(t + 4, kScaleBuf - scales);
+    }
+#pragma unroll
+    for (int s = 0; s < H; ++s) {
+      if (one_more) {
+        read_p(s, next);
+        if constexpr (kByte == 3) read_up(s, kScaleBuf - scales);
+      }
+      if (two_more) {
+#pragma unroll
+        for (int n = 0; n < kCopiesAStep; ++n) p.copy(s * kCopiesAStep + n, cur);
+      }
+      row(H + s, Y, H);
+    }
+#pragma unroll
+    for (int s = 0; s < H; ++s) {
+      if (one_more) {
+        read_q(Y + s, s, next);
+        if constexpr (kByte == 3) read_uq(H + s, kScaleBuf - scales);
+      }
+      if (two_more) {
+#pragma unroll
+        for (int n = 0; n < kCopiesAStep; ++n) q.copy(s * kCopiesAStep + n, cur);
+      }
+      row(H + s, X, 0);
+    }
+    p.advance();
+    q.advance();
+    if constexpr (kByte == 3) {
+      // their old values were in use until here
+#pragma unroll
+      for (int f = 0; f < H; ++f) {
+        read_up(H + f, kScaleBuf - scales);
+        read_uq(f, kScaleBuf - scales);
+      }
+    }
+  };
   auto stage = [&](unsigned buf) {
 #pragma unroll
     for (int n = 0; n < D::kCopies; ++n) {
@@ -91,69 +216,58 @@ __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds)
     p.advance();
     q.advance();
   };
-  auto both = [](uint4 lo, uint4 hi) {
-    return intx8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-  };
-  auto wait_all = [&] {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto multiply = [&](auto byte, unsigned buf) {
-    constexpr int kByte = decltype(byte)::value;
-    const char* const l = lds + buf;
-    intx8 fq[F];
-#pragma unroll
-    for (int k = 0; k < F; ++k)
-      fq[k] = both(S::template fragment<false>(l + S::kBytes, wr * (T / 2), k, 0),
-                   S::template fragment<false>(l + S::kBytes, wr * (T / 2), k, 1));
-#pragma unroll
-    for (int c = 0; c < F; ++c) {
-      const int base = wc * (T / 2) + 32 * (c / 2);
-      const intx8 fp = both(S::template fragment<true>(l, base, c & 1, 0), S::template fragment<true>(l, base, c & 1, 1));
-#pragma unroll
-      for (int k = 0; k < F; ++k) mfma8_acc<kByte>(acc[c][k], fp, fq[k], up[c], uq[k]);
-    }
-  };
 
+  copy_scales(t0, 0);
   stage(0);
-  unsigned cur = 0;
-  for (long t = t0; t < t1; ++t) {
-    wait_all();                                  // tile t is there, and every wave has read tile t - 1
-    if (((t - t0) & 3) == 0) {
+  if (t0 + 1 < t1) stage(kBuf);
+  wait_all();
 #pragma unroll
-      for (int f = 0; f < F; ++f) {
-        up[f] = *reinterpret_cast<const unsigned*>(sp[f] + t);
-        uq[f] = *reinterpret_cast<const unsigned*>(sq[f] + t);
-      }
-    }
-    if (t + 1 < t1) stage(kBuf - cur);
-    switch ((int)(t - t0) & 3) {
-      case 0: multiply(std::integral_constant<int, 0>{}, cur); break;
-      case 1: multiply(std::integral_constant<int, 1>{}, cur); break;
-      case 2: multiply(std::integral_constant<int, 2>{}, cur); break;
-      default: multiply(std::integral_constant<int, 3>{}, cur);
-    }
-    cur = kBuf - cur;
+  for (int f = 0; f < F; ++f) {
+    read_up(f, 0);
+    read_uq(f, 0);
+  }
+#pragma unroll
+  for (int f = 0; f < H; ++f) {
+    read_p(f, 0);
+    read_q(f, f, 0);
+  }
+  constexpr std::integral_constant<int, 0> kB0{};
+  constexpr std::integral_constant<int, 1> kB1{};
+  constexpr std::integral_constant<int, 2> kB2{};
+  constexpr std::integral_constant<int, 3> kB3{};
+  long t = t0;
+  unsigned scales = 0;
+  for (; t + 5 < t1; t += 4) {
+    tile(kB0, std::true_type{}, t, 0, scales);
+    tile(kB1, std::true_type{}, t + 1, kBuf, scales);
+    tile(kB2, std::true_type{}, t + 2, 0, scales);
+    tile(kB3, std::true_type{}, t + 3, kBuf, scales);
+    scales = kScaleBuf - scales;
+  }
+  for (; t < t1; t += 4) {
+    tile(kB0, std::false_type{}, t, 0, scales);
+    if (t + 1 < t1) tile(kB1, std::false_type{}, t + 1, kBuf, scales);
+    if (t + 2 < t1) tile(kB2, std::false_type{}, t + 2, 0, scales);
+    if (t + 3 < t1) tile(kB3, std::false_type{}, t + 3, kBuf, scales);
+    scales = kScaleBuf - scales;
   }
 #pragma unroll
   for (int c = 0; c < F; c += 2)
 #pragma unroll
     for (int k = 0; k < F; k += 2) settle(acc[c][k], acc[c][k + 1], acc[c + 1][k], acc[c + 1][k + 1]);
-  __syncthreads();
+  __syncthreads();                       // every wave has read its last fragments
   tile_epilogue<DT, EPI, F, F, false, WHERE>(a.e, acc, lds + wave * epilogue_bytes<F, F>(), i0 + wr * (T / 2),
                                              (int)j0 + wc * (T / 2), a.splits > 1 ? slice : -1, (long)tr * 2 + wr);
 }
 
 template <bool BF, int T, Caching WHERE>
 __global__ __launch_bounds__(256, workgroups_per_cu(T, T)) void dense_gemm8(Gemm8Args a) {
-  __shared__ __attribute__((aligned(1024))) char lds[gemm16_lds<T, T>()];
+  __shared__ __attribute__((aligned(1024))) char lds[gemm8_lds<T>()];
   gemm8<BF, kEpiLinear, T, WHERE>(a, blockIdx.x, lds);
 }
 template <bool BF, int T>
 __global__ __launch_bounds__(256, workgroups_per_cu(T, T)) void dense_gemm8_group(Gemm8Group g) {
-  __shared__ __attribute__((aligned(1024))) char lds[gemm16_lds<T, T>()];
+  __shared__ __attribute__((aligned(1024))) char lds[gemm8_lds<T>()];
   const int k = g.count > 1 && (int)blockIdx.x >= g.start[1] ? 1 : 0;
   gemm8<BF, kEpiStore, T, kEither>(g.a[k], blockIdx.x - g.start[k], lds);
 }
