@@ -29,7 +29,8 @@ struct Fp8PackArgs {
   int square;              // a scale for 128 x 128
   float* sums;             // column sums of each 128 rows before coding: [row block][n], may be null
 };
-long fp8_pack_blocks(long m, long n);
+long fp8_pack_blocks(long m, long n);      // at most
+inline long fp8_tiles(long m, long n) { return ((m + kFp8Block - 1) / kFp8Block) * (fp8_cols(n) / kFp8Block); }
 // Packs a and b in one launch (b.x null: a alone).
 hipError_t launch_fp8_pack(const Fp8PackArgs& a, const Fp8PackArgs& b, int dtype, hipStream_t stream);
 hipError_t launch_fp8_unpack(const void* packed, long m, long n, void* y, long ldy, int dtype, hipStream_t stream);
@@ -47,6 +48,9 @@ struct Gemm8Group {
   int start[kMaxGroup8];
   Gemm8Args a[kMaxGroup8];
 };
+// Forward products of at most kFewRows rows, in one launch; packed: g.q is packed, else a
+// matrix of dtype, k columns at pitch g.ldq.
+hipError_t launch_few8(const Gemm8Args& a, int k, bool packed, bool bf16, hipStream_t stream);
 // kEpiLinear, and kEpiStore for a group; 16-bit results.
 hipError_t launch_gemm8(const Gemm8Args& a, int tile, bool bf16, hipStream_t stream);
 hipError_t launch_gemm8_group(const Gemm8Group& g, int blocks, int tile, bool bf16, hipStream_t stream);

@@ -82,6 +82,7 @@ Gemm8Args gemm8_args(const Product8& p, const void* q, const void* pm, const Epi
 }
 
 struct Forward {
+  bool few;                // at most kFewRows rows: one launch, no workspace
   Product8 p;
   void *x8, *slices;
   size_t bytes;
@@ -89,6 +90,11 @@ struct Forward {
 Forward forward(long m, int k, int n, unsigned flags, void* ws) {
   Forward f{};
   f.p = product8(m, n, k);
+  f.few = m <= kFewRows;
+  if (f.few) {
+    f.p.plan = GemmPlan{64, 64, true, true, 1, 0};
+    return f;
+  }
   Product8* one = &f.p;
   plan_together(&one, 1);
   Regions r{static_cast<char*>(ws), 0};
@@ -98,6 +104,7 @@ Forward forward(long m, int k, int n, unsigned flags, void* ws) {
   return f;
 }
 int check_forward_launch(const Forward& f, long m, int k) {
+  if (f.few) return OIDN_OK;
   return check_launch(std::max({most_blocks(f.p), sum_blocks(f.p), f.x8 ? fp8_pack_blocks(m, k) : 0}));
 }
 
@@ -201,7 +208,7 @@ int oidn_linear_fp8(const void* x, long ldx, const void* w8, const float* bias, 
   const Forward f = forward(m, k, n, flags, workspace);
   OIDN_TRY(check_forward_launch(f, m, k));
   OIDN_TRY(check_workspace(workspace, ws_bytes, f.bytes));
-  if (!x8) {
+  if (!x8 && !f.few) {
     Fp8PackArgs a{};
     a.x = x;
     a.ldx = ldx;
@@ -217,7 +224,12 @@ int oidn_linear_fp8(const void* x, long ldx, const void* w8, const float* bias, 
   e.ldz = ldz;
   e.z8 = z8;
   e.act = act;
-  const Gemm8Args g = gemm8_args(f.p, x, w8, e, f.slices);
+  Gemm8Args g = gemm8_args(f.p, x, w8, e, f.slices);
+  if (f.few) {
+    if (!x8) g.g.ldq = ldx;
+    OIDN_TRY(ran(launch_few8(g, k, x8, dtype == OIDN_BF16, stream), "8-bit product launch"));
+    return clear_error();
+  }
   OIDN_TRY(ran(launch_gemm8(g, f.p.plan.tile_r, dtype == OIDN_BF16, stream), "8-bit product launch"));
   if (f.p.plan.splits > 1)
     OIDN_TRY(ran(launch_split_sum(g.g.e, f.p.plan.splits, dtype, stream), "slice sum launch"));

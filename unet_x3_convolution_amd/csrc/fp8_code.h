@@ -36,19 +36,16 @@ __device__ __forceinline__ int fp8_power(unsigned top) {
   return e < -120 ? -120 : e > 120 ? 120 : e;
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
-// Eight codes of x 2^-e, nearest even; `inverse` is 2^-e.
-__device__ __forceinline__ uint2 fp8_codes(const float (&x)[8], float inverse) {
-  float v[8];
+// Codes of x 2^-e, nearest even; `inverse` is 2^-e.
+__device__ __forceinline__ unsigned fp8_codes4(const float* x, float inverse) {
+  float v[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    v[k] = x[k] * inverse;
-    v[k] = __builtin_fabsf(x[k]) < __builtin_inff() ? v[k] : __builtin_nanf("");
-  }
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
-  return make_uint2((unsigned)lo, (unsigned)hi);
+  for (int k = 0; k < 4; ++k) v[k] = __builtin_fabsf(x[k]) < __builtin_inff() ? x[k] * inverse : __builtin_nanf("");
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+}
+__device__ __forceinline__ uint2 fp8_codes(const float (&x)[8], float inverse) {
+  return make_uint2(fp8_codes4(x, inverse), fp8_codes4(x + 4, inverse));
 }
 __device__ __forceinline__ Eight fp8_values(uint2 c, float scale) {
   typedef float floatx2 __attribute__((ext_vector_type(2)));

@@ -59,15 +59,15 @@ __device__ __forceinline__ void copy4(const void* base, unsigned off, unsigned l
 // A wave's F x F fragments are multiplied in four quarters, P's halves by Q's, such
 // that what a quarter needs is read from LDS a quarter earlier and only F + F
 // fragments' registers are held:
-//   A  P0 Q0   reads Q1
-//   B  P0 Q1   reads P1; then a wait for the copies of tile t + 1 and a barrier: all
-//              of tile t is in registers
-//   C  P1 Q1   reads P0 of tile t + 1; copies of tile t + 2 over tile t
-//   D  P1 Q0   reads Q0 of tile t + 1 in Q1's place; copies
+//   A  P0 Q0   reads Q1 and P1; then a wait for the copies of tile t + 1 and a barrier:
+//              all of tile t is in registers
+//   B  P0 Q1   copies of tile t + 2 over tile t
+//   C  P1 Q1   reads P0 of tile t + 1
+//   D  P1 Q0   reads Q0 of tile t + 1 in Q1's place
 // (every fourth tile C and D read the next word of scales too)
 // so that Q's halves change places from tile to tile, and a copy has a whole tile's
 // multiplications to arrive.  Within a quarter the order is fixed (sched_barrier): a
-// fragment's reads and some copies, then a row of multiplications.
+// read or a copy, then a multiplication, under whose 32 cycles the next one issues.
 template <bool BF, int EPI, int T, Caching WHERE>
 __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds) {
   const GemmArgs& a = a8.g;
@@ -77,7 +77,6 @@ __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds)
   typedef typename D::S S;
   constexpr unsigned kBuf = S::kBytes;           // from one buffer of an operand to the other
   constexpr unsigned kScales = 4 * S::kBytes, kScaleBuf = 2 * T * 4;
-  constexpr int kCopiesAStep = D::kCopies / H;
 
   int tc, tr, slice;
   if (!tile_and_slice(a, block, tc, tr, slice)) return;
@@ -127,16 +126,15 @@ __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds)
     for (int k = 0; k < F; ++k) acc[c][k] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   intx8 fp[F], fq[F];
-  auto both = [](uint4 lo, uint4 hi) {
-    return intx8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  // half h of a fragment: 16 bytes a lane
+  auto put = [](intx8& f, int h, uint4 v) {
+    f[4 * h] = (int)v.x, f[4 * h + 1] = (int)v.y, f[4 * h + 2] = (int)v.z, f[4 * h + 3] = (int)v.w;
   };
-  auto read_p = [&](int c, unsigned buf) {
-    const int base = wc * (T / 2) + 32 * (c / 2);
-    fp[c] = both(S::template fragment<true>(lds + buf, base, c & 1, 0), S::template fragment<true>(lds + buf, base, c & 1, 1));
+  auto read_p = [&](int c, int h, unsigned buf) {
+    put(fp[c], h, S::template fragment<true>(lds + buf, wc * (T / 2) + 32 * (c / 2), c & 1, h));
   };
-  auto read_q = [&](int place, int k, unsigned buf) {
-    const char* const l = lds + buf + 2 * S::kBytes;
-    fq[place] = both(S::template fragment<false>(l, wr * (T / 2), k, 0), S::template fragment<false>(l, wr * (T / 2), k, 1));
+  auto read_q = [&](int place, int k, int h, unsigned buf) {
+    put(fq[place], h, S::template fragment<false>(lds + buf + 2 * S::kBytes, wr * (T / 2), k, h));
   };
   auto wait_all = [&] {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -151,51 +149,52 @@ __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds)
     constexpr bool kFull = decltype(full)::value;
     const bool one_more = kFull || t + 1 < t1, two_more = kFull || t + 2 < t1;
     const unsigned next = kBuf - cur;
-    auto row = [&](int c, int place, int k0) {       // H multiplications
+    // A quarter's H x H multiplications, P's half from c0 on by Q's at `place`, and one
+    // other instruction before each: op(0) .. op(H * H - 1).
+    auto quarter = [&](int c0, int place, int k0, auto op) {
 #pragma unroll
-      for (int k = 0; k < H; ++k) mfma8_acc<kByte>(acc[c][k0 + k], fp[c], fq[place + k], up[c], uq[k0 + k]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int n = 0; n < H * H; ++n) {
+        op(n);
+        mfma8_acc<kByte>(acc[c0 + n / H][k0 + n % H], fp[c0 + n / H], fq[place + n % H], up[c0 + n / H], uq[k0 + n % H]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // spread(n, count, f): f of the step-n share of `count` things
+    auto spread = [](int n, int count, auto f) {
+#pragma unroll
+      for (int i = n * count / (H * H); i < (n + 1) * count / (H * H); ++i) f(i);
     };
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int s = 0; s < H; ++s) {
-      read_q(Y + s, H + s, cur);
-      row(s, X, 0);
-    }
-#pragma unroll
-    for (int s = 0; s < H; ++s) {
-      read_p(H + s, cur);
-      row(s, Y, H);
-    }
+    quarter(0, X, 0, [&](int n) {
+      spread(n, 4 * H, [&](int i) {
+        if (i < 2 * H) read_q(Y + i / 2, H + i / 2, i % 2, cur);
+        else read_p(i / 2, i % 2, cur);
+      });
+    });
     wait_all();
     if constexpr (kByte == 0) {
       // read three tiles on; what it overwrites was read at the end of the last word
       if (t + 4 < t1) copy_scales(t + 4, kScaleBuf - scales);
     }
-#pragma unroll
-    for (int s = 0; s < H; ++s) {
+    quarter(0, Y, H, [&](int n) {
+      if (two_more)
+        spread(n, 2 * D::kCopies, [&](int i) {
+          if (i % 2 == 0) p.copy(i / 2, cur);
+          else q.copy(i / 2, cur);
+        });
+    });
+    quarter(H, Y, H, [&](int n) {
       if (one_more) {
-        read_p(s, next);
-        if constexpr (kByte == 3) read_up(s, kScaleBuf - scales);
+        spread(n, 2 * H, [&](int i) { read_p(i / 2, i % 2, next); });
+        if constexpr (kByte == 3) spread(n, H, [&](int i) { read_up(i, kScaleBuf - scales); });
       }
-      if (two_more) {
-#pragma unroll
-        for (int n = 0; n < kCopiesAStep; ++n) p.copy(s * kCopiesAStep + n, cur);
-      }
-      row(H + s, Y, H);
-    }
-#pragma unroll
-    for (int s = 0; s < H; ++s) {
+    });
+    quarter(H, X, 0, [&](int n) {
       if (one_more) {
-        read_q(Y + s, s, next);
-        if constexpr (kByte == 3) read_uq(H + s, kScaleBuf - scales);
+        spread(n, 2 * H, [&](int i) { read_q(Y + i / 2, i / 2, i % 2, next); });
+        if constexpr (kByte == 3) spread(n, H, [&](int i) { read_uq(H + i, kScaleBuf - scales); });
       }
-      if (two_more) {
-#pragma unroll
-        for (int n = 0; n < kCopiesAStep; ++n) q.copy(s * kCopiesAStep + n, cur);
-      }
-      row(H + s, X, 0);
-    }
+    });
     p.advance();
     q.advance();
     if constexpr (kByte == 3) {
@@ -228,8 +227,10 @@ __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds)
   }
 #pragma unroll
   for (int f = 0; f < H; ++f) {
-    read_p(f, 0);
-    read_q(f, f, 0);
+    read_p(f, 0, 0);
+    read_p(f, 1, 0);
+    read_q(f, f, 0, 0);
+    read_q(f, f, 1, 0);
   }
   constexpr std::integral_constant<int, 0> kB0{};
   constexpr std::integral_constant<int, 1> kB1{};

@@ -6,69 +6,129 @@ namespace {
 
 constexpr int kPackThreads = 256;
 
-// Columns j .. j + 7 of row i, zeros past the matrix.
+// Columns j .. j + 7 of row i, zeros past the matrix.  The load is always made, from the
+// last row past the end, so that a thread's loads are in flight together.
 template <int DT>
-__device__ __forceinline__ Eight cell8(const void* p, long ld, long i, int j, long m, int n) {
-  Eight r{};
-  if (i < m) {
-    r = load_raw<DT>(p, i * ld + j, n - j, (m - 1 - i) * ld + n - j).value();
-    if (n - j < 8) clear_tail(n - j, r);
+struct Cell {
+  Raw<DT> raw;
+  int n;                   // columns that exist, 0 past the rows
+  __device__ __forceinline__ void load(const void* p, long ld, long i, int j, long m, int cols) {
+    const long at = i < m ? i : m - 1;
+    raw = load_raw<DT>(p, at * ld + j, cols - j, (m - 1 - at) * ld + cols - j);
+    n = i < m ? cols - j : 0;
   }
-  return r;
-}
+  __device__ __forceinline__ Eight value() const {
+    Eight r = raw.value();
+    if (n < 8) clear_tail(n, r);
+    return r;
+  }
+};
 __device__ __forceinline__ unsigned top_over(unsigned t, int lanes) {
   const unsigned o = __shfl_xor(t, lanes);
   return o > t ? o : t;
 }
+// The largest over the 16 lanes that hold a row's block.
+__device__ __forceinline__ unsigned top_of_block(unsigned t) {
+  t = top_of_quad(t);
+  return top_over(top_over(t, 4), 8);
+}
 
-// A workgroup takes 128 x 128 elements, a thread eight columns of eight rows that
-// follow each other, so that it holds eight codes in a row of either form.  A row's
-// block lies in 16 lanes; a column's in all waves.
+// x alone, blocks along the rows.  1 << lg lanes (16 to 64) take a row's one to four
+// blocks, so that a word of scales is theirs; a wave's loads are of kPackRows rows
+// each.  Bound by memory.
+constexpr int kPackRows = 4;
+template <int DT>
+__global__ __launch_bounds__(kPackThreads) void fp8_pack_rows(Fp8PackArgs a, int lg, int words) {
+  const int lane = threadIdx.x & 63, part = lane & ((1 << lg) - 1), rows = kPackThreads >> lg;
+  const long chunk = blockIdx.x / words;
+  const int word = (int)(blockIdx.x - chunk * words), j = word * 4 * kFp8Block + 8 * part;
+  const long i0 = chunk * rows * kPackRows + (threadIdx.x >> lg);
+  const Fp8At at = fp8_at(a.rows, a.m, a.n);
+  Cell<DT> cell[kPackRows];
+#pragma unroll
+  for (int k = 0; k < kPackRows; ++k) cell[k].load(a.x, a.ldx, i0 + k * rows, j, a.m, a.n);
+#pragma unroll
+  for (int k = 0; k < kPackRows; ++k) {
+    const long i = i0 + k * rows;
+    const Eight v = cell[k].value();
+    unsigned top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, finite_bits(v.v[e]));
+    const int p = fp8_power(top_of_block(top));
+    // each block's byte in its place of the word, brought together in the row's first lane
+    unsigned s = (unsigned)(p + 127) << (part / 16 * 8);
+    if (lg > 4) s |= __shfl_xor(s, 16);
+    if (lg > 5) s |= __shfl_xor(s, 32);
+    if (i < a.m) {
+      if (j < at.pitch) *reinterpret_cast<uint2*>(at.codes + i * at.pitch + j) = fp8_codes(v.v, power_of_two(-p));
+      if (part == 0) *reinterpret_cast<unsigned*>(at.scales + i * at.words + 4 * word) = s;
+    }
+  }
+}
+
+// Both forms, or with a slope, a square's scale or column sums.  A workgroup takes 128 x
+// 128 elements, a thread eight columns of four rows that follow each other, so that it
+// holds four codes in a row of the turned form.  A row's block lies in 16 lanes; a
+// column's in all waves.  The turned codes pass through LDS, from where whole lines
+// leave: 16-byte unit u of column 8 c + e sits at u ^ c % 8, and every second half of
+// the columns in the neighbouring row, so that a wave's writes go to 64 banks.
+constexpr int kTileThreads = 512, kTileWaves = kTileThreads / 64, kTileRows = 4;
 struct PackLds {
-  unsigned top[4][kFp8Block];
-  float sum[4][kFp8Block];
-  uint2 codes[kFp8Block][16];      // turned: [column][eight rows], unit u at u ^ (column / 8)
+  unsigned top[kTileWaves][kFp8Block];
+  float sum[kTileWaves][kFp8Block];
+  unsigned codes[kFp8Block][kFp8Block / 4];
 };
+__device__ __forceinline__ int turned_row(int column) { return column ^ (column >> 6 & 1); }
+__device__ __forceinline__ int turned_unit(int column, int unit) { return unit ^ (column >> 3 & 7); }
+
 template <int DT>
 __device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, PackLds& lds) {
   const long across = (a.n + kFp8Block - 1) / kFp8Block, tile_r = block / across;
   const int tile_c = (int)(block - tile_r * across);
   const int t = threadIdx.x, c = t & 15, g = t >> 4, wave = t >> 6;
-  const long i0 = tile_r * kFp8Block + 8 * g;
+  const long i0 = tile_r * kFp8Block + kTileRows * g;
   const int j = tile_c * kFp8Block + 8 * c;
-  Eight v[8];
+  Cell<DT> cell[kTileRows], slope[kTileRows];
+  RawCodes slope8[kTileRows];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = cell8<DT>(a.x, a.ldx, i0 + k, j, a.m, a.n);
-  if (a.z) {
+  for (int k = 0; k < kTileRows; ++k) cell[k].load(a.x, a.ldx, i0 + k, j, a.m, a.n);
+  if (a.z && !a.z8) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      Eight z{}, value;
-      if (a.z8) {
-        if (i0 + k < a.m && j < a.n) z = ckpt_load8(ckpt_at(const_cast<void*>(a.z), a.m, a.n), i0 + k, j);
-      } else {
-        z = cell8<DT>(a.z, a.ldz, i0 + k, j, a.m, a.n);
-      }
+    for (int k = 0; k < kTileRows; ++k) slope[k].load(a.z, a.ldz, i0 + k, j, a.m, a.n);
+  } else if (a.z) {
+#pragma unroll
+    for (int k = 0; k < kTileRows; ++k)
+      slope8[k] = load_codes(ckpt_at(const_cast<void*>(a.z), a.m, a.n), i0 + k < a.m ? i0 + k : a.m - 1,
+                             j < a.n ? j : 0);
+  }
+  Eight v[kTileRows];
+#pragma unroll
+  for (int k = 0; k < kTileRows; ++k) {
+    v[k] = cell[k].value();
+    if (a.z) {
+      Eight z = a.z8 ? slope8[k].value() : slope[k].value(), value;
       // the slope's fp32 form: a dz next to a border of two codes should fall as the formula's does
       activate_slope8<OIDN_F32>(a.act, z, value);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k].v[e] *= z.v[e];
+      for (int e = 0; e < 8; ++e)
+        if (e < cell[k].n) v[k].v[e] *= z.v[e];
     }
   }
-  unsigned row_top[8], col_top[8] = {};
+  unsigned row_top[kTileRows], col_top[8] = {};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kTileRows; ++k) {
     row_top[k] = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const unsigned b = finite_bits(v[k].v[e]);
-      row_top[k] = b > row_top[k] ? b : row_top[k];
-      col_top[e] = b > col_top[e] ? b : col_top[e];
+      row_top[k] = max(row_top[k], b);
+      col_top[e] = max(col_top[e], b);
     }
   }
   if (a.sums) {
-    Eight s{};
+    Eight s = v[0];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) add8(s, v[k]);
+    for (int k = 1; k < kTileRows; ++k) add8(s, v[k]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       s.v[e] += __shfl_xor(s.v[e], 16);
@@ -76,67 +136,75 @@ __device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, Pack
       if ((t & 63) < 16) lds.sum[wave][8 * c + e] = s.v[e];
     }
   }
+  if (a.turned || a.square) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    col_top[e] = top_over(top_over(col_top[e], 16), 32);
-    if ((t & 63) < 16) lds.top[wave][8 * c + e] = col_top[e];
+    for (int e = 0; e < 8; ++e) {
+      col_top[e] = top_over(top_over(col_top[e], 16), 32);
+      if ((t & 63) < 16) lds.top[wave][8 * c + e] = col_top[e];
+    }
   }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) row_top[k] = top_over(top_over(top_over(top_over(row_top[k], 1), 2), 4), 8);
   __syncthreads();
+  if (a.turned || a.square) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    col_top[e] = 0;
+    for (int e = 0; e < 8; ++e) {
+      col_top[e] = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) col_top[e] = max(col_top[e], lds.top[w][8 * c + e]);
+      for (int w = 0; w < kTileWaves; ++w) col_top[e] = max(col_top[e], lds.top[w][8 * c + e]);
+    }
   }
   if (a.square) {
     unsigned all = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) all = max(all, col_top[e]);
-    all = top_over(top_over(top_over(top_over(all, 1), 2), 4), 8);
+    all = top_of_block(all);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) row_top[k] = col_top[k] = all;
+    for (int e = 0; e < 8; ++e) col_top[e] = all;
+#pragma unroll
+    for (int k = 0; k < kTileRows; ++k) row_top[k] = all;
   }
-  if (a.sums && t < kFp8Block && tile_c * kFp8Block + t < a.n)
-    a.sums[tile_r * a.n + tile_c * kFp8Block + t] = lds.sum[0][t] + lds.sum[1][t] + lds.sum[2][t] + lds.sum[3][t];
+  if (a.sums && t < kFp8Block && tile_c * kFp8Block + t < a.n) {
+    float s = lds.sum[0][t];
+#pragma unroll
+    for (int w = 1; w < kTileWaves; ++w) s += lds.sum[w][t];
+    a.sums[tile_r * a.n + tile_c * kFp8Block + t] = s;
+  }
   if (a.rows) {
     const Fp8At at = fp8_at(a.rows, a.m, a.n);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kTileRows; ++k) {
       const long i = i0 + k;
-      if (i >= a.m) break;
-      const int e = fp8_power(row_top[k]);
-      *reinterpret_cast<uint2*>(at.codes + i * at.pitch + j) = fp8_codes(v[k].v, power_of_two(-e));
-      if (c == 0) at.scales[i * at.words + tile_c] = (unsigned char)(e + 127);
+      const int p = fp8_power(a.square ? row_top[k] : top_of_block(row_top[k]));
+      if (i >= a.m) continue;
+      *reinterpret_cast<uint2*>(at.codes + i * at.pitch + j) = fp8_codes(v[k].v, power_of_two(-p));
+      if (c == 0) at.scales[i * at.words + tile_c] = (unsigned char)(p + 127);
     }
   }
   if (a.turned) {
     const Fp8At at = fp8_at(a.turned, a.n, a.m);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int p = fp8_power(col_top[e]);
-      float col[8];
+      const int p = fp8_power(col_top[e]), column = 8 * c + e;
+      const float inverse = power_of_two(-p);
+      float f[kTileRows];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) col[k] = v[k].v[e];
-      lds.codes[8 * c + e][g ^ c] = fp8_codes(col, power_of_two(-p));
+      for (int k = 0; k < kTileRows; ++k) f[k] = v[k].v[e];
+      lds.codes[turned_row(column)][4 * turned_unit(column, g >> 2) + (g & 3)] = fp8_codes4(f, inverse);
       if (g == 0 && j + e < a.n) at.scales[(j + e) * at.words + tile_r] = (unsigned char)(p + 127);
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = t + k * kPackThreads, column = u >> 3, q = u & 7, x = column >> 3;
-      const int col = tile_c * kFp8Block + column;
-      if (col >= a.n) break;
-      const uint2 first = lds.codes[column][(2 * q) ^ x], second = lds.codes[column][(2 * q + 1) ^ x];
-      *reinterpret_cast<uint4*>(at.codes + col * at.pitch + tile_r * kFp8Block + 16 * q) =
-          make_uint4(first.x, first.y, second.x, second.y);
+    for (int k = 0; k < kFp8Block * kFp8Block / 16 / kTileThreads; ++k) {
+      const int u = t + k * kTileThreads, column = u >> 3, unit = u & 7;
+      const long col = tile_c * (long)kFp8Block + column;
+      if (col < a.n)
+        *reinterpret_cast<uint4*>(at.codes + col * at.pitch + tile_r * kFp8Block + 16 * unit) =
+            *reinterpret_cast<const uint4*>(&lds.codes[turned_row(column)][4 * turned_unit(column, unit)]);
     }
   }
 }
 
 template <int DT>
-__global__ __launch_bounds__(kPackThreads) void fp8_pack(Fp8PackArgs a, Fp8PackArgs b, int first) {
+__global__ __launch_bounds__(kTileThreads) void fp8_pack_tiles(Fp8PackArgs a, Fp8PackArgs b, int first) {
   __shared__ __attribute__((aligned(16))) PackLds lds;
   if ((int)blockIdx.x < first) pack_tile<DT>(a, blockIdx.x, lds);
   else pack_tile<DT>(b, (int)blockIdx.x - first, lds);
@@ -161,15 +229,36 @@ __global__ __launch_bounds__(kPackThreads) void fp8_unpack(void* packed, long m,
   }
 }
 
+bool rows_alone(const Fp8PackArgs& a) { return !a.turned && !a.z && !a.square && !a.sums; }
+// Lanes of a row in fp8_pack_rows.
+int row_lanes(long n) {
+  const long blocks = fp8_cols(n) / kFp8Block;
+  return blocks == 1 ? 4 : blocks == 2 ? 5 : 6;
+}
+long row_chunks(long m, long n) {
+  const long rows = (kPackThreads >> row_lanes(n)) * kPackRows;
+  return (m + rows - 1) / rows;
+}
+
 template <int DT>
 void launch(const Fp8PackArgs& a, const Fp8PackArgs& b, hipStream_t stream) {
-  const long first = fp8_pack_blocks(a.m, a.n), second = b.x ? fp8_pack_blocks(b.m, b.n) : 0;
-  hipLaunchKernelGGL(fp8_pack<DT>, dim3((unsigned)(first + second)), dim3(kPackThreads), 0, stream, a, b, (int)first);
+  if (rows_alone(a) && !b.x) {
+    const int words = (int)(fp8_scales(a.n) / 4);
+    hipLaunchKernelGGL(fp8_pack_rows<DT>, dim3((unsigned)(row_chunks(a.m, a.n) * words)), dim3(kPackThreads), 0, stream, a,
+                       row_lanes(a.n), words);
+    return;
+  }
+  const long first = fp8_tiles(a.m, a.n), second = b.x ? fp8_tiles(b.m, b.n) : 0;
+  hipLaunchKernelGGL(fp8_pack_tiles<DT>, dim3((unsigned)(first + second)), dim3(kTileThreads), 0, stream, a, b, (int)first);
 }
 
 }  // namespace
 
-long fp8_pack_blocks(long m, long n) { return ((m + kFp8Block - 1) / kFp8Block) * (fp8_cols(n) / kFp8Block); }
+// In workgroups of 256: a tile is twice that.
+long fp8_pack_blocks(long m, long n) {
+  const long rows = row_chunks(m, n) * (fp8_scales(n) / 4), tiles = 2 * fp8_tiles(m, n);
+  return rows > tiles ? rows : tiles;
+}
 
 hipError_t launch_fp8_pack(const Fp8PackArgs& a, const Fp8PackArgs& b, int dtype, hipStream_t stream) {
   if (dtype == OIDN_F32) launch<OIDN_F32>(a, b, stream);
