@@ -59,7 +59,7 @@ def test_norm_limits():
 
 
 def norm_backward(**kw):
-    a = dict(dy=P, lddy=48, x=P, ldx=48, weight=P, add=P, ldadd=48, dx=P, lddx=48, dweight=P, dshift=P, m=10, n=48,
+    a = dict(dy=P, lddy=48, x=P, ldx=48, weight=P, add=P, ldadd=48, dx=P, lddx=48, dweight=P, dshift=P, m=5000, n=48,
              norm=U.OIDN_NORM_LAYER, eps=1e-5, dtype=U.OIDN_BF16, workspace=P, ws_bytes=1 << 40)
     a.update(kw)
     return U.oidn_norm_backward(**a, stream=0)
@@ -95,7 +95,7 @@ def test_norm_residual_refuses(bad):
 def residual_backward(**kw):
     a = dict(du=P, lddu=48, dv=P, lddv=48, o=P, ldo=48, weight=P, shift=P, gate=P, ldg=48, gate_rows=4, u=P, ldu=48,
              scale=0.5, p=0.1, rng=P, next_weight=P, dx=P, lddx=48, d_o=P, lddo=48, dgate=P, lddg=48, dweight=P,
-             dshift=P, dnext_weight=P, dnext_shift=P, m=10, n=48, norm=U.OIDN_NORM_RMS, next_norm=U.OIDN_NORM_LAYER,
+             dshift=P, dnext_weight=P, dnext_shift=P, m=5000, n=48, norm=U.OIDN_NORM_RMS, next_norm=U.OIDN_NORM_LAYER,
              eps=1e-5, dtype=U.OIDN_F16, workspace=P, ws_bytes=1 << 40)
     a.update(kw)
     return U.oidn_norm_residual_backward(**a, stream=0)
@@ -114,9 +114,9 @@ def test_norm_residual_backward_refuses(bad):
 
 
 def test_workspaces():
-    need = U.oidn_norm_backward_workspace_bytes(10, 48, U.OIDN_BF16)
+    need = U.oidn_norm_backward_workspace_bytes(5000, 48, U.OIDN_BF16)
     refused(U.OIDN_E_WORKSPACE, norm_backward, ws_bytes=need - 1)
-    need = U.oidn_norm_residual_backward_workspace_bytes(10, 48, 4, U.OIDN_F16)
+    need = U.oidn_norm_residual_backward_workspace_bytes(5000, 48, 4, U.OIDN_F16)
     refused(U.OIDN_E_WORKSPACE, residual_backward, ws_bytes=need - 1)
     assert U.oidn_norm_backward_workspace_bytes(0, 48, U.OIDN_F16) == 0
     assert U.oidn_norm_residual_backward_workspace_bytes(0, 48, 0, U.OIDN_F16) == 0

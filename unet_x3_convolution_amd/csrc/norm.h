@@ -42,8 +42,20 @@ struct NormChunks {
   long rows;               // of a chunk
   long per_group;          // chunks of a gate group; 0: a chunk holds whole groups
   long group_rows;         // rows that share a gate, all of them without one
+  int lane_groups;         // a chunk's groups are its row lanes' (norm_fast.h), else the workgroup's
   long count;
 };
+// Lanes that hold a row, eight columns each (norm_fast.h): 0 if it is too wide for them
+// (norm_wide.h).
+inline int norm_lanes(int n) {
+  int lanes = 4;
+  while (8 * lanes < n) lanes *= 2;
+  return lanes <= 1024 ? lanes : 0;
+}
+inline int norm_row_lanes(int n) {       // rows that a workgroup takes at once
+  const int lanes = norm_lanes(n);
+  return lanes && lanes < 256 ? 256 / lanes : 1;
+}
 constexpr int kNormSums = 4;       // dweight, dshift, dnext_weight, dnext_shift
 // D = du + next_norm'(dv; u),  dx = scale D, and the branch's gradients
 struct NormBackArgs {
@@ -68,8 +80,8 @@ struct NormBackArgs {
   long lddg;
   float* sums[kNormSums];
   float* rows;                     // workspace: kRowFloats of every row (wide rows)
-  float* part;                     // workspace: [chunk][kNormSums][n]
-  float* gate_part;                // workspace: [chunk][n]
+  float* part;                     // workspace, with more than one chunk: [chunk][kNormSums][n]
+  float* gate_part;                // workspace, where a group has more than one: [chunk][n]
   NormChunks chunks;
   long m;
   int n;

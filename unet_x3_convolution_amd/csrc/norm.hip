@@ -1,4 +1,5 @@
 // The norms before and after a block, forward, and dropout.
+#include "norm_fast.h"
 #include "norm_wide.h"
 
 namespace oidn {
@@ -20,8 +21,28 @@ __global__ __launch_bounds__(kNormThreads) void dropout_rows(const void* x, long
   }
 }
 
+template <int DT, int LANES>
+hipError_t launch_rows(const NormArgs& a, hipStream_t stream) {
+  constexpr int kThreads = norm_threads<LANES>(), kRows = kThreads / LANES;
+  const long blocks = (a.m + kRows - 1) / kRows, most = 2048 * 256 / kThreads;
+  const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(kThreads);
+  if (a.n % 8 == 0) hipLaunchKernelGGL((norm_rows<DT, LANES, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((norm_rows<DT, LANES, false>), grid, block, 0, stream, a);
+  return hipGetLastError();
+}
 template <int DT>
 hipError_t launch_type(const NormArgs& a, hipStream_t stream) {
+  switch (norm_lanes(a.n)) {
+    case 4: return launch_rows<DT, 4>(a, stream);
+    case 8: return launch_rows<DT, 8>(a, stream);
+    case 16: return launch_rows<DT, 16>(a, stream);
+    case 32: return launch_rows<DT, 32>(a, stream);
+    case 64: return launch_rows<DT, 64>(a, stream);
+    case 128: return launch_rows<DT, 128>(a, stream);
+    case 256: return launch_rows<DT, 256>(a, stream);
+    case 512: return launch_rows<DT, 512>(a, stream);
+    case 1024: return launch_rows<DT, 1024>(a, stream);
+  }
   const dim3 grid((unsigned)(a.m < 65536 ? a.m : 65536));
   hipLaunchKernelGGL(norm_wide<DT>, grid, dim3(kNormThreads), 0, stream, a);
   return hipGetLastError();

@@ -47,10 +47,10 @@ BackSpace back_space(long m, int n, long gate_rows, void* ws) {
   BackSpace b{};
   b.chunks = norm_chunks(m, n, gate_rows);
   Regions r{static_cast<char*>(ws), 0};
-  b.rows = static_cast<float*>(r.take(align256((size_t)m * kRowFloats * sizeof(float))));
-  b.part = static_cast<float*>(r.take(align256((size_t)b.chunks.count * kNormSums * n * sizeof(float))));
-  b.gate_part = static_cast<float*>(
-      gate_rows && b.chunks.per_group ? r.take(align256((size_t)b.chunks.count * n * sizeof(float))) : nullptr);
+  auto floats = [&](size_t count) { return static_cast<float*>(r.take(align256(count * sizeof(float)))); };
+  if (!norm_lanes(n)) b.rows = floats((size_t)m * kRowFloats);
+  if (b.chunks.count > 1) b.part = floats((size_t)b.chunks.count * kNormSums * n);
+  if (gate_rows && b.chunks.per_group > 1) b.gate_part = floats((size_t)b.chunks.count * n);
   b.bytes = r.used;
   return b;
 }

@@ -1,4 +1,5 @@
 // Gradients of the norms before and after a block.
+#include "norm_fast.h"
 #include "norm_wide.h"
 
 namespace oidn {
@@ -16,13 +17,13 @@ __global__ __launch_bounds__(kNormThreads) void norm_finish(NormBackArgs a) {
   float* out;
   long count, step;
   if (what < kNormSums) {
-    out = a.sums[what];
+    out = a.chunks.count > 1 ? a.sums[what] : nullptr;
     p = a.part + what * n;
     count = a.chunks.count;
     step = (long)kNormSums * n;
   } else {
     const long group = what - kNormSums;
-    out = a.dgate && a.chunks.per_group ? a.dgate + group * a.lddg : nullptr;
+    out = a.dgate + group * a.lddg;
     p = a.gate_part + group * a.chunks.per_group * n;
     count = a.chunks.per_group;
     step = n;
@@ -41,39 +42,63 @@ __global__ __launch_bounds__(kNormThreads) void norm_finish(NormBackArgs a) {
   }
 }
 
+template <int DT, int LANES>
+void launch_rows(const NormBackArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)a.chunks.count), block(norm_threads<LANES>());
+  if (a.o && a.n % 8 == 0) hipLaunchKernelGGL((norm_back_rows<DT, LANES, true, true>), grid, block, 0, stream, a);
+  else if (a.o) hipLaunchKernelGGL((norm_back_rows<DT, LANES, true, false>), grid, block, 0, stream, a);
+  else if (a.n % 8 == 0) hipLaunchKernelGGL((norm_back_rows<DT, LANES, false, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((norm_back_rows<DT, LANES, false, false>), grid, block, 0, stream, a);
+}
 template <int DT>
 hipError_t launch_type(const NormBackArgs& a, hipStream_t stream) {
-  const dim3 block(kNormThreads);
-  hipLaunchKernelGGL(norm_back_wide<DT>, dim3((unsigned)(a.m < 65536 ? a.m : 65536)), block, 0, stream, a);
-  hipError_t e = hipGetLastError();
   bool columns = a.dgate != nullptr;
   for (int k = 0; k < kNormSums; ++k) columns = columns || a.sums[k];
-  if (e != hipSuccess || !columns) return e;
-  const unsigned across = (unsigned)((a.n + 8l * kNormThreads - 1) / (8 * kNormThreads));
-  hipLaunchKernelGGL(norm_columns<DT>, dim3((unsigned)a.chunks.count, across), block, 0, stream, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const long groups = a.dgate && a.chunks.per_group ? a.chunks.count / a.chunks.per_group : 0;
-  hipLaunchKernelGGL(norm_finish, dim3((unsigned)((a.n + kAcross - 1l) / kAcross), (unsigned)(kNormSums + groups)), block,
-                     0, stream, a);
+  switch (norm_lanes(a.n)) {
+    case 4: launch_rows<DT, 4>(a, stream); break;
+    case 8: launch_rows<DT, 8>(a, stream); break;
+    case 16: launch_rows<DT, 16>(a, stream); break;
+    case 32: launch_rows<DT, 32>(a, stream); break;
+    case 64: launch_rows<DT, 64>(a, stream); break;
+    case 128: launch_rows<DT, 128>(a, stream); break;
+    case 256: launch_rows<DT, 256>(a, stream); break;
+    case 512: launch_rows<DT, 512>(a, stream); break;
+    case 1024: launch_rows<DT, 1024>(a, stream); break;
+    default: {
+      const dim3 block(kNormThreads);
+      hipLaunchKernelGGL(norm_back_wide<DT>, dim3((unsigned)(a.m < 65536 ? a.m : 65536)), block, 0, stream, a);
+      const unsigned across = (unsigned)((a.n + 8l * kNormThreads - 1) / (8 * kNormThreads));
+      if (columns) hipLaunchKernelGGL(norm_columns<DT>, dim3((unsigned)a.chunks.count, across), block, 0, stream, a);
+    }
+  }
+  const hipError_t e = hipGetLastError();
+  const long groups = a.dgate && a.chunks.per_group > 1 ? a.chunks.count / a.chunks.per_group : 0;
+  if (e != hipSuccess || !columns || (a.chunks.count == 1 && !groups)) return e;
+  hipLaunchKernelGGL(norm_finish, dim3((unsigned)((a.n + kAcross - 1l) / kAcross), (unsigned)(kNormSums + groups)),
+                     dim3(kNormThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// At most about 1024 chunks, so that the sums over them stay a short pass.
+// Chunks enough to fill the device, and few enough that the sums over them stay a short
+// pass: at most about 1024, half of that where a workgroup takes one row at a time.
 NormChunks norm_chunks(long m, int n, long gate_rows) {
   NormChunks c{};
-  (void)n;
-  long most = (m + 1023) / 1024;
-  if (most < 16) most = 16;
+  const long at_once = norm_row_lanes(n), target = at_once > 1 ? 1024 : 512;
+  long most = (m + target - 1) / target;
+  if (most < at_once) most = at_once;
   c.group_rows = gate_rows && gate_rows < m ? gate_rows : m;
   if (c.group_rows <= most) {
-    c.rows = most / c.group_rows * c.group_rows;
+    // a group of so few rows leaves most of a workgroup's row lanes without one
+    c.lane_groups = c.group_rows * 4 <= at_once;
+    const long least = c.lane_groups ? at_once * c.group_rows : 0, rows = most > least ? most : least;
+    c.rows = rows / c.group_rows * c.group_rows;
     c.count = (m + c.rows - 1) / c.rows;
   } else {
-    c.per_group = (c.group_rows + most - 1) / most;
-    c.rows = (c.group_rows + c.per_group - 1) / c.per_group;
+    const long parts = (c.group_rows + most - 1) / most;
+    c.rows = ((c.group_rows + parts - 1) / parts + at_once - 1) / at_once * at_once;
+    c.per_group = (c.group_rows + c.rows - 1) / c.rows;
     c.count = (m + c.group_rows - 1) / c.group_rows * c.per_group;
   }
   return c;

@@ -1,0 +1,358 @@
+// Rows that a workgroup holds in registers: each element is read once.
+//
+// LANES lanes take a row, a lane eight columns.  Up to 64 lanes lie in a wave, which takes 64 / LANES rows at
+// once and exchanges sums by shuffles; more are a workgroup's waves, which exchange
+// them through LDS.  The layer norm's squares are of deviations from the mean,
+// formed in a second round over the registers.
+#pragma once
+
+#include "norm_rows.h"
+
+namespace oidn {
+namespace {
+
+template <int LANES>
+constexpr int norm_threads() { return LANES > 64 ? LANES : 256; }
+
+// Sums of a pair over a row's lanes.  `turn` alternates the LDS that waves meet in, so
+// that one barrier is enough.
+template <int LANES>
+struct RowSum {
+  static constexpr int kWaves = LANES > 64 ? LANES / 64 : 1;
+  float2 (*const lds)[kWaves];       // [2][waves]
+  int turn;
+  __device__ __forceinline__ explicit RowSum(float2 (*at)[kWaves]) : lds(at), turn(0) {}
+  __device__ __forceinline__ float2 operator()(float x, float y) {
+    constexpr int kIn = LANES > 64 ? 64 : LANES;
+#pragma unroll
+    for (int s = 1; s < kIn; s *= 2) {
+      x += __shfl_xor(x, s);
+      y += __shfl_xor(y, s);
+    }
+    if constexpr (LANES > 64) {
+      float2* const at = lds[turn];
+      turn ^= 1;
+      if ((threadIdx.x & 63) == 0) at[threadIdx.x >> 6] = {x, y};
+      __syncthreads();
+      x = y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        x += at[w].x;
+        y += at[w].y;
+      }
+    }
+    return {x, y};
+  }
+};
+
+// The statistics of a row; a lane's columns past its `left` do not count.
+template <int LANES, bool WHOLE>
+__device__ __forceinline__ Stat row_stat(int kind, const Eight& x, int left, float each, float eps, RowSum<LANES>& sum) {
+  if (kind == OIDN_NORM_NONE) return {0.f, 1.f};
+  Stat s{0.f, 0.f};
+  if (kind == OIDN_NORM_LAYER) {
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t += x.v[e];
+    s.mean = sum(t, 0.f).x * each;
+  }
+  float t = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float d = x.v[e] - s.mean;
+    if (WHOLE || e < left) t += d * d;
+  }
+  if (WHOLE && left <= 0) t = 0.f;
+  s.r = rsqrtf(sum(t, 0.f).x * each + eps);
+  return s;
+}
+
+// A lane's eight columns: their first, and how many exist (WHOLE: eight or none).
+// Loads are made whether they or the row exist or not, from others in their place.
+template <int DT, bool WHOLE>
+struct Unit {
+  Raw<DT> raw;
+  __device__ __forceinline__ void load(const void* p, long ld, long i, int j, long m, int n) {
+    const long at = i < m ? i : m - 1;
+    const int c = j < n ? j : 0;
+    if constexpr (WHOLE) __builtin_memcpy(&raw.e, static_cast<const typename Raw<DT>::T*>(p) + at * ld + c, sizeof(raw.e));
+    else raw = load_raw<DT>(p, at * ld + c, n - c, (m - 1 - at) * ld + n - c);
+  }
+  __device__ __forceinline__ Eight value(int left) const {
+    Eight x = raw.value();
+    if constexpr (WHOLE) {
+      if (left <= 0) x = Eight{};
+    } else {
+      clear_tail(left, x);
+    }
+    return x;
+  }
+};
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void put8(void* p, long i, const Eight& x, int left) {
+  if (left > 0) store8<DT>(p, i, x, WHOLE ? 8 : left);
+}
+template <bool WHOLE>
+__device__ __forceinline__ Eight unit_of(const float* p, int j, int n, float other) {
+  if constexpr (WHOLE) {
+    Eight r;
+    if (p) {
+      __builtin_memcpy(r.v, p + (j < n ? j : 0), 32);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.v[e] = other;
+    }
+    return r;
+  } else {
+    return vector8(p, j < n ? j : 0, n, other);
+  }
+}
+
+// WHOLE: n is a multiple of 8, so that no single columns are looked at.
+template <int DT, int LANES, bool WHOLE>
+__global__ __launch_bounds__(norm_threads<LANES>()) void norm_rows(NormArgs a) {
+  constexpr int kThreads = norm_threads<LANES>(), kRows = kThreads / LANES;
+  __shared__ float2 lds[2][RowSum<LANES>::kWaves];
+  const Generator random(a.drop);
+  const int part = threadIdx.x % LANES, n = a.n, j = 8 * part, left = n - j;
+  const float each = 1.f / n;
+  const long units = (n + 7l) / 8, step = (long)gridDim.x * kRows;
+  RowSum<LANES> sum(lds);
+  Eight w, s, next_w, next_s;
+  if (a.o) {
+    w = unit_of<WHOLE>(a.weight, j, n, 1.f);
+    s = unit_of<WHOLE>(a.shift, j, n, 0.f);
+  }
+  if (a.v) {
+    next_w = unit_of<WHOLE>(a.next_weight, j, n, 1.f);
+    next_s = unit_of<WHOLE>(a.next_shift, j, n, 0.f);
+  }
+  // a row's loads are made before the row in front of it is worked on
+  Unit<DT, WHOLE> raw_o, raw_x;
+  long i = (long)blockIdx.x * kRows + threadIdx.x / LANES;
+  raw_x.load(a.x, a.ldx, i, j, a.m, n);
+  if (a.o) raw_o.load(a.o, a.ldo, i, j, a.m, n);
+  for (long first = (long)blockIdx.x * kRows; first < a.m; first += step, i += step) {
+    const bool ok = i < a.m;
+    Eight u = raw_x.value(left), b;
+    if (a.o) b = raw_o.value(left);
+    if (first + step < a.m) {
+      raw_x.load(a.x, a.ldx, i + step, j, a.m, n);
+      if (a.o) raw_o.load(a.o, a.ldo, i + step, j, a.m, n);
+    }
+    if (a.o) {
+      const Stat t = row_stat<LANES, WHOLE>(a.norm, b, left, each, a.eps, sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b.v[e] = (b.v[e] - t.mean) * t.r * w.v[e] + s.v[e];
+      if (a.drop.threshold) drop8(b, random.words(i * units + part), a.drop);
+      if (a.gate) {
+        const Eight g = unit_of<WHOLE>(a.gate + (ok ? i : a.m - 1) / a.gate_rows * a.ldg, j, n, 1.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b.v[e] *= g.v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u.v[e] = rounded<DT>(a.scale * u.v[e] + b.v[e]);
+      if (ok) put8<DT, WHOLE>(a.u, i * a.ldu + j, u, left);
+      if (left < 8) clear_tail(left, u);
+    }
+    if (!a.v) continue;
+    const Stat t = row_stat<LANES, WHOLE>(a.next_norm, u, left, each, a.eps, sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u.v[e] = (u.v[e] - t.mean) * t.r * next_w.v[e] + next_s.v[e];
+    if (ok) put8<DT, WHOLE>(a.v, i * a.ldv + j, u, left);
+  }
+}
+
+// ------------------------------------------------------------------ gradients
+// A row lane is the LANES threads of a row.  Column sums stay in registers over a
+// chunk's rows and are added over the row lanes at its end; a gate's, where chunks hold
+// whole groups, at the group's end: groups of few rows are a row lane's each, others
+// the whole workgroup's.
+template <int LANES>
+struct ColumnSum {
+  static constexpr int kWaves = LANES > 64 ? 1 : norm_threads<LANES>() / 64;
+  typedef float Lds[kWaves][LANES > 64 ? 1 : LANES * 8];
+  // Adds over the row lanes; the sums are in the first one's threads.
+  static __device__ __forceinline__ void over_rows(Eight& x, Lds& lds) {
+    if constexpr (LANES <= 64) {
+      const int lane = threadIdx.x & 63;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+#pragma unroll
+        for (int s = LANES; s < 64; s *= 2) x.v[e] += __shfl_xor(x.v[e], s);
+        if (lane < LANES) lds[threadIdx.x >> 6][e * LANES + lane] = x.v[e];
+      }
+      __syncthreads();
+      if (threadIdx.x < LANES) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int w = 1; w < kWaves; ++w) x.v[e] += lds[w][e * LANES + threadIdx.x];
+      }
+      __syncthreads();
+    }
+  }
+};
+
+template <int DT, int LANES, bool BRANCH, bool WHOLE>
+__global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBackArgs a) {
+  constexpr int kThreads = norm_threads<LANES>(), kRowLanes = kThreads / LANES;
+  typedef ColumnSum<LANES> Columns;
+  __shared__ float2 lds[2][RowSum<LANES>::kWaves];
+  __shared__ typename Columns::Lds column_lds;
+  const Generator random(a.drop);
+  const int part = threadIdx.x % LANES, lane = threadIdx.x / LANES, n = a.n, j = 8 * part, left = n - j;
+  const float each = 1.f / n;
+  const long units = (n + 7l) / 8;
+  const NormChunks& c = a.chunks;
+  RowSum<LANES> sum(lds);
+  Eight w, s, next_w, along{}, total{}, next_along{}, next_total{}, gate_sum{};
+  if constexpr (BRANCH) {
+    w = unit_of<WHOLE>(a.weight, j, n, 1.f);
+    s = unit_of<WHOLE>(a.shift, j, n, 0.f);
+  }
+  if (a.dv) next_w = unit_of<WHOLE>(a.next_weight, j, n, 1.f);
+
+  Unit<DT, WHOLE> raw_du, raw_dv, raw_u, raw_o;
+  // (every lambda here is inlined: left to itself the compiler calls them and keeps the
+  // arrays in memory)
+  auto load = [&](long i) __attribute__((always_inline)) {
+    if (a.du) raw_du.load(a.du, a.lddu, i, j, a.m, n);
+    if (a.dv) {
+      raw_dv.load(a.dv, a.lddv, i, j, a.m, n);
+      raw_u.load(a.u, a.ldu, i, j, a.m, n);
+    }
+    if constexpr (BRANCH) raw_o.load(a.o, a.ldo, i, j, a.m, n);
+  };
+  // Row i, whose elements are loaded; ok: it exists.  `next`: the row to load meanwhile.
+  auto row = [&](long i, bool ok, long next) __attribute__((always_inline)) {
+    Eight d{}, dv, u, o;
+    if (a.du) d = raw_du.value(left);
+    if (a.dv) {
+      dv = raw_dv.value(left);
+      u = raw_u.value(left);
+    }
+    if constexpr (BRANCH) o = raw_o.value(left);
+    if (next >= 0) load(next);
+    if (a.dv) {
+      const Stat t = row_stat<LANES, WHOLE>(a.next_norm, u, left, each, a.eps, sum);
+      float c0 = 0.f, c1 = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        u.v[e] = (u.v[e] - t.mean) * t.r;
+        if (ok) {
+          next_along.v[e] += dv.v[e] * u.v[e];
+          next_total.v[e] += dv.v[e];
+        }
+        dv.v[e] *= next_w.v[e];
+        c0 += dv.v[e];
+        c1 += dv.v[e] * u.v[e];
+      }
+      const float2 both = sum(c0, c1);
+      c0 = a.next_norm == OIDN_NORM_LAYER ? both.x * each : 0.f;
+      c1 = both.y * each;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d.v[e] += t.r * (dv.v[e] - c0 - u.v[e] * c1);
+    }
+    if (a.dx && ok) {
+      Eight x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.v[e] = a.scale * d.v[e];
+      put8<DT, WHOLE>(a.dx, i * a.lddx + j, x, left);
+    }
+    if constexpr (BRANCH) {
+      const Stat t = row_stat<LANES, WHOLE>(a.norm, o, left, each, a.eps, sum);
+      uint4 words;
+      if (a.drop.threshold) words = random.words(i * units + part);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o.v[e] = (o.v[e] - t.mean) * t.r;
+      if (a.dgate) {
+        Eight b;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b.v[e] = o.v[e] * w.v[e] + s.v[e];
+        if (a.drop.threshold) drop8(b, words, a.drop);
+        if (ok) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) gate_sum.v[e] += d.v[e] * b.v[e];
+        }
+      }
+      if (a.gate) {
+        const Eight g = unit_of<WHOLE>(a.gate + (ok ? i : a.m - 1) / c.group_rows * a.ldg, j, n, 1.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d.v[e] *= g.v[e];
+      }
+      // h, and h hat(o), which is 0 in dropped places whatever o holds
+      Eight weighted;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) weighted.v[e] = d.v[e] * o.v[e];
+      if (a.drop.threshold) {
+        drop8(d, words, a.drop);
+        drop8(weighted, words, a.drop);
+      }
+      float c0 = 0.f, c1 = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (ok) {
+          along.v[e] += weighted.v[e];
+          total.v[e] += d.v[e];
+        }
+        d.v[e] *= w.v[e];
+        if (WHOLE || e < left) {
+          c0 += d.v[e];
+          c1 += weighted.v[e] * w.v[e];
+        }
+      }
+      if (WHOLE && left <= 0) c0 = c1 = 0.f;
+      if (a.d_o) {
+        if (a.norm != OIDN_NORM_NONE) {
+          const float2 both = sum(c0, c1);
+          c0 = a.norm == OIDN_NORM_LAYER ? both.x * each : 0.f;
+          c1 = both.y * each;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d.v[e] = t.r * (d.v[e] - c0 - o.v[e] * c1);
+        }
+        if (ok) put8<DT, WHOLE>(a.d_o, i * a.lddo + j, d, left);
+      }
+    }
+  };
+  const long chunk = blockIdx.x, group = c.per_group ? chunk / c.per_group : 0;
+  const bool alone = c.lane_groups && LANES <= 64;       // a row lane's groups are its own
+  long first = chunk * c.rows, last = first + c.rows, span = c.group_rows;
+  if (c.per_group) {                                     // a part of one group
+    first = group * c.group_rows + (chunk - group * c.per_group) * c.rows;
+    span = c.rows;
+    last = first + span < (group + 1) * c.group_rows ? first + span : (group + 1) * c.group_rows;
+  }
+  last = last < a.m ? last : a.m;
+  const int lanes = alone ? 1 : kRowLanes;
+  long g = first;
+  do {       // once for a part, which may be empty
+    const long begin = g + (alone ? lane * span : 0), end = begin + span < last ? begin + span : last;
+    long i = begin + (alone ? 0 : lane);
+    load(i);
+    for (long r = begin; r < end; r += lanes, i += lanes) row(i, i < end, r + lanes < end ? i + lanes : -1);
+    if (BRANCH && a.dgate) {
+      if (!alone) Columns::over_rows(gate_sum, column_lds);
+      float* const out = c.per_group > 1 ? a.gate_part + chunk * n
+                                         : a.dgate + (c.per_group ? group : begin / c.group_rows) * a.lddg;
+      if (alone ? begin < end : lane == 0) put8<OIDN_F32, WHOLE>(out, j, gate_sum, left);
+      gate_sum = Eight{};
+    }
+    g += alone ? span * kRowLanes : span;
+  } while (g < last);
+  auto finish = [&](int which, Eight& x) __attribute__((always_inline)) {
+    if (!a.sums[which]) return;
+    Columns::over_rows(x, column_lds);
+    if (lane == 0)
+      put8<OIDN_F32, WHOLE>(c.count > 1 ? a.part + (chunk * kNormSums + which) * n : a.sums[which], j, x, left);
+  };
+  if constexpr (BRANCH) {
+    finish(0, along);
+    finish(1, total);
+  }
+  finish(2, next_along);
+  finish(3, next_total);
+}
+
+}  // namespace
+}  // namespace oidn
