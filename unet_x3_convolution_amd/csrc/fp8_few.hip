@@ -12,6 +12,7 @@
 #include "dense_few.h"
 #include "fp8_code.h"
 #include "fp8_gemm.h"
+#include "lanes.h"
 
 namespace oidn {
 namespace {
@@ -30,8 +31,7 @@ __device__ __forceinline__ intx8 code32(const Raw<DT> (&x)[4], unsigned& scale) 
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, finite_bits(v[q].v[e]));
   }
-  top = max(top, (unsigned)__shfl_xor(top, 16));
-  top = max(top, (unsigned)__shfl_xor(top, 32));
+  top = lanes_max<64, 16>(top);
   const int p = fp8_power(top);
   scale = (unsigned)(p + 127);
   intx8 r;

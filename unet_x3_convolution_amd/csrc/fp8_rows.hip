@@ -1,5 +1,6 @@
 // Matrices to 8-bit floating point and back.
 #include "fp8_code.h"
+#include "lanes.h"
 
 namespace oidn {
 namespace {
@@ -23,16 +24,6 @@ struct Cell {
     return r;
   }
 };
-__device__ __forceinline__ unsigned top_over(unsigned t, int lanes) {
-  const unsigned o = __shfl_xor(t, lanes);
-  return o > t ? o : t;
-}
-// The largest over the 16 lanes that hold a row's block.
-__device__ __forceinline__ unsigned top_of_block(unsigned t) {
-  t = top_of_quad(t);
-  return top_over(top_over(t, 4), 8);
-}
-
 // x alone, blocks along the rows.  1 << lg lanes (16 to 64) take a row's one to four
 // blocks, so that a word of scales is theirs; a wave's loads are of kPackRows rows
 // each.  Bound by memory.
@@ -54,7 +45,7 @@ __global__ __launch_bounds__(kPackThreads) void fp8_pack_rows(Fp8PackArgs a, int
     unsigned top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, finite_bits(v.v[e]));
-    const int p = fp8_power(top_of_block(top));
+    const int p = fp8_power(lanes_max<16>(top));
     // each block's byte in its place of the word, brought together in the row's first lane
     unsigned s = (unsigned)(p + 127) << (part / 16 * 8);
     if (lg > 4) s |= __shfl_xor(s, 16);
@@ -131,15 +122,14 @@ __device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, Pack
     for (int k = 1; k < kTileRows; ++k) add8(s, v[k]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      s.v[e] += __shfl_xor(s.v[e], 16);
-      s.v[e] += __shfl_xor(s.v[e], 32);
+      s.v[e] = lanes_sum<64, 16>(s.v[e]);
       if ((t & 63) < 16) lds.sum[wave][8 * c + e] = s.v[e];
     }
   }
   if (a.turned || a.square) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      col_top[e] = top_over(top_over(col_top[e], 16), 32);
+      col_top[e] = lanes_max<64, 16>(col_top[e]);
       if ((t & 63) < 16) lds.top[wave][8 * c + e] = col_top[e];
     }
   }
@@ -156,7 +146,7 @@ __device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, Pack
     unsigned all = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) all = max(all, col_top[e]);
-    all = top_of_block(all);
+    all = lanes_max<16>(all);
 #pragma unroll
     for (int e = 0; e < 8; ++e) col_top[e] = all;
 #pragma unroll
@@ -173,7 +163,7 @@ __device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, Pack
 #pragma unroll
     for (int k = 0; k < kTileRows; ++k) {
       const long i = i0 + k;
-      const int p = fp8_power(a.square ? row_top[k] : top_of_block(row_top[k]));
+      const int p = fp8_power(a.square ? row_top[k] : lanes_max<16>(row_top[k]));
       if (i >= a.m) continue;
       *reinterpret_cast<uint2*>(at.codes + i * at.pitch + j) = fp8_codes(v[k].v, power_of_two(-p));
       if (c == 0) at.scales[i * at.words + tile_c] = (unsigned char)(p + 127);

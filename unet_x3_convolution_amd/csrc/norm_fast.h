@@ -1,11 +1,12 @@
 // Rows that a workgroup holds in registers: each element is read once.
 //
 // LANES lanes take a row, a lane eight columns.  Up to 64 lanes lie in a wave, which takes 64 / LANES rows at
-// once and exchanges sums by shuffles; more are a workgroup's waves, which exchange
+// once and exchanges sums in registers; more are a workgroup's waves, which exchange
 // them through LDS.  The layer norm's squares are of deviations from the mean,
 // formed in a second round over the registers.
 #pragma once
 
+#include "lanes.h"
 #include "norm_rows.h"
 
 namespace oidn {
@@ -24,11 +25,8 @@ struct RowSum {
   __device__ __forceinline__ explicit RowSum(float2 (*at)[kWaves]) : lds(at), turn(0) {}
   __device__ __forceinline__ float2 operator()(float x, float y) {
     constexpr int kIn = LANES > 64 ? 64 : LANES;
-#pragma unroll
-    for (int s = 1; s < kIn; s *= 2) {
-      x += __shfl_xor(x, s);
-      y += __shfl_xor(y, s);
-    }
+    x = lanes_sum<kIn>(x);
+    y = lanes_sum<kIn>(y);
     if constexpr (LANES > 64) {
       float2* const at = lds[turn];
       turn ^= 1;
@@ -45,25 +43,43 @@ struct RowSum {
   }
 };
 
-// The statistics of a row; a lane's columns past its `left` do not count.
+// The statistics of two rows at once (or of one: kind OIDN_NORM_NONE), so that they share
+// their rounds of sums; a lane's columns past its `left` do not count.
 template <int LANES, bool WHOLE>
-__device__ __forceinline__ Stat row_stat(int kind, const Eight& x, int left, float each, float eps, RowSum<LANES>& sum) {
-  if (kind == OIDN_NORM_NONE) return {0.f, 1.f};
-  Stat s{0.f, 0.f};
-  if (kind == OIDN_NORM_LAYER) {
-    float t = 0.f;
+__device__ __forceinline__ void row_stats(int kind_x, const Eight& x, Stat& sx, int kind_y, const Eight& y, Stat& sy,
+                                          int left, float each, float eps, RowSum<LANES>& sum) {
+  sx = sy = {0.f, 1.f};
+  const bool layer_x = kind_x == OIDN_NORM_LAYER, layer_y = kind_y == OIDN_NORM_LAYER;
+  if (layer_x || layer_y) {
+    float t = 0.f, u = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t += x.v[e];
-    s.mean = sum(t, 0.f).x * each;
+    for (int e = 0; e < 8; ++e) {
+      if (layer_x) t += x.v[e];
+      if (layer_y) u += y.v[e];
+    }
+    const float2 both = sum(t, u);
+    sx.mean = both.x * each;
+    sy.mean = both.y * each;
   }
-  float t = 0.f;
+  if (kind_x == OIDN_NORM_NONE && kind_y == OIDN_NORM_NONE) return;
+  float t = 0.f, u = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float d = x.v[e] - s.mean;
-    if (WHOLE || e < left) t += d * d;
+    const float d = x.v[e] - sx.mean, f = y.v[e] - sy.mean;
+    if (WHOLE || e < left) {
+      if (kind_x != OIDN_NORM_NONE) t += d * d;
+      if (kind_y != OIDN_NORM_NONE) u += f * f;
+    }
   }
-  if (WHOLE && left <= 0) t = 0.f;
-  s.r = rsqrtf(sum(t, 0.f).x * each + eps);
+  if (WHOLE && left <= 0) t = u = 0.f;
+  const float2 both = sum(t, u);
+  if (kind_x != OIDN_NORM_NONE) sx.r = rsqrtf(both.x * each + eps);
+  if (kind_y != OIDN_NORM_NONE) sy.r = rsqrtf(both.y * each + eps);
+}
+template <int LANES, bool WHOLE>
+__device__ __forceinline__ Stat row_stat(int kind, const Eight& x, int left, float each, float eps, RowSum<LANES>& sum) {
+  Stat s, none;
+  row_stats<LANES, WHOLE>(kind, x, s, OIDN_NORM_NONE, x, none, left, each, eps, sum);
   return s;
 }
 
@@ -226,7 +242,7 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBack
   };
   // Row i, whose elements are loaded; ok: it exists.  `next`: the row to load meanwhile.
   auto row = [&](long i, bool ok, long next) __attribute__((always_inline)) {
-    Eight d{}, dv, u, o;
+    Eight d{}, dv{}, u{}, o{};
     if (a.du) d = raw_du.value(left);
     if (a.dv) {
       dv = raw_dv.value(left);
@@ -234,12 +250,14 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBack
     }
     if constexpr (BRANCH) o = raw_o.value(left);
     if (next >= 0) load(next);
+    Stat of_u, of_o;
+    row_stats<LANES, WHOLE>(a.dv ? a.next_norm : OIDN_NORM_NONE, u, of_u, BRANCH ? a.norm : OIDN_NORM_NONE, o, of_o, left,
+                            each, a.eps, sum);
     if (a.dv) {
-      const Stat t = row_stat<LANES, WHOLE>(a.next_norm, u, left, each, a.eps, sum);
       float c0 = 0.f, c1 = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        u.v[e] = (u.v[e] - t.mean) * t.r;
+        u.v[e] = (u.v[e] - of_u.mean) * of_u.r;
         if (ok) {
           next_along.v[e] += dv.v[e] * u.v[e];
           next_total.v[e] += dv.v[e];
@@ -252,7 +270,7 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBack
       c0 = a.next_norm == OIDN_NORM_LAYER ? both.x * each : 0.f;
       c1 = both.y * each;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d.v[e] += t.r * (dv.v[e] - c0 - u.v[e] * c1);
+      for (int e = 0; e < 8; ++e) d.v[e] += of_u.r * (dv.v[e] - c0 - u.v[e] * c1);
     }
     if (a.dx && ok) {
       Eight x;
@@ -261,11 +279,10 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBack
       put8<DT, WHOLE>(a.dx, i * a.lddx + j, x, left);
     }
     if constexpr (BRANCH) {
-      const Stat t = row_stat<LANES, WHOLE>(a.norm, o, left, each, a.eps, sum);
       uint4 words;
       if (a.drop.threshold) words = random.words(i * units + part);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o.v[e] = (o.v[e] - t.mean) * t.r;
+      for (int e = 0; e < 8; ++e) o.v[e] = (o.v[e] - of_o.mean) * of_o.r;
       if (a.dgate) {
         Eight b;
 #pragma unroll
@@ -309,7 +326,7 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBack
           c0 = a.norm == OIDN_NORM_LAYER ? both.x * each : 0.f;
           c1 = both.y * each;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d.v[e] = t.r * (d.v[e] - c0 - o.v[e] * c1);
+          for (int e = 0; e < 8; ++e) d.v[e] = of_o.r * (d.v[e] - c0 - o.v[e] * c1);
         }
         if (ok) put8<DT, WHOLE>(a.d_o, i * a.lddo + j, d, left);
       }

@@ -3,6 +3,7 @@
 // own, from what the first left of every row.
 #pragma once
 
+#include "lanes.h"
 #include "norm_rows.h"
 
 namespace oidn {
@@ -10,11 +11,8 @@ namespace {
 
 // Sums of a pair over the workgroup; lds: kNormThreads / 64 pairs.
 __device__ __forceinline__ float2 sum_of_group(float2 v, float2* lds) {
-#pragma unroll
-  for (int s = 32; s; s >>= 1) {
-    v.x += __shfl_xor(v.x, s);
-    v.y += __shfl_xor(v.y, s);
-  }
+  v.x = lanes_sum<64>(v.x);
+  v.y = lanes_sum<64>(v.y);
   __syncthreads();                       // what was summed before has been read
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
