@@ -83,7 +83,7 @@ def test_unpack_refuses(bad):
 
 
 def linear(**kw):
-    a = dict(x=P, ldx=64, w8=P, bias=P, residual=P, ldr=48, y=P, ldy=48, z=P, ldz=48, m=100, k=64, n=48,
+    a = dict(x=P, ldx=160, w8=P, bias=P, residual=P, ldr=48, y=P, ldy=48, z=P, ldz=48, m=100, k=160, n=48,
              act=U.OIDN_ACT_GELU, dtype=U.OIDN_F16, flags=0, workspace=P, ws_bytes=1 << 40)
     a.update(kw)
     return U.oidn_linear_fp8(**a, stream=0)
@@ -91,7 +91,7 @@ def linear(**kw):
 
 @pytest.mark.parametrize("bad", [
     dict(x=None), dict(w8=None), dict(y=None), dict(x=P + 1), dict(w8=P + 8), dict(y=P + 1), dict(residual=P + 1),
-    dict(z=P + 1), dict(bias=P + 2), dict(ldx=63), dict(ldr=47), dict(ldy=47), dict(ldz=47), dict(m=-1), dict(k=0),
+    dict(z=P + 1), dict(bias=P + 2), dict(ldx=159), dict(ldr=47), dict(ldy=47), dict(ldz=47), dict(m=-1), dict(k=0),
     dict(n=0), dict(act=4), dict(act=-1), dict(dtype=3), dict(flags=U.OIDN_X_CKPT8), dict(flags=U.OIDN_FP8_SQUARE),
     dict(flags=16), dict(flags=U.OIDN_Z_CKPT8, z=None), dict(flags=U.OIDN_X_FP8, x=P + 2), dict(workspace=None),
     dict(workspace=P + 8)], ids=str)
@@ -110,10 +110,10 @@ def test_linear_limits():
 
 
 def test_linear_workspace():
-    need = U.oidn_linear_fp8_workspace_bytes(100, 64, 48, U.OIDN_F16, 0)
-    assert need >= U.oidn_fp8_bytes(100, 64)
+    need = U.oidn_linear_fp8_workspace_bytes(100, 160, 48, U.OIDN_F16, 0)
+    assert need >= U.oidn_fp8_bytes(100, 160)
     refused(U.OIDN_E_WORKSPACE, linear, ws_bytes=need - 1)
-    assert U.oidn_linear_fp8_workspace_bytes(100, 64, 48, U.OIDN_F16, U.OIDN_X_FP8) < need
+    assert U.oidn_linear_fp8_workspace_bytes(100, 160, 48, U.OIDN_F16, U.OIDN_X_FP8) < need
     assert U.oidn_linear_fp8_workspace_bytes(0, 64, 48, U.OIDN_F16, 0) == 0
     refused(U.OIDN_E_INVALID, U.oidn_linear_fp8_workspace_bytes, 4, 0, 4, U.OIDN_F16, 0)
     refused(U.OIDN_E_INVALID, U.oidn_linear_fp8_workspace_bytes, 4, 4, 4, U.OIDN_F16, 4)

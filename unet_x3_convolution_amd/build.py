@@ -18,7 +18,7 @@ SOURCES = ["api.cpp", "conv_f16.hip", "conv_f32.hip", "elementwise.hip", "noallo
            "calibrate.hip", "dense_api.cpp", "dense_rows.hip", "dense_gemm16_forward.hip",
            "dense_gemm16_gated_back.hip", "dense_gemm16_group.hip", "dense_gemm32.hip", "dense_few.hip", "dense_narrow.hip",
            "norm_api.cpp", "norm.hip", "norm_back.hip", "fp8_api.cpp", "fp8_rows.hip", "fp8_gemm.hip",
-           "fp8_few.hip"]
+           "fp8_few.hip", "fp8_narrow.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # Packed-fp32 ops are turned off for the device code: plain fp32 arithmetic only.

@@ -48,9 +48,16 @@ struct Gemm8Group {
   int start[kMaxGroup8];
   Gemm8Args a[kMaxGroup8];
 };
-// Forward products of at most kFewRows rows, in one launch; packed: g.q is packed, else a
-// matrix of dtype, k columns at pitch g.ldq.
+// Forward products of at most kFewRows packed rows, in one launch, or (packed false) of
+// at most kCodedRows rows of dtype, k columns at pitch g.ldq, coded on the way.
+// In a launch of their own from 5 rows on (us a call, coded on the way against before; bf16
+// 4096 -> 4096: 1 row 7.0 and 10.4, 4 rows 8.8 and 10.6, 8 rows 10.8 and 11.0; 8192 ->
+// 2048, 8 rows 14.7 and 14.1).
+constexpr int kCodedRows = 4;
 hipError_t launch_few8(const Gemm8Args& a, int k, bool packed, bool bf16, hipStream_t stream);
+// Forward products of k <= kFp8Block inputs: g.q is a matrix of dtype, k columns at pitch
+// g.ldq, coded on the way; tile 64 or 128.
+hipError_t launch_narrow8(const Gemm8Args& a, int k, int tile, bool bf16, hipStream_t stream);
 // kEpiLinear, and kEpiStore for a group; 16-bit results.
 hipError_t launch_gemm8(const Gemm8Args& a, int tile, bool bf16, hipStream_t stream);
 hipError_t launch_gemm8_group(const Gemm8Group& g, int blocks, int tile, bool bf16, hipStream_t stream);

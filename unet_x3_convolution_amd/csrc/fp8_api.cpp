@@ -82,7 +82,9 @@ Gemm8Args gemm8_args(const Product8& p, const void* q, const void* pm, const Epi
 }
 
 struct Forward {
-  bool few;                // at most kFewRows rows: one launch, no workspace
+  bool narrow;             // at most kFp8Block inputs, not packed: one launch
+  bool few;                // else at most kFewRows rows: the product in one launch
+  bool pack;               // x is packed first
   Product8 p;
   void *x8, *slices;
   size_t bytes;
@@ -90,22 +92,25 @@ struct Forward {
 Forward forward(long m, int k, int n, unsigned flags, void* ws) {
   Forward f{};
   f.p = product8(m, n, k);
-  f.few = m <= kFewRows;
-  if (f.few) {
-    f.p.plan = GemmPlan{64, 64, true, true, 1, 0};
-    return f;
-  }
+  const bool x8 = flags & OIDN_X_FP8;
+  f.narrow = !x8 && k <= kFp8Block && m > kCodedRows;
+  f.few = !f.narrow && m <= kFewRows;
+  f.pack = !x8 && !f.narrow && m > kCodedRows;
   Product8* one = &f.p;
-  plan_together(&one, 1);
+  if (f.narrow) {
+    // one staged tile: 128 x 128 where they fill the units
+    const int tile = ((m + 127) / 128) * ((n + 127l) / 128) >= 512 ? 128 : 64;
+    f.p.plan = GemmPlan{tile, tile, false, true, 1, 4};
+  } else if (f.few) f.p.plan = GemmPlan{64, 64, true, true, 1, 0};
+  else plan_together(&one, 1);
   Regions r{static_cast<char*>(ws), 0};
-  f.x8 = flags & OIDN_X_FP8 ? nullptr : r.take(fp8_bytes(m, k));
+  f.x8 = f.pack ? r.take(fp8_bytes(m, k)) : nullptr;
   f.slices = r.take(slice_bytes(f.p));
   f.bytes = r.used;
   return f;
 }
 int check_forward_launch(const Forward& f, long m, int k) {
-  if (f.few) return OIDN_OK;
-  return check_launch(std::max({most_blocks(f.p), sum_blocks(f.p), f.x8 ? fp8_pack_blocks(m, k) : 0}));
+  return check_launch(std::max({f.few ? 0 : most_blocks(f.p), sum_blocks(f.p), f.pack ? fp8_pack_blocks(m, k) : 0}));
 }
 
 struct Backward {
@@ -208,7 +213,7 @@ int oidn_linear_fp8(const void* x, long ldx, const void* w8, const float* bias, 
   const Forward f = forward(m, k, n, flags, workspace);
   OIDN_TRY(check_forward_launch(f, m, k));
   OIDN_TRY(check_workspace(workspace, ws_bytes, f.bytes));
-  if (!x8 && !f.few) {
+  if (f.pack) {
     Fp8PackArgs a{};
     a.x = x;
     a.ldx = ldx;
@@ -225,9 +230,15 @@ int oidn_linear_fp8(const void* x, long ldx, const void* w8, const float* bias, 
   e.z8 = z8;
   e.act = act;
   Gemm8Args g = gemm8_args(f.p, x, w8, e, f.slices);
+  if (f.narrow) {
+    g.g.ldq = ldx;
+    OIDN_TRY(ran(launch_narrow8(g, k, f.p.plan.tile_r, dtype == OIDN_BF16, stream), "8-bit product launch"));
+    return clear_error();
+  }
   if (f.few) {
-    if (!x8) g.g.ldq = ldx;
-    OIDN_TRY(ran(launch_few8(g, k, x8, dtype == OIDN_BF16, stream), "8-bit product launch"));
+    const bool packed = x8 || f.pack;
+    if (!packed) g.g.ldq = ldx;
+    OIDN_TRY(ran(launch_few8(g, k, packed, dtype == OIDN_BF16, stream), "8-bit product launch"));
     return clear_error();
   }
   OIDN_TRY(ran(launch_gemm8(g, f.p.plan.tile_r, dtype == OIDN_BF16, stream), "8-bit product launch"));

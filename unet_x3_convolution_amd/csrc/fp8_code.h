@@ -24,10 +24,25 @@ __device__ __forceinline__ Fp8At fp8_at(void* packed, long m, long n) {
   unsigned char* const p = static_cast<unsigned char*>(packed);
   return {p, p + m * pitch, pitch, words};
 }
-// Bits of the magnitude, 0 for what is not finite.
+// Bits of the magnitude; of infinities and NaN: 0x7f800000 and more.
+__device__ __forceinline__ unsigned magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The same, 0 for what is not finite.
 __device__ __forceinline__ unsigned finite_bits(float v) {
-  const unsigned b = __float_as_uint(v) & 0x7fffffffu;
+  const unsigned b = magnitude_bits(v);
   return b < 0x7f800000u ? b : 0u;
+}
+// The largest finite magnitude of eight values: infinities and NaN are rare, so they are
+// left out only where the plain maximum shows one.
+__device__ __forceinline__ unsigned finite_top(const Eight& x) {
+  unsigned t = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t = max(t, magnitude_bits(x.v[e]));
+  if (t >= 0x7f800000u) {
+    t = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t = max(t, finite_bits(x.v[e]));
+  }
+  return t;
 }
 // e of a block from the bits of its largest magnitude; 448 = 1.75 * 2^8.
 __device__ __forceinline__ int fp8_power(unsigned top) {
@@ -36,13 +51,11 @@ __device__ __forceinline__ int fp8_power(unsigned top) {
   return e < -120 ? -120 : e > 120 ? 120 : e;
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
-// Codes of x 2^-e, nearest even; `inverse` is 2^-e.
+// Codes of x 2^-e, nearest even; `inverse` is 2^-e.  The conversion gives NaN for infinities
+// and NaN; finite values do not pass its range.
 __device__ __forceinline__ unsigned fp8_codes4(const float* x, float inverse) {
-  float v[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = __builtin_fabsf(x[k]) < __builtin_inff() ? x[k] * inverse : __builtin_nanf("");
-  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-  return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * inverse, x[1] * inverse, 0, false);
+  return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * inverse, x[3] * inverse, lo, true);
 }
 __device__ __forceinline__ uint2 fp8_codes(const float (&x)[8], float inverse) {
   return make_uint2(fp8_codes4(x, inverse), fp8_codes4(x + 4, inverse));

@@ -2,13 +2,12 @@
 //
 // The weights are all there is to read, each once.  A workgroup of 8 waves owns 16
 // columns (32 where an 8-bit block of z has to be whole) and all of the summed length,
-// which its waves share in turns of one block of 128; every wave loads weight codes
-// straight into registers, kDepth blocks at once, and multiplies them by the rows' with
-// v_mfma_scale_f32_16x16x128_f8f6f4 (rows past the last read the last).  Rows that come
-// in 16 bits are coded on the way, by every workgroup for itself: a lane holds 32 of
-// a row's 128 values, four lanes a block.  That costs about 150 vector instructions a
-// block, less than the launch that would code them once.  The waves' sums meet in LDS
-// and are added in wave order.
+// in segments of 32 blocks of 128: a wave loads the weight codes of four neighbouring
+// blocks and their word of scales straight into registers and multiplies them by the
+// rows' with v_mfma_scale_f32_16x16x128_f8f6f4 (rows past the last read the last).  Rows
+// that come in 16 bits, kCodedRows at most, are coded on the way, by every workgroup for
+// itself, while the weights' loads are in flight: a thread codes eight values of each row's segment, which
+// the waves read from LDS.  The waves' sums meet in LDS and are added in wave order.
 #include "dense_few.h"
 #include "fp8_code.h"
 #include "fp8_gemm.h"
@@ -17,52 +16,28 @@
 namespace oidn {
 namespace {
 
-constexpr int kDepth8 = 4;
+constexpr int kSegment = 4 * kFewWaves;      // blocks
 
-// 32 values of a row as codes, and their block's scale byte.  The four lanes that hold
-// a block (16 apart) call it together.
-template <int DT>
-__device__ __forceinline__ intx8 code32(const Raw<DT> (&x)[4], unsigned& scale) {
-  Eight v[4];
-  unsigned top = 0;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    v[q] = x[q].value();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, finite_bits(v[q].v[e]));
-  }
-  top = lanes_max<64, 16>(top);
-  const int p = fp8_power(top);
-  scale = (unsigned)(p + 127);
-  intx8 r;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint2 c = fp8_codes(v[q].v, power_of_two(-p));
-    r[2 * q] = (int)c.x;
-    r[2 * q + 1] = (int)c.y;
-  }
-  return r;
-}
-
-// One block's product.  The compiler knows neither what the instruction reads nor when
-// its result is there: the waits are for operands that vector instructions have just
-// written, and for the next product, which adds to the same registers (12 wait states
-// cover an 8-pass instruction).
-__device__ __forceinline__ void mfma8_now(floatx4& c, const intx8& a, const intx8& b, unsigned sa, unsigned sb) {
-  asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0]\n\ts_nop 11"
-      : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb));
-}
-
-// x of dtype (PACKED false: a.g.q elements at pitch a.g.ldq) or packed.  MF: fragments
-// of 16 rows; NF: of 16 columns.
-template <int DT, bool PACKED, int MF, int NF>
+// x of dtype (PACKED false: k columns at pitch a.g.ldq) or packed.  ROWS: rows at most;
+// NF: fragments of 16 columns.
+template <int DT, bool PACKED, int ROWS, int NF>
 __global__ __launch_bounds__(64 * kFewWaves) void dense_few8(Gemm8Args a, int k) {
+  constexpr int MF = ROWS > 16 ? 2 : 1;        // fragments of 16 rows
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int j0 = blockIdx.x * 16 * NF;
   const long pitch = 2 * a.g.ldp, blocks = pitch / kFp8Block;      // bytes of a row of codes
   const EpilogueArgs& e = a.g.e;
+  // a segment's codes, rows 32 bytes apart in the banks, and its scales
+  constexpr int kRowBytes = kSegment * kFp8Block + 32;
+  constexpr int kCols = 16 * NF, kPitch = kCols + 4;         // a row of sums is padded by 16 bytes
+  constexpr int kCodes = PACKED ? 0 : ROWS * (kRowBytes + kSegment), kSums = kFewWaves * 16 * MF * kPitch * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[kCodes > kSums ? kCodes : kSums];
+  unsigned char* const codes = lds;
+  unsigned char* const scales = lds + ROWS * kRowBytes;
+  typedef float Sums[16 * MF][kPitch];
+  Sums* const part = reinterpret_cast<Sums*>(lds);           // [wave][row][column], after the codes
 
-  const unsigned char *wp[NF], *ws[NF], *xp[MF], *xs[MF];
+  const unsigned char *wp[NF], *ws[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
     long j = j0 + 16 * f + r;
@@ -70,79 +45,99 @@ __global__ __launch_bounds__(64 * kFewWaves) void dense_few8(Gemm8Args a, int k)
     wp[f] = static_cast<const unsigned char*>(a.g.p) + j * pitch + 32 * g;
     ws[f] = a.ps + j * a.pn;
   }
-  long row[MF];
+  int row[MF];
 #pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    row[f] = 16 * f + r < e.rows ? 16 * f + r : e.rows - 1;
-    if constexpr (PACKED) {
-      xp[f] = static_cast<const unsigned char*>(a.g.q) + row[f] * pitch + 32 * g;
-      xs[f] = a.qs + row[f] * a.qn;
-    }
-  }
+  for (int f = 0; f < MF; ++f) row[f] = 16 * f + r < e.rows ? 16 * f + r : (int)e.rows - 1;
   floatx4 acc[NF][MF];
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
     for (int m = 0; m < MF; ++m) acc[f][m] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  auto block = [&](long b, auto depth) {       // blocks b, b + kFewWaves, ... of this wave
-    constexpr int kN = decltype(depth)::value;
-    intx8 w[kN][NF], xc[kN][MF];
-    unsigned sw[kN][NF], sx[kN][MF];
-    Raw<DT> raw[kN][MF][4];
+  for (long from = 0; from < blocks; from += kSegment) {
+    // blocks past the last are loaded from the last and not multiplied
+    const long b0 = from + 4 * wave;
+    const int exist = __builtin_amdgcn_readfirstlane((int)(blocks - b0 < 4 ? blocks - b0 : 4));
+    intx8 w[4][NF];
+    unsigned sw[NF];
 #pragma unroll
-    for (int d = 0; d < kN; ++d) {
-      const long at = b + d * kFewWaves;
+    for (int f = 0; f < NF; ++f) {
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        __builtin_memcpy(&w[d][f], wp[f] + at * kFp8Block, 32);
-        sw[d][f] = ws[f][at];
-      }
+      for (int d = 0; d < 4; ++d)
+        __builtin_memcpy(&w[d][f], wp[f] + (b0 + d < blocks ? b0 + d : blocks - 1) * kFp8Block, 32);
+      sw[f] = *reinterpret_cast<const unsigned*>(ws[f] + (b0 < blocks ? b0 : 0));
+    }
+    intx8 x[4][MF];
+    unsigned sx[MF];
+    if constexpr (PACKED) {
+      const unsigned char* const q = static_cast<const unsigned char*>(a.g.q);
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
-        if constexpr (PACKED) {
-          __builtin_memcpy(&xc[d][m], xp[m] + at * kFp8Block, 32);
-          sx[d][m] = xs[m][at];
-        } else {
-          const long j = at * kFp8Block + 32 * g;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const long n = k - (j + 8 * q), left = (e.rows - 1 - row[m]) * a.g.ldq + n;
-            raw[d][m][q] = load_raw<DT>(a.g.q, row[m] * a.g.ldq + j + 8 * q, n < 8 ? (int)(n < 0 ? 0 : n) : 8, left);
-            if (n < 8) {
+        for (int d = 0; d < 4; ++d) {
+          __builtin_memcpy(&x[d][m], q + row[m] * pitch + (b0 + d < blocks ? b0 + d : blocks - 1) * kFp8Block + 32 * g, 32);
+        }
+        sx[m] = *reinterpret_cast<const unsigned*>(a.qs + row[m] * a.qn + (b0 < blocks ? b0 : 0));
+      }
+    } else {
+      // thread t: values 8 t .. + 7 of the segment, of every row; 16 lanes hold a block
+      typedef typename Raw<DT>::T T;
+      const long j = from * kFp8Block + 8 * threadIdx.x, left = k - j;
+      constexpr int kAtOnce = ROWS < 4 ? ROWS : 4;
+      for (int i = 0; i < e.rows; i += kAtOnce) {
+        Raw<DT> raw[kAtOnce];
 #pragma unroll
-              for (int t = 0; t < 8; ++t)
-                if (t >= n) raw[d][m][q].e[t] = (typename Raw<DT>::T)0.f;
-            }
+        for (int n = 0; n < kAtOnce; ++n) {
+          const T* const p = static_cast<const T*>(a.g.q) + (i + n < e.rows ? i + n : e.rows - 1) * a.g.ldq;
+          if (left >= 8) {
+            __builtin_memcpy(&raw[n].e, p + j, 16);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) raw[n].e[c] = c < left ? p[j + c] : (T)0.f;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kAtOnce; ++n) {
+          const Eight v = raw[n].value();
+          const int power = fp8_power(lanes_max<16>(finite_top(v)));
+          if (i + n < e.rows) {
+            *reinterpret_cast<uint2*>(codes + (i + n) * kRowBytes + 8 * threadIdx.x) = fp8_codes(v.v, power_of_two(-power));
+            if (threadIdx.x % 16 == 0) scales[(i + n) * kSegment + threadIdx.x / 16] = (unsigned char)(power + 127);
           }
         }
       }
-    }
+      __syncthreads();
 #pragma unroll
-    for (int d = 0; d < kN; ++d) {
-      if constexpr (!PACKED) {
+      for (int m = 0; m < MF; ++m) {
 #pragma unroll
-        for (int m = 0; m < MF; ++m) xc[d][m] = code32<DT>(raw[d][m], sx[d][m]);
+        for (int d = 0; d < 4; ++d) {
+          const uint4* const p = reinterpret_cast<const uint4*>(codes + row[m] * kRowBytes + (4 * wave + d) * kFp8Block + 32 * g);
+          const uint4 lo = p[0], hi = p[1];
+          x[d][m] = intx8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+        }
+        sx[m] = *reinterpret_cast<const unsigned*>(scales + row[m] * kSegment + 4 * wave);
       }
-#pragma unroll
-      for (int f = 0; f < NF; ++f)
-#pragma unroll
-        for (int m = 0; m < MF; ++m) mfma8_now(acc[f][m], w[d][f], xc[d][m], sw[d][f], sx[d][m]);
     }
-  };
-  constexpr int kAtOnce = MF == 1 ? kDepth8 : 2;
-  long b = wave;
-  for (; b + (kAtOnce - 1) * kFewWaves < blocks; b += kAtOnce * kFewWaves)
-    block(b, std::integral_constant<int, kAtOnce>{});
-  for (; b < blocks; b += kFewWaves) block(b, std::integral_constant<int, 1>{});
+    auto multiply = [&](auto byte) {
+      constexpr int kByte = decltype(byte)::value;
+      if (kByte < exist) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+          for (int m = 0; m < MF; ++m) mfma8_acc<kByte, true>(acc[f][m], w[kByte][f], x[kByte][m], sw[f], sx[m]);
+      }
+    };
+    multiply(std::integral_constant<int, 0>{});
+    multiply(std::integral_constant<int, 1>{});
+    multiply(std::integral_constant<int, 2>{});
+    multiply(std::integral_constant<int, 3>{});
+    if (!PACKED) __syncthreads();      // the codes have been read
+  }
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
     for (int m = 0; m < MF; ++m) asm volatile("s_nop 15" : "+a"(acc[f][m]));
 
-  // [wave][row][column]; a row's pitch is padded by 16 bytes
-  constexpr int kCols = 16 * NF, kPitch = kCols + 4;
-  __shared__ __attribute__((aligned(16))) float part[kFewWaves][16 * MF][kPitch];
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
@@ -173,8 +168,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void dense_few8(Gemm8Args a, int k)
 template <int DT, bool PACKED, int NF>
 void launch_rows(const Gemm8Args& a, int k, hipStream_t stream) {
   const dim3 grid((unsigned)((a.g.e.cols + 16 * NF - 1) / (16 * NF))), block(64 * kFewWaves);
-  if (a.g.e.rows <= 16) hipLaunchKernelGGL((dense_few8<DT, PACKED, 1, NF>), grid, block, 0, stream, a, k);
-  else hipLaunchKernelGGL((dense_few8<DT, PACKED, 2, NF>), grid, block, 0, stream, a, k);
+  const long m = a.g.e.rows;
+  if constexpr (PACKED) {
+    if (m <= 16) hipLaunchKernelGGL((dense_few8<DT, true, 16, NF>), grid, block, 0, stream, a, k);
+    else hipLaunchKernelGGL((dense_few8<DT, true, kFewRows, NF>), grid, block, 0, stream, a, k);
+  } else {
+    if (m == 1) hipLaunchKernelGGL((dense_few8<DT, false, 1, NF>), grid, block, 0, stream, a, k);
+    else hipLaunchKernelGGL((dense_few8<DT, false, kCodedRows, NF>), grid, block, 0, stream, a, k);
+  }
 }
 template <int DT>
 void launch_type(const Gemm8Args& a, int k, bool packed, hipStream_t stream) {
@@ -191,7 +192,7 @@ void launch_type(const Gemm8Args& a, int k, bool packed, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_few8(const Gemm8Args& a, int k, bool packed, bool bf16, hipStream_t stream) {
-  if (a.g.e.rows > kFewRows) return hipErrorInvalidValue;
+  if (a.g.e.rows > (packed ? kFewRows : kCodedRows)) return hipErrorInvalidValue;
   if (bf16) launch_type<OIDN_BF16>(a, k, packed, stream);
   else launch_type<OIDN_F16>(a, k, packed, stream);
   return hipGetLastError();

@@ -24,21 +24,28 @@ typedef int intx8 __attribute__((ext_vector_type(8)));
 
 // c += a b in place, scales in byte BYTE of sa and sb.  As an instruction of its own:
 // the builtin's result may be given the registers of an operand (seen with the
-// scale's, and wrong sums with it).  The waits are dense_gemm16_direct.h's settle().
-template <int BYTE>
+// scale's, and wrong sums with it).  The compiler knows neither what it reads nor when
+// its result is there.  WAITS false: operands come from loads, the same c follows 4
+// such instructions later or more, and dense_gemm16_direct.h's settle() stands before
+// its first read.  WAITS true: after vector instructions that wrote an operand, and
+// before the next product into the same c (12 wait states cover its 8 passes; without
+// them sums were wrong).
+template <int BYTE, bool WAITS = false>
 __device__ __forceinline__ void mfma8_acc(floatx4& c, const intx8& a, const intx8& b, unsigned sa, unsigned sb) {
-  if constexpr (BYTE == 0)
-    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0]"
-        : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb));
-  else if constexpr (BYTE == 1)
-    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0]"
-        : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb));
-  else if constexpr (BYTE == 2)
-    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[1,1,0]"
-        : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb));
-  else
-    asm("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0]"
-        : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb));
+#define OIDN_MFMA8(before, sel, after)                                                                      \
+  asm(before "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " sel after                          \
+      : "+a"(c) : "v"(a), "v"(b), "v"(sa), "v"(sb))
+#define OIDN_MFMA8_BYTE(sel)                                                 \
+  do {                                                                       \
+    if constexpr (WAITS) OIDN_MFMA8("s_nop 1\n\t", sel, "\n\ts_nop 11");    \
+    else OIDN_MFMA8("", sel, "");                                            \
+  } while (0)
+  if constexpr (BYTE == 0) OIDN_MFMA8_BYTE("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
+  else if constexpr (BYTE == 1) OIDN_MFMA8_BYTE("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+  else if constexpr (BYTE == 2) OIDN_MFMA8_BYTE("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
+  else OIDN_MFMA8_BYTE("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#undef OIDN_MFMA8_BYTE
+#undef OIDN_MFMA8
 }
 
 // LDS: two buffers of a P tile, two of a Q tile, then two of the rows' scales, a word

@@ -42,10 +42,7 @@ __global__ __launch_bounds__(kPackThreads) void fp8_pack_rows(Fp8PackArgs a, int
   for (int k = 0; k < kPackRows; ++k) {
     const long i = i0 + k * rows;
     const Eight v = cell[k].value();
-    unsigned top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, finite_bits(v.v[e]));
-    const int p = fp8_power(lanes_max<16>(top));
+    const int p = fp8_power(lanes_max<16>(finite_top(v)));
     // each block's byte in its place of the word, brought together in the row's first lane
     unsigned s = (unsigned)(p + 127) << (part / 16 * 8);
     if (lg > 4) s |= __shfl_xor(s, 16);
@@ -98,24 +95,30 @@ __device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, Pack
     v[k] = cell[k].value();
     if (a.z) {
       Eight z = a.z8 ? slope8[k].value() : slope[k].value(), value;
-      // the slope's fp32 form: a dz next to a border of two codes should fall as the formula's does
-      activate_slope8<OIDN_F32>(a.act, z, value);
+      activate_slope8<DT>(a.act, z, value);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (e < cell[k].n) v[k].v[e] *= z.v[e];
     }
   }
-  unsigned row_top[kTileRows], col_top[8] = {};
+  unsigned row_top[kTileRows], col_top[8] = {}, top = 0;
+  auto tops = [&](auto bits) {
 #pragma unroll
-  for (int k = 0; k < kTileRows; ++k) {
-    row_top[k] = 0;
+    for (int e = 0; e < 8; ++e) col_top[e] = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const unsigned b = finite_bits(v[k].v[e]);
-      row_top[k] = max(row_top[k], b);
-      col_top[e] = max(col_top[e], b);
+    for (int k = 0; k < kTileRows; ++k) {
+      row_top[k] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const unsigned b = bits(v[k].v[e]);
+        row_top[k] = max(row_top[k], b);
+        col_top[e] = max(col_top[e], b);
+      }
+      top = max(top, row_top[k]);
     }
-  }
+  };
+  tops([](float f) { return magnitude_bits(f); });
+  if (top >= 0x7f800000u) tops([](float f) { return finite_bits(f); });      // rare
   if (a.sums) {
     Eight s = v[0];
 #pragma unroll
