@@ -15,7 +15,7 @@ __global__ __launch_bounds__(kNormThreads) void dropout_rows(const void* x, long
     const long i = t / units;
     const int j = (int)(t - i * units) * 8;
     Eight v = row8<DT>(x, ldx, i, j, m, n);
-    if (d.threshold) drop8(v, random.words(t), d);
+    if (d.threshold) drop8(v, kept8(random.words(t), d), d);
     if (residual) add8(v, row8<DT>(residual, ldr, i, j, m, n));
     store8<DT>(y, i * ldy + j, v, n - j);
   }

@@ -42,13 +42,19 @@ __global__ __launch_bounds__(kNormThreads) void norm_finish(NormBackArgs a) {
   }
 }
 
+template <int DT, int LANES, bool BRANCH, bool WHOLE, bool SHIFTS>
+void launch_kernel(const NormBackArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((norm_back_rows<DT, LANES, BRANCH, WHOLE, SHIFTS>), dim3((unsigned)a.chunks.count),
+                     dim3(norm_threads<LANES>()), 0, stream, a);
+}
 template <int DT, int LANES>
 void launch_rows(const NormBackArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.chunks.count), block(norm_threads<LANES>());
-  if (a.o && a.n % 8 == 0) hipLaunchKernelGGL((norm_back_rows<DT, LANES, true, true>), grid, block, 0, stream, a);
-  else if (a.o) hipLaunchKernelGGL((norm_back_rows<DT, LANES, true, false>), grid, block, 0, stream, a);
-  else if (a.n % 8 == 0) hipLaunchKernelGGL((norm_back_rows<DT, LANES, false, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((norm_back_rows<DT, LANES, false, false>), grid, block, 0, stream, a);
+  const bool whole = a.n % 8 == 0;
+  if (!a.o && whole) launch_kernel<DT, LANES, false, true, true>(a, stream);
+  else if (!a.o) launch_kernel<DT, LANES, false, false, true>(a, stream);
+  else if (!whole) launch_kernel<DT, LANES, true, false, true>(a, stream);
+  else if (a.sums[1] || a.sums[3]) launch_kernel<DT, LANES, true, true, true>(a, stream);
+  else launch_kernel<DT, LANES, true, true, false>(a, stream);
 }
 template <int DT>
 hipError_t launch_type(const NormBackArgs& a, hipStream_t stream) {

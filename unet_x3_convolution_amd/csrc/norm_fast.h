@@ -145,7 +145,7 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_rows(NormArgs a) {
   }
   // a row's loads are made before the row in front of it is worked on
   Unit<DT, WHOLE> raw_o, raw_x;
-  long i = (long)blockIdx.x * kRows + threadIdx.x / LANES;
+  long i = (long)blockIdx.x * kRows + (kRows == 1 ? 0 : threadIdx.x / LANES);
   raw_x.load(a.x, a.ldx, i, j, a.m, n);
   if (a.o) raw_o.load(a.o, a.ldo, i, j, a.m, n);
   for (long first = (long)blockIdx.x * kRows; first < a.m; first += step, i += step) {
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_rows(NormArgs a) {
       const Stat t = row_stat<LANES, WHOLE>(a.norm, b, left, each, a.eps, sum);
 #pragma unroll
       for (int e = 0; e < 8; ++e) b.v[e] = (b.v[e] - t.mean) * t.r * w.v[e] + s.v[e];
-      if (a.drop.threshold) drop8(b, random.words(i * units + part), a.drop);
+      if (a.drop.threshold) drop8(b, kept8(random.words(i * units + part), a.drop), a.drop);
       if (a.gate) {
         const Eight g = unit_of<WHOLE>(a.gate + (ok ? i : a.m - 1) / a.gate_rows * a.ldg, j, n, 1.f);
 #pragma unroll
@@ -210,24 +210,37 @@ struct ColumnSum {
   }
 };
 
-template <int DT, int LANES, bool BRANCH, bool WHOLE>
-__global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBackArgs a) {
+// SHIFTS: the shifts' gradients are wanted too.
+template <int DT, int LANES, bool BRANCH, bool WHOLE, bool SHIFTS>
+__global__ __launch_bounds__(norm_threads<LANES>(), LANES >= 128 && !SHIFTS ? 4 : 1) void norm_back_rows(NormBackArgs a) {
   constexpr int kThreads = norm_threads<LANES>(), kRowLanes = kThreads / LANES;
   typedef ColumnSum<LANES> Columns;
   __shared__ float2 lds[2][RowSum<LANES>::kWaves];
   __shared__ typename Columns::Lds column_lds;
+  // the norms' weights, read again for every row: held in registers they leave a unit half
+  // as many waves
+  __shared__ __attribute__((aligned(16))) float vectors[3][8 * LANES];
   const Generator random(a.drop);
-  const int part = threadIdx.x % LANES, lane = threadIdx.x / LANES, n = a.n, j = 8 * part, left = n - j;
+  const int part = threadIdx.x % LANES, lane = kRowLanes == 1 ? 0 : threadIdx.x / LANES, n = a.n, j = 8 * part, left = n - j;
   const float each = 1.f / n;
   const long units = (n + 7l) / 8;
   const NormChunks& c = a.chunks;
   RowSum<LANES> sum(lds);
-  Eight w, s, next_w, along{}, total{}, next_along{}, next_total{}, gate_sum{};
-  if constexpr (BRANCH) {
-    w = unit_of<WHOLE>(a.weight, j, n, 1.f);
-    s = unit_of<WHOLE>(a.shift, j, n, 0.f);
+  Eight along{}, total{}, next_along{}, next_total{}, gate_sum{};
+  if (lane == 0) {
+    auto hold = [&](int which, const Eight& v) { __builtin_memcpy(&vectors[which][j], v.v, 32); };
+    if constexpr (BRANCH) {
+      hold(0, unit_of<WHOLE>(a.weight, j, n, 1.f));
+      hold(1, unit_of<WHOLE>(a.shift, j, n, 0.f));
+    }
+    if (a.dv) hold(2, unit_of<WHOLE>(a.next_weight, j, n, 1.f));
   }
-  if (a.dv) next_w = unit_of<WHOLE>(a.next_weight, j, n, 1.f);
+  __syncthreads();
+  auto held = [&](int which) __attribute__((always_inline)) {
+    Eight v;
+    __builtin_memcpy(v.v, &vectors[which][j], 32);
+    return v;
+  };
 
   Unit<DT, WHOLE> raw_du, raw_dv, raw_u, raw_o;
   // (every lambda here is inlined: left to itself the compiler calls them and keeps the
@@ -254,13 +267,14 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBack
     row_stats<LANES, WHOLE>(a.dv ? a.next_norm : OIDN_NORM_NONE, u, of_u, BRANCH ? a.norm : OIDN_NORM_NONE, o, of_o, left,
                             each, a.eps, sum);
     if (a.dv) {
+      const Eight next_w = held(2);
       float c0 = 0.f, c1 = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         u.v[e] = (u.v[e] - of_u.mean) * of_u.r;
         if (ok) {
           next_along.v[e] += dv.v[e] * u.v[e];
-          next_total.v[e] += dv.v[e];
+          if constexpr (SHIFTS) next_total.v[e] += dv.v[e];
         }
         dv.v[e] *= next_w.v[e];
         c0 += dv.v[e];
@@ -279,20 +293,25 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBack
       put8<DT, WHOLE>(a.dx, i * a.lddx + j, x, left);
     }
     if constexpr (BRANCH) {
-      uint4 words;
-      if (a.drop.threshold) words = random.words(i * units + part);
+      __builtin_amdgcn_sched_barrier(0);       // d alone is left of what is above
+      unsigned keep = 0;
+      if (a.drop.threshold) keep = kept8(random.words(i * units + part), a.drop);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o.v[e] = (o.v[e] - of_o.mean) * of_o.r;
+      const Eight w = held(0);
       if (a.dgate) {
+        const Eight s = held(1);
         Eight b;
 #pragma unroll
         for (int e = 0; e < 8; ++e) b.v[e] = o.v[e] * w.v[e] + s.v[e];
-        if (a.drop.threshold) drop8(b, words, a.drop);
+        if (a.drop.threshold) drop8(b, keep, a.drop);
         if (ok) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) gate_sum.v[e] += d.v[e] * b.v[e];
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
       if (a.gate) {
         const Eight g = unit_of<WHOLE>(a.gate + (ok ? i : a.m - 1) / c.group_rows * a.ldg, j, n, 1.f);
 #pragma unroll
@@ -303,15 +322,15 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBack
 #pragma unroll
       for (int e = 0; e < 8; ++e) weighted.v[e] = d.v[e] * o.v[e];
       if (a.drop.threshold) {
-        drop8(d, words, a.drop);
-        drop8(weighted, words, a.drop);
+        drop8(d, keep, a.drop);
+        drop8(weighted, keep, a.drop);
       }
       float c0 = 0.f, c1 = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (ok) {
           along.v[e] += weighted.v[e];
-          total.v[e] += d.v[e];
+          if constexpr (SHIFTS) total.v[e] += d.v[e];
         }
         d.v[e] *= w.v[e];
         if (WHOLE || e < left) {
@@ -365,10 +384,10 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_back_rows(NormBack
   };
   if constexpr (BRANCH) {
     finish(0, along);
-    finish(1, total);
+    if constexpr (SHIFTS) finish(1, total);
   }
   finish(2, next_along);
-  finish(3, next_total);
+  if constexpr (SHIFTS) finish(3, next_total);
 }
 
 }  // namespace

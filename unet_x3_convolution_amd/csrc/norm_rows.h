@@ -40,14 +40,21 @@ struct Generator {
     return make_uint4(a, b, c, d);
   }
 };
-// Dropped elements become 0 whatever they hold, the others times the gain.
-__device__ __forceinline__ void drop8(Eight& x, const uint4& w, const Dropout& d) {
+// Bit k: column k of the eight is kept.
+__device__ __forceinline__ unsigned kept8(const uint4& w, const Dropout& d) {
   const unsigned v[4] = {w.x, w.y, w.z, w.w};
+  unsigned keep = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const unsigned bits = k % 2 ? v[k / 2] >> 16 : v[k / 2] & 0xffffu;
-    x.v[k] = bits >= d.threshold ? x.v[k] * d.gain : 0.f;
+    keep |= bits >= d.threshold ? 1u << k : 0u;
   }
+  return keep;
+}
+// Dropped elements become 0 whatever they hold, the others times the gain.
+__device__ __forceinline__ void drop8(Eight& x, unsigned keep, const Dropout& d) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x.v[k] = keep >> k & 1u ? x.v[k] * d.gain : 0.f;
 }
 
 // --------------------------------------------------------------------- rows

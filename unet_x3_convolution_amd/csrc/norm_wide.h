@@ -70,7 +70,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_wide(NormArgs a) {
                     g = vector8(gate, j, n, 1.f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) b.v[k] = (b.v[k] - s.mean) * s.r * w.v[k] + t.v[k];
-        if (a.drop.threshold) drop8(b, random.words(i * ((n + 7l) / 8) + j / 8), a.drop);
+        if (a.drop.threshold) drop8(b, kept8(random.words(i * ((n + 7l) / 8) + j / 8), a.drop), a.drop);
 #pragma unroll
         for (int k = 0; k < 8; ++k) b.v[k] = a.scale * x.v[k] + g.v[k] * b.v[k];
         store8<DT>(a.u, i * a.ldu + j, b, n - j);
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_back_wide(NormBackArgs a) {
       Eight h;
 #pragma unroll
       for (int k = 0; k < 8; ++k) h.v[k] = d.v[k] * g.v[k];
-      if (a.drop.threshold) drop8(h, random.words(i * ((n + 7l) / 8) + j / 8), a.drop);
+      if (a.drop.threshold) drop8(h, kept8(random.words(i * ((n + 7l) / 8) + j / 8), a.drop), a.drop);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         hat.v[k] = (hat.v[k] - r.o.mean) * r.o.r;
@@ -235,10 +235,10 @@ __global__ __launch_bounds__(kNormThreads) void norm_columns(NormBackArgs a) {
       along.v[k] = h.v[k] * hat.v[k];
     }
     if (a.drop.threshold) {
-      const uint4 words = random.words(i * ((n + 7l) / 8) + j / 8);
-      drop8(b, words, a.drop);
-      drop8(h, words, a.drop);
-      drop8(along, words, a.drop);
+      const unsigned keep = kept8(random.words(i * ((n + 7l) / 8) + j / 8), a.drop);
+      drop8(b, keep, a.drop);
+      drop8(h, keep, a.drop);
+      drop8(along, keep, a.drop);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
