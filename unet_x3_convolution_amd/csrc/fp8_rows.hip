@@ -69,21 +69,32 @@ struct PackLds {
 __device__ __forceinline__ int turned_row(int column) { return column ^ (column >> 6 & 1); }
 __device__ __forceinline__ int turned_unit(int column, int unit) { return unit ^ (column >> 3 & 7); }
 
-template <int DT>
-__device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, PackLds& lds) {
-  const long across = (a.n + kFp8Block - 1) / kFp8Block, tile_r = block / across;
-  const int tile_c = (int)(block - tile_r * across);
+// INSIDE: all of the tile lies in the matrix.  ACT: that of z, where there is a z; a
+// kernel for each, as the code of all of them takes longer to fetch than to run.
+template <int DT, bool INSIDE, int ACT>
+__device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long tile_r, int tile_c, PackLds& lds) {
   const int t = threadIdx.x, c = t & 15, g = t >> 4, wave = t >> 6;
   const long i0 = tile_r * kFp8Block + kTileRows * g;
   const int j = tile_c * kFp8Block + 8 * c;
+  typedef typename Storage<DT>::T E;
   Cell<DT> cell[kTileRows], slope[kTileRows];
   RawCodes slope8[kTileRows];
+  auto load = [&](Cell<DT> (&to)[kTileRows], const void* p, long ld) __attribute__((always_inline)) {
+    const E* at = static_cast<const E*>(p) + i0 * ld + j;
 #pragma unroll
-  for (int k = 0; k < kTileRows; ++k) cell[k].load(a.x, a.ldx, i0 + k, j, a.m, a.n);
-  if (a.z && !a.z8) {
-#pragma unroll
-    for (int k = 0; k < kTileRows; ++k) slope[k].load(a.z, a.ldz, i0 + k, j, a.m, a.n);
-  } else if (a.z) {
+    for (int k = 0; k < kTileRows; ++k) {
+      if constexpr (INSIDE) {
+        __builtin_memcpy(&to[k].raw.e, at, sizeof(to[k].raw.e));
+        at += ld;
+      } else {
+        to[k].load(p, ld, i0 + k, j, a.m, a.n);
+      }
+    }
+  };
+  load(cell, a.x, a.ldx);
+  if (ACT != OIDN_ACT_NONE && a.z && !a.z8) {
+    load(slope, a.z, a.ldz);
+  } else if (ACT != OIDN_ACT_NONE && a.z) {
 #pragma unroll
     for (int k = 0; k < kTileRows; ++k)
       slope8[k] = load_codes(ckpt_at(const_cast<void*>(a.z), a.m, a.n), i0 + k < a.m ? i0 + k : a.m - 1,
@@ -92,13 +103,13 @@ __device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, Pack
   Eight v[kTileRows];
 #pragma unroll
   for (int k = 0; k < kTileRows; ++k) {
-    v[k] = cell[k].value();
-    if (a.z) {
-      Eight z = a.z8 ? slope8[k].value() : slope[k].value(), value;
-      activate_slope8<DT>(a.act, z, value);
+    v[k] = INSIDE ? cell[k].raw.value() : cell[k].value();
+    if (ACT != OIDN_ACT_NONE && a.z) {
+      Eight z = a.z8 ? slope8[k].value() : INSIDE ? slope[k].raw.value() : slope[k].value(), value;
+      activate_slope8<DT>(ACT, z, value);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < cell[k].n) v[k].v[e] *= z.v[e];
+        if (INSIDE || e < cell[k].n) v[k].v[e] *= z.v[e];
     }
   }
   unsigned row_top[kTileRows], col_top[8] = {}, top = 0;
@@ -167,7 +178,7 @@ __device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, Pack
     for (int k = 0; k < kTileRows; ++k) {
       const long i = i0 + k;
       const int p = fp8_power(a.square ? row_top[k] : lanes_max<16>(row_top[k]));
-      if (i >= a.m) continue;
+      if (!INSIDE && i >= a.m) continue;
       *reinterpret_cast<uint2*>(at.codes + i * at.pitch + j) = fp8_codes(v[k].v, power_of_two(-p));
       if (c == 0) at.scales[i * at.words + tile_c] = (unsigned char)(p + 127);
     }
@@ -182,25 +193,30 @@ __device__ __forceinline__ void pack_tile(const Fp8PackArgs& a, long block, Pack
 #pragma unroll
       for (int k = 0; k < kTileRows; ++k) f[k] = v[k].v[e];
       lds.codes[turned_row(column)][4 * turned_unit(column, g >> 2) + (g & 3)] = fp8_codes4(f, inverse);
-      if (g == 0 && j + e < a.n) at.scales[(j + e) * at.words + tile_r] = (unsigned char)(p + 127);
+      if (g == 0 && (INSIDE || j + e < a.n)) at.scales[(j + e) * at.words + tile_r] = (unsigned char)(p + 127);
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kFp8Block * kFp8Block / 16 / kTileThreads; ++k) {
       const int u = t + k * kTileThreads, column = u >> 3, unit = u & 7;
       const long col = tile_c * (long)kFp8Block + column;
-      if (col < a.n)
+      if (INSIDE || col < a.n)
         *reinterpret_cast<uint4*>(at.codes + col * at.pitch + tile_r * kFp8Block + 16 * unit) =
             *reinterpret_cast<const uint4*>(&lds.codes[turned_row(column)][4 * turned_unit(column, unit)]);
     }
   }
 }
 
-template <int DT>
+template <int DT, int ACT>
 __global__ __launch_bounds__(kTileThreads) void fp8_pack_tiles(Fp8PackArgs a, Fp8PackArgs b, int first) {
   __shared__ __attribute__((aligned(16))) PackLds lds;
-  if ((int)blockIdx.x < first) pack_tile<DT>(a, blockIdx.x, lds);
-  else pack_tile<DT>(b, (int)blockIdx.x - first, lds);
+  const bool second = (int)blockIdx.x >= first;
+  const Fp8PackArgs& p = second ? b : a;
+  const long block = (int)blockIdx.x - (second ? first : 0), across = (p.n + kFp8Block - 1) / kFp8Block;
+  const long tile_r = block / across;
+  const int tile_c = (int)(block - tile_r * across);
+  if ((tile_r + 1) * kFp8Block <= p.m && (tile_c + 1) * kFp8Block <= p.n) pack_tile<DT, true, ACT>(p, tile_r, tile_c, lds);
+  else pack_tile<DT, false, ACT>(p, tile_r, tile_c, lds);
 }
 
 // A thread takes eight columns.  A finite value whose rounding passes the type's
@@ -242,7 +258,12 @@ void launch(const Fp8PackArgs& a, const Fp8PackArgs& b, hipStream_t stream) {
     return;
   }
   const long first = fp8_tiles(a.m, a.n), second = b.x ? fp8_tiles(b.m, b.n) : 0;
-  hipLaunchKernelGGL(fp8_pack_tiles<DT>, dim3((unsigned)(first + second)), dim3(kTileThreads), 0, stream, a, b, (int)first);
+  const dim3 grid((unsigned)(first + second)), block(kTileThreads);
+  const int act = a.z ? a.act : OIDN_ACT_NONE;
+  if (act == OIDN_ACT_NONE) hipLaunchKernelGGL((fp8_pack_tiles<DT, OIDN_ACT_NONE>), grid, block, 0, stream, a, b, (int)first);
+  else if (act == OIDN_ACT_RELU) hipLaunchKernelGGL((fp8_pack_tiles<DT, OIDN_ACT_RELU>), grid, block, 0, stream, a, b, (int)first);
+  else if (act == OIDN_ACT_SILU) hipLaunchKernelGGL((fp8_pack_tiles<DT, OIDN_ACT_SILU>), grid, block, 0, stream, a, b, (int)first);
+  else hipLaunchKernelGGL((fp8_pack_tiles<DT, OIDN_ACT_GELU>), grid, block, 0, stream, a, b, (int)first);
 }
 
 }  // namespace
