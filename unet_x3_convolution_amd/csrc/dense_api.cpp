@@ -28,7 +28,7 @@ void plan_together(Product* const* p, int count) {
   bool direct = true;
   for (int k = 0; k < count; ++k) {
     plans[k] = &p[k]->plan;
-    shapes[k] = {p[k]->rows, p[k]->cols, p[k]->len, p[k]->epi};
+    shapes[k] = {p[k]->rows, p[k]->cols, p[k]->len, p[k]->epi, 0};
     direct = direct && direct_sizes(*p[k]);
   }
   plan_products(plans, shapes, count, p[0]->dtype, direct);
@@ -321,6 +321,8 @@ void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, i
   double best = 0;
   for (int c = 0; c < choices; ++c) {
     const TileCost t = shapes[0].epi == kEpiGated && table[c].tile == 64 ? kCostGated : table[c];
+    // smaller tiles' activations run beside other workgroups' multiplications
+    const double each = t.each + shapes[0].extra * (t.tile == 256 ? 1.0 : t.tile == 128 ? 0.16 : 0.05);
     long tiles[kMaxGroup], kt[kMaxGroup], longest = 1;
     for (int k = 0; k < count; ++k) {
       const PlanShape& s = shapes[k];
@@ -357,7 +359,7 @@ void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, i
         q = whole;
       }
       const double pace = t.share * work / kCus;
-      const double cost = t.start + t.each * q + (pace > own ? pace : own) + (slices > 0 ? kSliceLaunch + slices : 0);
+      const double cost = t.start + each * q + (pace > own ? pace : own) + (slices > 0 ? kSliceLaunch + slices : 0);
       if (best == 0 || cost < best) {
         best = cost;
         for (int k = 0; k < count; ++k) *plans[k] = tried[k];

@@ -34,6 +34,7 @@ int check_layer(long m, int k, int n, int dtype) {
 
 struct Product8 {
   long rows, cols, len;    // len: bytes of a row
+  int act;
   GemmPlan plan;
 };
 // Plans products that share a launch, as 16-bit ones of half the length: a staged
@@ -43,7 +44,11 @@ void plan_together(Product8* const* p, int count) {
   PlanShape shapes[kMaxGroup8];
   for (int k = 0; k < count; ++k) {
     plans[k] = &p[k]->plan;
-    shapes[k] = {p[k]->rows, p[k]->cols, p[k]->len / 2, kEpiStore};
+    // A 256 x 256 tile's activation stands beside a loop half as long as a 16-bit product's
+    // (us, 256 x 256 against 128 x 128: 8192 x 1024 -> 4096 plain 49 and 49, gelu 68 and 61; 8192
+    // x 4096 -> 4096 gelu 132 and 140).
+    const double extra[] = {0, 2, 5, 10};      // none, relu, silu, gelu
+    shapes[k] = {p[k]->rows, p[k]->cols, p[k]->len / 2, kEpiStore, extra[p[k]->act]};
   }
   plan_products(plans, shapes, count, OIDN_F16, true);
   for (int k = 0; k < count; ++k) {
@@ -52,7 +57,9 @@ void plan_together(Product8* const* p, int count) {
     p[k]->plan.splits = (int)((tiles + p[k]->plan.per_split - 1) / p[k]->plan.per_split);
   }
 }
-Product8 product8(long rows, long cols, long len) { return Product8{rows, cols, fp8_cols(len), {}}; }
+Product8 product8(long rows, long cols, long len, int act = OIDN_ACT_NONE) {
+  return Product8{rows, cols, fp8_cols(len), act, {}};
+}
 size_t slice_bytes(const Product8& p) {
   return p.plan.splits > 1 ? align256((size_t)p.plan.splits * p.rows * p.cols * sizeof(float)) : 0;
 }
@@ -89,9 +96,9 @@ struct Forward {
   void *x8, *slices;
   size_t bytes;
 };
-Forward forward(long m, int k, int n, unsigned flags, void* ws) {
+Forward forward(long m, int k, int n, int act, unsigned flags, void* ws) {
   Forward f{};
-  f.p = product8(m, n, k);
+  f.p = product8(m, n, k, act);
   const bool x8 = flags & OIDN_X_FP8;
   f.narrow = !x8 && k <= kFp8Block && m > kCodedRows;
   f.few = !f.narrow && m <= kFewRows;
@@ -187,9 +194,12 @@ int oidn_linear_fp8_workspace_bytes(long m, int k, int n, int dtype, unsigned fl
   OIDN_TRY(check_flags(flags, OIDN_X_FP8 | OIDN_Z_CKPT8));
   *bytes = 0;
   if (m) {
-    const Forward f = forward(m, k, n, flags, nullptr);
-    OIDN_TRY(check_forward_launch(f, m, k));
-    *bytes = f.bytes;
+    // the plan goes by the activation too: enough for each
+    for (int act = OIDN_ACT_NONE; act <= OIDN_ACT_GELU; ++act) {
+      const Forward f = forward(m, k, n, act, flags, nullptr);
+      OIDN_TRY(check_forward_launch(f, m, k));
+      *bytes = std::max(*bytes, f.bytes);
+    }
   }
   return clear_error();
 }
@@ -210,7 +220,7 @@ int oidn_linear_fp8(const void* x, long ldx, const void* w8, const float* bias, 
   OIDN_TRY(check_matrix("y", y, ldy, n, dtype, false));
   if (z8) OIDN_TRY(check_blob("z", z));
   else OIDN_TRY(check_matrix("z", z, ldz, n, dtype, true));
-  const Forward f = forward(m, k, n, flags, workspace);
+  const Forward f = forward(m, k, n, act, flags, workspace);
   OIDN_TRY(check_forward_launch(f, m, k));
   OIDN_TRY(check_workspace(workspace, ws_bytes, f.bytes));
   if (f.pack) {
