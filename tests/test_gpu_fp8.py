@@ -192,6 +192,24 @@ def test_whole_numbers_are_exact(m, k, n):
     assert loss(run(x, w + step_w)) - loss(y) == float((dw * step_w).sum())
 
 
+@pytest.mark.parametrize("m, k, n", [(8200, 2056, 4104), (130568, 72, 136), (2056, 8200, 264)])
+def test_whole_numbers_in_large_tiles(m, k, n):
+    """The same over many tiles of each size, partial ones at every edge, against products in fp32 (sums below 2^24 are
+    exact there; results below 2^11 are exact in fp16)."""
+    g = torch.Generator(device="cuda").manual_seed(k)
+    rand = lambda most, *shape: torch.randint(-most, most + 1, shape, generator=g, device="cuda").half()  # noqa: E731
+    share = lambda t, of: t * (torch.rand(t.shape, generator=g, device="cuda") < of)  # noqa: E731
+    x, w, dy = share(rand(2, m, k), 400 / max(m, k, 400)), rand(1, n, k), share(rand(1, m, n), 400 / max(m, n, 400))
+    want = [x.float() @ w.float().T, dy.float() @ w.float(), dy.float().T @ x.float()]
+    assert all(float(t.abs().max()) <= 2048 for t in want)
+    y = run_linear(x, packed(w, U.OIDN_FP8_SQUARE), n, None, None, "none", "f16").get()
+    dx, dw, db = (t.get() for t in run_back(dy, x, None, w, "none", "f16"))
+    for got, v in zip((y, dx, dw, db[0]), want + [dy.float().sum(0)]):
+        assert torch.equal(got.float(), v)
+    y = run_linear(packed(x), packed(w, U.OIDN_FP8_SQUARE), n, None, None, "relu", "f16", flags=U.OIDN_X_FP8, m=m, k=k).get()
+    assert torch.equal(y.float(), want[0].clamp_min(0))
+
+
 @pytest.mark.parametrize("precision", HALVES)
 @pytest.mark.parametrize("m", [1, 20, 70])
 def test_linear_keeps_rows_apart(m, precision):
@@ -205,7 +223,7 @@ def test_linear_keeps_rows_apart(m, precision):
     assert y[bad].isnan().all() and y[~bad].isfinite().all()
 
 
-@pytest.mark.parametrize("m, k, n", [(5, 200, 96), (40, 200, 100), (300, 130, 264)])
+@pytest.mark.parametrize("m, k, n", [(5, 200, 96), (40, 200, 100), (100, 96, 70), (300, 130, 264)])
 def test_z_in_eight_bits(m, k, n):
     mk = Maker(9, "f16")
     x, w, bias = mk.rows(m, k), mk.rows(n, k, scale=k ** -0.5), mk.vec(n)

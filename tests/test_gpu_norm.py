@@ -276,7 +276,7 @@ def test_norm_residual_backward(m, n, kind, precision):
 
 
 @pytest.mark.parametrize("gate_rows", [1, 2, 15, 16, 17, 100, 333, 1000, 1500])
-@pytest.mark.parametrize("m, n", [(1000, 24), (333, 520)])
+@pytest.mark.parametrize("m, n", [(1000, 24), (333, 520), (120, 4800), (50, 8200)])
 def test_gate_groups(m, n, gate_rows):
     """Groups shorter and longer than a workgroup's rows, the last one short."""
     c = back_case(m, n, "rms", "rms", "f32", 25)
@@ -314,7 +314,7 @@ def test_norm_backward(m, n, kind, precision):
         check(dw.get()[0], want["dnext_weight"], "f32", "dweight")
 
 
-@pytest.mark.parametrize("n", [40, 700, 9000])
+@pytest.mark.parametrize("n", [40, 700, 1600, 4800, 9000])
 @pytest.mark.parametrize("asked", ["dx", "d_o", "dgate", "dweight", "dshift", "dnext_weight", "dnext_shift", "nothing"])
 def test_backward_parts(asked, n):
     """Each gradient alone: the same bits as all at once."""
