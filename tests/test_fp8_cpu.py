@@ -14,7 +14,7 @@ P = 4096          # a 16-byte aligned non-null "address"
 
 @pytest.fixture(scope="module", autouse=True)
 def built_library():
-    if not os.path.exists(U.LIB_PATH):
+    if not (os.path.exists(U.LIB_PATH) and os.path.exists(U.BINDING_PATH)):
         from unet_x3_convolution_amd import build
         build.build(verbose=False)
     U.lib()

@@ -15,7 +15,7 @@ NAN, INF = float("nan"), float("inf")
 
 @pytest.fixture(scope="module", autouse=True)
 def built_library():
-    if not os.path.exists(U.LIB_PATH):
+    if not (os.path.exists(U.LIB_PATH) and os.path.exists(U.BINDING_PATH)):
         from unet_x3_convolution_amd import build
         build.build(verbose=False)
     U.lib()

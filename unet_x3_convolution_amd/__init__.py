@@ -14,6 +14,7 @@ import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liboidn_mi355x.so")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 
 OIDN_OK = 0
 OIDN_E_INVALID = -1
@@ -184,6 +185,21 @@ def lib() -> ctypes.CDLL:
             fn.restype = res
         _lib = L
     return _lib
+
+
+_native = None
+
+
+def _calls():
+    """The calls of csrc/binding.cpp: they take tensors, and cost less of the host's time than ctypes."""
+    global _native
+    if _native is None:
+        lib()
+        if not os.path.exists(BINDING_PATH):
+            raise OidnError(OIDN_E_HIP, f"{BINDING_PATH} is not built; run __graft_entry__.build()")
+        from . import _binding
+        _native = _binding
+    return _native
 
 
 def _check_single_hip_runtime():
@@ -524,11 +540,11 @@ def oidn_fp8_bytes(m: int, n: int) -> int:
 
 
 def oidn_fp8_pack(x, ldx: int, m: int, n: int, packed, packed_t, dtype: int, flags: int, stream=None):
-    _check(lib().oidn_fp8_pack(_p(x), ldx, m, n, _p(packed), _p(packed_t), dtype, flags, _s(stream)))
+    _check(_calls().oidn_fp8_pack(x, ldx, m, n, packed, packed_t, dtype, flags, _s(stream)))
 
 
 def oidn_fp8_unpack(packed, m: int, n: int, y, ldy: int, dtype: int, stream=None):
-    _check(lib().oidn_fp8_unpack(_p(packed), m, n, _p(y), ldy, dtype, _s(stream)))
+    _check(_calls().oidn_fp8_unpack(packed, m, n, y, ldy, dtype, _s(stream)))
 
 
 def oidn_linear_fp8_workspace_bytes(m: int, k: int, n: int, dtype: int, flags: int) -> int:
@@ -537,8 +553,8 @@ def oidn_linear_fp8_workspace_bytes(m: int, k: int, n: int, dtype: int, flags: i
 
 def oidn_linear_fp8(x, ldx: int, w8, bias, residual, ldr: int, y, ldy: int, z, ldz: int, m: int, k: int, n: int,
                     act: int, dtype: int, flags: int, workspace, ws_bytes: int, stream=None):
-    _check(lib().oidn_linear_fp8(_p(x), ldx, _p(w8), _p(bias), _p(residual), ldr, _p(y), ldy, _p(z), ldz, m, k, n,
-                                 act, dtype, flags, _p(workspace), ws_bytes, _s(stream)))
+    _check(_calls().oidn_linear_fp8(x, ldx, w8, bias, residual, ldr, y, ldy, z, ldz, m, k, n, act, dtype, flags,
+                                    workspace, ws_bytes, _s(stream)))
 
 
 def oidn_linear_fp8_backward_workspace_bytes(m: int, k: int, n: int, act: int, dtype: int, flags: int) -> int:
@@ -548,15 +564,14 @@ def oidn_linear_fp8_backward_workspace_bytes(m: int, k: int, n: int, act: int, d
 def oidn_linear_fp8_backward(dy, lddy: int, x, ldx: int, z, ldz: int, w8t, dx, lddx: int, dw, lddw: int, dbias,
                              m: int, k: int, n: int, act: int, dtype: int, flags: int, workspace, ws_bytes: int,
                              stream=None):
-    _check(lib().oidn_linear_fp8_backward(_p(dy), lddy, _p(x), ldx, _p(z), ldz, _p(w8t), _p(dx), lddx, _p(dw), lddw,
-                                          _p(dbias), m, k, n, act, dtype, flags, _p(workspace), ws_bytes,
-                                          _s(stream)))
+    _check(_calls().oidn_linear_fp8_backward(dy, lddy, x, ldx, z, ldz, w8t, dx, lddx, dw, lddw, dbias, m, k, n, act,
+                                             dtype, flags, workspace, ws_bytes, _s(stream)))
 
 
 # ------------------------------------------------- around a block over rows
 def oidn_norm(x, ldx: int, weight, shift, y, ldy: int, m: int, n: int, norm: int, eps: float, dtype: int,
               stream=None):
-    _check(lib().oidn_norm(_p(x), ldx, _p(weight), _p(shift), _p(y), ldy, m, n, norm, eps, dtype, _s(stream)))
+    _check(_calls().oidn_norm(x, ldx, weight, shift, y, ldy, m, n, norm, eps, dtype, _s(stream)))
 
 
 def oidn_norm_backward_workspace_bytes(m: int, n: int, dtype: int) -> int:
@@ -565,17 +580,17 @@ def oidn_norm_backward_workspace_bytes(m: int, n: int, dtype: int) -> int:
 
 def oidn_norm_backward(dy, lddy: int, x, ldx: int, weight, add, ldadd: int, dx, lddx: int, dweight, dshift, m: int,
                        n: int, norm: int, eps: float, dtype: int, workspace, ws_bytes: int, stream=None):
-    _check(lib().oidn_norm_backward(_p(dy), lddy, _p(x), ldx, _p(weight), _p(add), ldadd, _p(dx), lddx, _p(dweight),
-                                    _p(dshift), m, n, norm, eps, dtype, _p(workspace), ws_bytes, _s(stream)))
+    _check(_calls().oidn_norm_backward(dy, lddy, x, ldx, weight, add, ldadd, dx, lddx, dweight, dshift, m, n, norm,
+                                       eps, dtype, workspace, ws_bytes, _s(stream)))
 
 
 def oidn_norm_residual(o, ldo: int, weight, shift, gate, ldg: int, gate_rows: int, x, ldx: int, scale: float,
                        p: float, rng, u, ldu: int, next_weight, next_shift, v, ldv: int, m: int, n: int, norm: int,
                        next_norm: int, eps: float, dtype: int, stream=None):
     """rng: two 64-bit words in device memory (an int64 tensor of seed and offset)."""
-    _check(lib().oidn_norm_residual(_p(o), ldo, _p(weight), _p(shift), _p(gate), ldg, gate_rows, _p(x), ldx, scale,
-                                    p, _p(rng), _p(u), ldu, _p(next_weight), _p(next_shift), _p(v), ldv, m, n, norm,
-                                    next_norm, eps, dtype, _s(stream)))
+    _check(_calls().oidn_norm_residual(o, ldo, weight, shift, gate, ldg, gate_rows, x, ldx, scale, p, rng, u, ldu,
+                                       next_weight, next_shift, v, ldv, m, n, norm, next_norm, eps, dtype,
+                                       _s(stream)))
 
 
 def oidn_norm_residual_backward_workspace_bytes(m: int, n: int, gate_rows: int, dtype: int) -> int:
@@ -587,16 +602,16 @@ def oidn_norm_residual_backward(du, lddu: int, dv, lddv: int, o, ldo: int, weigh
                                 d_o, lddo: int, dgate, lddg: int, dweight, dshift, dnext_weight, dnext_shift, m: int,
                                 n: int, norm: int, next_norm: int, eps: float, dtype: int, workspace, ws_bytes: int,
                                 stream=None):
-    _check(lib().oidn_norm_residual_backward(
-        _p(du), lddu, _p(dv), lddv, _p(o), ldo, _p(weight), _p(shift), _p(gate), ldg, gate_rows, _p(u), ldu, scale, p,
-        _p(rng), _p(next_weight), _p(dx), lddx, _p(d_o), lddo, _p(dgate), lddg, _p(dweight), _p(dshift),
-        _p(dnext_weight), _p(dnext_shift), m, n, norm, next_norm, eps, dtype, _p(workspace), ws_bytes, _s(stream)))
+    _check(_calls().oidn_norm_residual_backward(du, lddu, dv, lddv, o, ldo, weight, shift, gate, ldg, gate_rows, u,
+                                                ldu, scale, p, rng, next_weight, dx, lddx, d_o, lddo, dgate, lddg,
+                                                dweight, dshift, dnext_weight, dnext_shift, m, n, norm, next_norm,
+                                                eps, dtype, workspace, ws_bytes, _s(stream)))
 
 
 def oidn_dropout(x, ldx: int, residual, ldr: int, y, ldy: int, m: int, n: int, p: float, rng, dtype: int,
                  stream=None):
     """rng: two 64-bit words in device memory (an int64 tensor of seed and offset)."""
-    _check(lib().oidn_dropout(_p(x), ldx, _p(residual), ldr, _p(y), ldy, m, n, p, _p(rng), dtype, _s(stream)))
+    _check(_calls().oidn_dropout(x, ldx, residual, ldr, y, ldy, m, n, p, rng, dtype, _s(stream)))
 
 
 def oidn_calibrate_mfma(dtype: int, iters: int, blocks: int, sink, stream=None) -> int:
