@@ -35,6 +35,17 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
   }
 }
+// Over the lanes of a wave that are a multiple of N apart, N from 4 to 64.
+template <int N>
+__device__ __forceinline__ float strided_sum(float v) {
+  // rotated by 8, by 4 in 16 lanes
+  if constexpr (N <= 8) v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x128, 0xF, 0xF, false));
+  if constexpr (N <= 4) v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x124, 0xF, 0xF, false));
+  const auto add = [](unsigned a, unsigned b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); };
+  if constexpr (N <= 16) v = __uint_as_float(combine_lanes<16>(__float_as_uint(v), add));
+  if constexpr (N <= 32) v = __uint_as_float(combine_lanes<32>(__float_as_uint(v), add));
+  return v;
+}
 template <int N, int FROM = 1>
 __device__ __forceinline__ unsigned lanes_max(unsigned v) {
   if constexpr (FROM < N)

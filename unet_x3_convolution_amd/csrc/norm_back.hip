@@ -7,10 +7,13 @@ namespace {
 
 // Sums of partial rows: kinds 0 .. kNormSums - 1 over all chunks, then a gate
 // group's chunks.  A workgroup takes kAcross columns, its threads share the rows,
-// whose sums are added in order.
-constexpr int kAcross = 16;
-__global__ __launch_bounds__(kNormThreads) void norm_finish(NormBackArgs a) {
-  __shared__ float lds[kNormThreads];
+// whose sums are added in order.  Bound by the latency of few loads at narrow rows and by
+// memory at wide ones: 16 columns and 16 lines of threads instead take 2 us more of
+// 16384 x 4096 and 6 of 4096 x 8192, and no less at 96 columns.
+constexpr int kAcross = 32, kFinishThreads = 512;
+__global__ __launch_bounds__(kFinishThreads) void norm_finish(NormBackArgs a) {
+  constexpr int kLines = kFinishThreads / kAcross;
+  __shared__ float lds[kFinishThreads];
   const int c = threadIdx.x % kAcross, l = threadIdx.x / kAcross, n = a.n;
   const long j = (long)blockIdx.x * kAcross + c, what = blockIdx.y;
   const float* p;
@@ -31,13 +34,14 @@ __global__ __launch_bounds__(kNormThreads) void norm_finish(NormBackArgs a) {
   if (!out) return;
   float s = 0.f;
   if (j < n) {
-#pragma unroll 8
-    for (long g = l; g < count; g += kNormThreads / kAcross) s += p[g * step + j];
+#pragma unroll 16
+    for (long g = l; g < count; g += kLines) s += p[g * step + j];
   }
   lds[threadIdx.x] = s;
   __syncthreads();
   if (l == 0 && j < n) {
-    for (int k = 1; k < kNormThreads / kAcross; ++k) s += lds[k * kAcross + c];
+#pragma unroll
+    for (int k = 1; k < kLines; ++k) s += lds[k * kAcross + c];
     out[j] = s;
   }
 }
@@ -81,7 +85,7 @@ hipError_t launch_type(const NormBackArgs& a, hipStream_t stream) {
   const long groups = a.dgate && a.chunks.per_group > 1 ? a.chunks.count / a.chunks.per_group : 0;
   if (e != hipSuccess || !columns || (a.chunks.count == 1 && !groups)) return e;
   hipLaunchKernelGGL(norm_finish, dim3((unsigned)((a.n + kAcross - 1l) / kAcross), (unsigned)(kNormSums + groups)),
-                     dim3(kNormThreads), 0, stream, a);
+                     dim3(kFinishThreads), 0, stream, a);
   return hipGetLastError();
 }
 

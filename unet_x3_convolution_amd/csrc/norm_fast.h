@@ -184,28 +184,28 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_rows(NormArgs a) {
 // chunk's rows and are added over the row lanes at its end; a gate's, where chunks hold
 // whole groups, at the group's end: groups of few rows are a row lane's each, others
 // the whole workgroup's.
-template <int LANES>
-struct ColumnSum {
-  static constexpr int kWaves = LANES > 64 ? 1 : norm_threads<LANES>() / 64;
-  typedef float Lds[kWaves][LANES > 64 ? 1 : LANES * 8];
-  // Adds over the row lanes; the sums are in the first one's threads.
-  static __device__ __forceinline__ void over_rows(Eight& x, Lds& lds) {
+// Column sums of a workgroup's COUNT kinds, in LDS: a kind's sums over each wave's rows,
+// which the threads then add, every column by one of them.
+template <int LANES, int COUNT>
+struct ColumnSums {
+  static constexpr int kThreads = norm_threads<LANES>(), kWaves = LANES > 64 ? 1 : kThreads / 64, kColumns = 8 * LANES;
+  typedef float Lds[LANES > 64 ? 1 : COUNT][kWaves][LANES > 64 ? 1 : kColumns];
+  // Puts a kind's; where a row is more than a wave there is nothing to add.
+  static __device__ __forceinline__ void put(Eight& x, int kind, Lds& lds) {
     if constexpr (LANES <= 64) {
       const int lane = threadIdx.x & 63;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 8; ++e) x.v[e] = strided_sum<LANES>(x.v[e]);
+      if (lane < LANES) __builtin_memcpy(&lds[kind][threadIdx.x >> 6][8 * lane], x.v, 32);
+    }
+  }
+  // Columns' sums to `out`, all of the workgroup's threads calling; between barriers.
+  static __device__ __forceinline__ void get(int kind, const Lds& lds, float* out, int n) {
+    for (int j = threadIdx.x; j < n; j += kThreads) {
+      float s = 0.f;
 #pragma unroll
-        for (int s = LANES; s < 64; s *= 2) x.v[e] += __shfl_xor(x.v[e], s);
-        if (lane < LANES) lds[threadIdx.x >> 6][e * LANES + lane] = x.v[e];
-      }
-      __syncthreads();
-      if (threadIdx.x < LANES) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-#pragma unroll
-          for (int w = 1; w < kWaves; ++w) x.v[e] += lds[w][e * LANES + threadIdx.x];
-      }
-      __syncthreads();
+      for (int w = 0; w < kWaves; ++w) s += lds[kind][w][j];
+      out[j] = s;
     }
   }
 };
@@ -214,9 +214,10 @@ struct ColumnSum {
 template <int DT, int LANES, bool BRANCH, bool WHOLE, bool SHIFTS>
 __global__ __launch_bounds__(norm_threads<LANES>(), LANES >= 128 && !SHIFTS ? 4 : 1) void norm_back_rows(NormBackArgs a) {
   constexpr int kThreads = norm_threads<LANES>(), kRowLanes = kThreads / LANES;
-  typedef ColumnSum<LANES> Columns;
+  constexpr int kSums = SHIFTS ? 4 : 2;
+  typedef ColumnSums<LANES, BRANCH ? kSums : kSums / 2> Columns;
   __shared__ float2 lds[2][RowSum<LANES>::kWaves];
-  __shared__ typename Columns::Lds column_lds;
+  __shared__ __attribute__((aligned(16))) typename Columns::Lds column_lds;
   // the norms' weights, read again for every row: held in registers they leave a unit half
   // as many waves
   __shared__ __attribute__((aligned(16))) float vectors[3][8 * LANES];
@@ -227,15 +228,14 @@ __global__ __launch_bounds__(norm_threads<LANES>(), LANES >= 128 && !SHIFTS ? 4 
   const NormChunks& c = a.chunks;
   RowSum<LANES> sum(lds);
   Eight along{}, total{}, next_along{}, next_total{}, gate_sum{};
-  if (lane == 0) {
-    auto hold = [&](int which, const Eight& v) { __builtin_memcpy(&vectors[which][j], v.v, 32); };
+  auto hold_all = [&]() __attribute__((always_inline)) {
+    auto hold = [&](int which, const Eight& v) __attribute__((always_inline)) { __builtin_memcpy(&vectors[which][j], v.v, 32); };
     if constexpr (BRANCH) {
       hold(0, unit_of<WHOLE>(a.weight, j, n, 1.f));
       hold(1, unit_of<WHOLE>(a.shift, j, n, 0.f));
     }
     if (a.dv) hold(2, unit_of<WHOLE>(a.next_weight, j, n, 1.f));
-  }
-  __syncthreads();
+  };
   auto held = [&](int which) __attribute__((always_inline)) {
     Eight v;
     __builtin_memcpy(v.v, &vectors[which][j], 32);
@@ -366,28 +366,45 @@ __global__ __launch_bounds__(norm_threads<LANES>(), LANES >= 128 && !SHIFTS ? 4 
     const long begin = g + (alone ? lane * span : 0), end = begin + span < last ? begin + span : last;
     long i = begin + (alone ? 0 : lane);
     load(i);
+    if (g == first) {                                    // behind the first row's loads
+      if (lane == 0) hold_all();
+      __syncthreads();
+    }
     for (long r = begin; r < end; r += lanes, i += lanes) row(i, i < end, r + lanes < end ? i + lanes : -1);
     if (BRANCH && a.dgate) {
-      if (!alone) Columns::over_rows(gate_sum, column_lds);
       float* const out = c.per_group > 1 ? a.gate_part + chunk * n
                                          : a.dgate + (c.per_group ? group : begin / c.group_rows) * a.lddg;
-      if (alone ? begin < end : lane == 0) put8<OIDN_F32, WHOLE>(out, j, gate_sum, left);
+      if (alone || LANES > 64) {
+        if (begin < end || !alone) put8<OIDN_F32, WHOLE>(out, j, gate_sum, left);
+      } else {
+        Columns::put(gate_sum, 0, column_lds);
+        __syncthreads();
+        Columns::get(0, column_lds, out, n);
+        __syncthreads();
+      }
       gate_sum = Eight{};
     }
     g += alone ? span * kRowLanes : span;
   } while (g < last);
-  auto finish = [&](int which, Eight& x) __attribute__((always_inline)) {
-    if (!a.sums[which]) return;
-    Columns::over_rows(x, column_lds);
-    if (lane == 0)
-      put8<OIDN_F32, WHOLE>(c.count > 1 ? a.part + (chunk * kNormSums + which) * n : a.sums[which], j, x, left);
+  auto each_kind = [&](auto take) __attribute__((always_inline)) {
+    if constexpr (BRANCH) {
+      if (a.sums[0]) take(0, 0, along);
+      if constexpr (SHIFTS) if (a.sums[1]) take(1, 1, total);
+    }
+    constexpr int kFirst = BRANCH ? kSums / 2 : 0;
+    if (a.sums[2]) take(2, kFirst, next_along);
+    if constexpr (SHIFTS) if (a.sums[3]) take(3, kFirst + 1, next_total);
   };
-  if constexpr (BRANCH) {
-    finish(0, along);
-    if constexpr (SHIFTS) finish(1, total);
+  auto out_of = [&](int which) __attribute__((always_inline)) {
+    return c.count > 1 ? a.part + (chunk * kNormSums + which) * n : a.sums[which];
+  };
+  if constexpr (LANES > 64) {
+    each_kind([&](int which, int, Eight& x) __attribute__((always_inline)) { put8<OIDN_F32, WHOLE>(out_of(which), j, x, left); });
+  } else {
+    each_kind([&](int, int at, Eight& x) __attribute__((always_inline)) { Columns::put(x, at, column_lds); });
+    __syncthreads();
+    each_kind([&](int which, int at, Eight&) __attribute__((always_inline)) { Columns::get(at, column_lds, out_of(which), n); });
   }
-  finish(2, next_along);
-  if constexpr (SHIFTS) finish(3, next_total);
 }
 
 }  // namespace
