@@ -173,10 +173,12 @@ hipError_t launch_split_sum(const EpilogueArgs& e, int splits, int dtype, hipStr
 
 // What ends a backward pass, in one launch: sums of products' slices
 // (kEpiStore) and of partial column sums, all in a fixed order.
+// out[j] = the sum of part[0 .. groups][j]
+struct ColumnJob { const float* part; long groups; int cols; float* out; };
 struct FinishArgs {
   int products, columns;
   struct { EpilogueArgs e; int splits; } product[kMaxGroup];
-  struct { const float* part; long groups; int cols; float* out; } column[2];
+  ColumnJob column[2];
 };
 hipError_t launch_finish(const FinishArgs& a, int dtype, hipStream_t stream);
 

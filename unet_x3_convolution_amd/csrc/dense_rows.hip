@@ -5,6 +5,7 @@
 // Small ones take a launch's 2 to 3 us; 32640 x 112 fp16 goes to 8 bits in 5.2 us
 // and back in 4.0, 16384 x 2048 bf16 (103 MB) in 22.6 us (4.6 TB/s), there and back
 // in 40.
+#include "dense_columns.h"
 #include "dense_slope.h"
 
 namespace oidn {
@@ -56,26 +57,6 @@ __global__ __launch_bounds__(kRowThreads) void split_sum(EpilogueArgs e, int spl
   sum_slices<DT, kEpiLinear>(e, splits, lg, blockIdx.x, lds);
 }
 
-// Columns of partial sums, 256 / lanes of them a workgroup: each is shared by
-// `lanes` threads, eight reads in flight each, added in order.
-__device__ __forceinline__ void sum_columns(const float* __restrict__ part, long groups, int cols,
-                                            float* __restrict__ out, int block, int lanes, char* mem) {
-  const int across = kRowThreads / lanes, c = threadIdx.x % across, l = threadIdx.x / across, j = block * across + c;
-  float s = 0.f;
-  if (j < cols) {
-#pragma unroll 8
-    for (long g = l; g < groups; g += lanes) s += part[g * cols + j];
-  }
-  float* const lds = reinterpret_cast<float*>(mem);
-  lds[threadIdx.x] = s;
-  __syncthreads();
-  if (l == 0 && j < cols) {
-    for (int k = 1; k < lanes; ++k) s += lds[k * across + c];
-    out[j] = s;
-  }
-}
-int column_lanes(long groups) { return groups > 64 ? 32 : 8; }
-
 struct FinishPlan {
   int start[kMaxGroup + 2 + 1];     // first workgroup of each job, products first
   int lg[kMaxGroup];
@@ -90,7 +71,7 @@ __global__ __launch_bounds__(kRowThreads) void finish_sums(FinishArgs a, FinishP
   if (k < a.products) {
     sum_slices<DT, kEpiStore>(a.product[k].e, a.product[k].splits, p.lg[k], block, lds);
   } else {
-    const auto& c = a.column[k - a.products];
+    const ColumnJob& c = a.column[k - a.products];
     sum_columns(c.part, c.groups, c.cols, c.out, block, p.lanes[k - a.products], lds);
   }
 }

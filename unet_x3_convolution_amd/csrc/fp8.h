@@ -47,6 +47,8 @@ struct Gemm8Group {
   int count;
   int start[kMaxGroup8];
   Gemm8Args a[kMaxGroup8];
+  ColumnJob column;                // sums in workgroups of their own, from `columns` on; out null: none
+  int columns;
 };
 // Forward products of at most kFewRows packed rows, in one launch, or (packed false) of
 // at most kCodedRows rows of dtype, k columns at pitch g.ldq, coded on the way.
@@ -60,6 +62,7 @@ hipError_t launch_few8(const Gemm8Args& a, int k, bool packed, bool bf16, hipStr
 hipError_t launch_narrow8(const Gemm8Args& a, int k, int tile, bool bf16, hipStream_t stream);
 // kEpiLinear, and kEpiStore for a group; 16-bit results.
 hipError_t launch_gemm8(const Gemm8Args& a, int tile, bool bf16, hipStream_t stream);
-hipError_t launch_gemm8_group(const Gemm8Group& g, int blocks, int tile, bool bf16, hipStream_t stream);
+// `blocks` of the products
+hipError_t launch_gemm8_group(Gemm8Group g, int blocks, int tile, bool bf16, hipStream_t stream);
 
 }  // namespace oidn

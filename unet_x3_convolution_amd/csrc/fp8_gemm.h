@@ -14,6 +14,7 @@
 // instructions without scales do the same.
 #pragma once
 
+#include "dense_columns.h"
 #include "dense_gemm16_direct.h"
 #include "fp8.h"
 
@@ -273,9 +274,15 @@ __global__ __launch_bounds__(256, workgroups_per_cu(T, T)) void dense_gemm8(Gemm
   __shared__ __attribute__((aligned(1024))) char lds[gemm8_lds<T>()];
   gemm8<BF, kEpiLinear, T, WHERE>(a, blockIdx.x, lds);
 }
+// Products that do not depend on each other, and column sums of the pass before them.
 template <bool BF, int T>
 __global__ __launch_bounds__(256, workgroups_per_cu(T, T)) void dense_gemm8_group(Gemm8Group g) {
   __shared__ __attribute__((aligned(1024))) char lds[gemm8_lds<T>()];
+  if ((int)blockIdx.x >= g.columns) {
+    const ColumnJob& c = g.column;
+    sum_columns(c.part, c.groups, c.cols, c.out, blockIdx.x - g.columns, column_lanes(c.groups), lds);
+    return;
+  }
   const int k = g.count > 1 && (int)blockIdx.x >= g.start[1] ? 1 : 0;
   gemm8<BF, kEpiStore, T, kEither>(g.a[k], blockIdx.x - g.start[k], lds);
 }

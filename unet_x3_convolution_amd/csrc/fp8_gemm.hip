@@ -31,7 +31,9 @@ hipError_t launch_gemm8(const Gemm8Args& a, int tile, bool bf16, hipStream_t str
   else launch_tile<false>(a, tile, stream);
   return hipGetLastError();
 }
-hipError_t launch_gemm8_group(const Gemm8Group& g, int blocks, int tile, bool bf16, hipStream_t stream) {
+hipError_t launch_gemm8_group(Gemm8Group g, int blocks, int tile, bool bf16, hipStream_t stream) {
+  g.columns = blocks;
+  if (g.column.out) blocks += (int)column_blocks(g.column.groups, g.column.cols);
   if (bf16) launch_group<true>(g, blocks, tile, stream);
   else launch_group<false>(g, blocks, tile, stream);
   return hipGetLastError();
