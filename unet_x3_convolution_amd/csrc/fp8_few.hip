@@ -8,6 +8,10 @@
 // that come in 16 bits, kCodedRows at most, are coded on the way, by every workgroup for
 // itself, while the weights' loads are in flight: a thread codes eight values of each row's segment, which
 // the waves read from LDS.  The waves' sums meet in LDS and are added in wave order.
+//
+// Bound by the weights' bytes and a launch's latency: bf16 4096 -> 4096 (17 MB, 3.3 us at a
+// copy's rate) 7.0 us for one row, 8.4 to 8.8 for 2 to 4, 11.0 for 8 and 14.2 for 32 with
+// their packing; 8192 -> 8192 (67 MB) 17 us, 3.9 TB/s, where 16-bit weights take 24.8.
 #include "dense_few.h"
 #include "fp8_code.h"
 #include "fp8_gemm.h"

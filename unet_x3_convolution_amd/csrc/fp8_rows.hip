@@ -26,7 +26,7 @@ struct Cell {
 };
 // x alone, blocks along the rows.  1 << lg lanes (16 to 64) take a row's one to four
 // blocks, so that a word of scales is theirs; a wave's loads are of kPackRows rows
-// each.  Bound by memory.
+// each.  Bound by memory: 8192 x 4096 bf16 (101 MB) 18.1 us, 5.6 TB/s.
 constexpr int kPackRows = 4;
 template <int DT>
 __global__ __launch_bounds__(kPackThreads) void fp8_pack_rows(Fp8PackArgs a, int lg, int words) {
@@ -60,6 +60,9 @@ __global__ __launch_bounds__(kPackThreads) void fp8_pack_rows(Fp8PackArgs a, int
 // column's in all waves.  The turned codes pass through LDS, from where whole lines
 // leave: 16-byte unit u of column 8 c + e sits at u ^ c % 8, and every second half of
 // the columns in the neighbouring row, so that a wave's writes go to 64 banks.
+// 8192 x 4096 bf16: turned (101 MB) 20.0 us, both forms (135 MB) 26.9, 5.0 TB/s; with the slope
+// of gelu and column sums (202 MB) 52 to 58, bound by the activation's instructions.  Few
+// tiles are bound by one tile's latency, about 5 us.
 constexpr int kTileThreads = 512, kTileWaves = kTileThreads / 64, kTileRows = 4;
 struct PackLds {
   unsigned top[kTileWaves][kFp8Block];
@@ -212,9 +215,9 @@ __global__ __launch_bounds__(kTileThreads) void fp8_pack_tiles(Fp8PackArgs a, Fp
   __shared__ __attribute__((aligned(16))) PackLds lds;
   const bool second = (int)blockIdx.x >= first;
   const Fp8PackArgs& p = second ? b : a;
-  const long block = (int)blockIdx.x - (second ? first : 0), across = (p.n + kFp8Block - 1) / kFp8Block;
+  const unsigned block = blockIdx.x - (second ? first : 0), across = ((unsigned)p.n + kFp8Block - 1) / kFp8Block;
   const long tile_r = block / across;
-  const int tile_c = (int)(block - tile_r * across);
+  const int tile_c = (int)(block % across);
   if ((tile_r + 1) * kFp8Block <= p.m && (tile_c + 1) * kFp8Block <= p.n) pack_tile<DT, true, ACT>(p, tile_r, tile_c, lds);
   else pack_tile<DT, false, ACT>(p, tile_r, tile_c, lds);
 }

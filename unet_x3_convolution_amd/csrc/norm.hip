@@ -5,7 +5,10 @@
 namespace oidn {
 namespace {
 
-// A thread takes eight columns.
+// y = drop(x) + residual, rounded once.  A thread takes eight columns, the share of one call
+// of the generator (norm_rows.h).  Bound by memory: 16384 x 4096 bf16 with a residual
+// (403 MB) 68.9 us, without one (268 MB) 48.7, 5.5 TB/s (the end of the last pass's results is
+// still in the caches); 32640 x 112 fp16 4.9.
 template <int DT>
 __global__ __launch_bounds__(kNormThreads) void dropout_rows(const void* x, long ldx, const void* residual, long ldr,
                                                              void* y, long ldy, long m, int n, long units, Dropout d) {

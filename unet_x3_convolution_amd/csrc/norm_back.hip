@@ -6,16 +6,19 @@ namespace oidn {
 namespace {
 
 // Sums of partial rows: kinds 0 .. kNormSums - 1 over all chunks, then a gate
-// group's chunks.  A workgroup takes kAcross columns, its threads share the rows,
-// whose sums are added in order.  Bound by the latency of few loads at narrow rows and by
-// memory at wide ones: 16 columns and 16 lines of threads instead take 2 us more of
-// 16384 x 4096 and 6 of 4096 x 8192, and no less at 96 columns.
-constexpr int kAcross = 32, kFinishThreads = 512;
+// group's chunks.  A workgroup takes ACROSS columns, its threads share the rows,
+// whose sums are added in order.  Wide rows are bound by memory, narrow ones by the latency
+// of a thread's loads, which are made sixteen at a time (us a call, 16 and 32 columns: 16384 x
+// 4096 188 and 185, 4096 x 8192 149 and 143; 8160 x 96 fp32 14.4 and 15.3, 16384 x 128 19.6 and
+// 21.1; in turn past the last sixteen, 8160 x 96 took 18.2).
+constexpr int kFinishThreads = 512;
+inline int finish_columns(int n) { return n >= 1024 ? 32 : 16; }
+template <int ACROSS>
 __global__ __launch_bounds__(kFinishThreads) void norm_finish(NormBackArgs a) {
-  constexpr int kLines = kFinishThreads / kAcross;
+  constexpr int kLines = kFinishThreads / ACROSS;
   __shared__ float lds[kFinishThreads];
-  const int c = threadIdx.x % kAcross, l = threadIdx.x / kAcross, n = a.n;
-  const long j = (long)blockIdx.x * kAcross + c, what = blockIdx.y;
+  const int c = threadIdx.x % ACROSS, l = threadIdx.x / ACROSS, n = a.n;
+  const long j = (long)blockIdx.x * ACROSS + c, what = blockIdx.y;
   const float* p;
   float* out;
   long count, step;
@@ -34,14 +37,20 @@ __global__ __launch_bounds__(kFinishThreads) void norm_finish(NormBackArgs a) {
   if (!out) return;
   float s = 0.f;
   if (j < n) {
-#pragma unroll 16
-    for (long g = l; g < count; g += kLines) s += p[g * step + j];
+    // sixteen reads at a time, the last row in place of those past it
+    for (long g = l; g < count; g += 16 * kLines) {
+      float t[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) t[k] = p[(g + k * kLines < count ? g + k * kLines : count - 1) * step + j];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s += g + k * kLines < count ? t[k] : 0.f;
+    }
   }
   lds[threadIdx.x] = s;
   __syncthreads();
   if (l == 0 && j < n) {
 #pragma unroll
-    for (int k = 1; k < kLines; ++k) s += lds[k * kAcross + c];
+    for (int k = 1; k < kLines; ++k) s += lds[k * ACROSS + c];
     out[j] = s;
   }
 }
@@ -84,8 +93,10 @@ hipError_t launch_type(const NormBackArgs& a, hipStream_t stream) {
   const hipError_t e = hipGetLastError();
   const long groups = a.dgate && a.chunks.per_group > 1 ? a.chunks.count / a.chunks.per_group : 0;
   if (e != hipSuccess || !columns || (a.chunks.count == 1 && !groups)) return e;
-  hipLaunchKernelGGL(norm_finish, dim3((unsigned)((a.n + kAcross - 1l) / kAcross), (unsigned)(kNormSums + groups)),
-                     dim3(kFinishThreads), 0, stream, a);
+  const int across = finish_columns(a.n);
+  const dim3 grid((unsigned)((a.n + across - 1l) / across), (unsigned)(kNormSums + groups)), block(kFinishThreads);
+  if (across == 32) hipLaunchKernelGGL(norm_finish<32>, grid, block, 0, stream, a);
+  else hipLaunchKernelGGL(norm_finish<16>, grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
