@@ -288,6 +288,13 @@ def test_gate_groups(m, n, gate_rows):
     check(outs["d_o"].get(), want["d_o"], "f32", "d_o")
 
 
+@pytest.mark.parametrize("m, n, gate_rows", [(3001, 24, 1), (3001, 24, 3), (3001, 24, 5), (2600, 30, 5), (8193, 31, 16),
+                                             (1201, 96, 2), (1201, 200, 1), (1201, 200, 2), (1101, 512, 1),
+                                             (512 * 4, 64, 4), (513 * 4, 64, 4)])
+def test_many_gate_groups(m, n, gate_rows):
+    test_gate_groups(m, n, gate_rows)
+
+
 @pytest.mark.parametrize("precision", PRECISIONS)
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 @pytest.mark.parametrize("m, n", BACK)
