@@ -58,3 +58,21 @@ def test_native_calls_are_the_librarys():
     native = U.lib().oidn_last_error()
     assert status == U.lib().oidn_dropout(*args) == U.OIDN_E_INVALID
     assert native == U.lib().oidn_last_error() != b""
+
+
+def residual(scale):
+    U.oidn_norm_residual(4096, 8, None, None, None, 0, 0, 4096, 8, scale, 0.0, None, 4096, 8, None, None, None, 0, 0, 8,
+                         U.OIDN_NORM_RMS, U.OIDN_NORM_NONE, 1e-5, U.OIDN_F16, stream=0)
+
+
+@pytest.mark.parametrize("scale", [1e300, -1e300, 3.5e38, 2 ** 1000])
+def test_a_native_call_refuses_floats_past_the_range(scale):
+    """Finite numbers that would become infinities of float32."""
+    with pytest.raises(OverflowError):
+        residual(scale)
+
+
+@pytest.mark.parametrize("scale", [1, True, 3.4028235e38, float("inf"), -float("inf"), float("nan"), 1e-300])
+def test_a_native_call_takes_floats(scale):
+    """The largest, infinities and NaN as they are; what is below the range is rounded, as every number is."""
+    residual(scale)

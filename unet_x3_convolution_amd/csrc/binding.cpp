@@ -9,6 +9,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <cmath>
 #include <tuple>
 #include <type_traits>
 #include <utility>
@@ -40,8 +41,12 @@ bool convert(PyObject* o, T& out) {
     out = static_cast<T>(p);
     return true;
   } else if constexpr (std::is_floating_point_v<T>) {
-    out = static_cast<T>(PyFloat_AsDouble(o));
-    return !PyErr_Occurred();
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) return false;
+    out = static_cast<T>(v);
+    if (std::isfinite(out) || !std::isfinite(v)) return true;
+    PyErr_Format(PyExc_OverflowError, "%R does not fit the parameter", o);
+    return false;
   } else if constexpr (std::is_same_v<T, size_t>) {
     out = PyLong_AsSize_t(o);
     return !PyErr_Occurred();
