@@ -10,11 +10,15 @@ There is no fallback: if the library is not built, loading raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import math
+import operator
 import os
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liboidn_mi355x.so")
-BINDING_PATH = os.path.join(HERE, "_binding.so")
+BINDING_PATH = os.path.join(HERE, "_binding" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 OIDN_OK = 0
 OIDN_E_INVALID = -1
@@ -187,6 +191,39 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+def _converted(v, t):
+    """The argument v of a parameter of type t, refused where ctypes would cut it."""
+    if t is _vp:
+        a = None if v is None else operator.index(_p(v))
+        if a is not None and not -1 << 63 <= a < 1 << 64:
+            raise OverflowError(f"{v!r} does not fit the parameter")
+        return a
+    if t is _f:
+        c = _f(v)
+        if math.isinf(c.value) and not (isinstance(v, float) and math.isinf(v)):
+            raise OverflowError(f"{v!r} does not fit the parameter")
+        return c
+    c = t(operator.index(v))
+    if c.value != v:
+        raise OverflowError(f"{v!r} does not fit the parameter")
+    return c
+
+
+class _ThroughCtypes:
+    """The calls of csrc/binding.cpp where that is not built."""
+
+    def __getattr__(self, name):
+        f = getattr(lib(), name)
+
+        def call(*args):
+            if len(args) != len(f.argtypes):
+                raise TypeError(f"{len(args)} arguments given, {len(f.argtypes)} taken")
+            return f(*[_converted(v, t) for v, t in zip(args, f.argtypes)])
+
+        setattr(self, name, call)
+        return call
+
+
 _native = None
 
 
@@ -195,10 +232,12 @@ def _calls():
     global _native
     if _native is None:
         lib()
-        if not os.path.exists(BINDING_PATH):
-            raise OidnError(OIDN_E_HIP, f"{BINDING_PATH} is not built; run __graft_entry__.build()")
-        from . import _binding
-        _native = _binding
+        if os.path.exists(BINDING_PATH):
+            from . import _binding
+            _native = _binding
+        else:
+            warnings.warn(f"{BINDING_PATH} is not built: calls go through ctypes and take longer", RuntimeWarning)
+            _native = _ThroughCtypes()
     return _native
 
 

@@ -9,13 +9,14 @@ import os
 import subprocess
 import sys
 import sysconfig
+from importlib.machinery import EXTENSION_SUFFIXES
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "liboidn_mi355x.so")
-BINDING = os.path.join(HERE, "_binding.so")
+BINDING = os.path.join(HERE, "_binding" + EXTENSION_SUFFIXES[0])      # of this Python's ABI
 SOURCES = ["api.cpp", "conv_f16.hip", "conv_f32.hip", "elementwise.hip", "noalloc.hip",
            "calibrate.hip", "dense_api.cpp", "dense_rows.hip", "dense_gemm16_forward.hip",
            "dense_gemm16_gated_back.hip", "dense_gemm16_group.hip", "dense_gemm32.hip", "dense_few.hip", "dense_narrow.hip",
@@ -23,8 +24,8 @@ SOURCES = ["api.cpp", "conv_f16.hip", "conv_f32.hip", "elementwise.hip", "noallo
            "fp8_few.hip", "fp8_narrow.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-CXX = os.environ.get("CXX", "g++")
 ROCM_INCLUDE = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")
+PYTHON_INCLUDE = sysconfig.get_paths()["include"]
 # Packed-fp32 ops are turned off for the device code: plain fp32 arithmetic only.
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -51,10 +52,18 @@ def _compile(src: str) -> str:
 
 
 def _binding() -> None:
-    """The Python calls of csrc/binding.cpp, on the library beside them."""
+    """The Python calls of csrc/binding.cpp, on the library beside them.  Without Python's headers there
+    are none, and the package calls the library through ctypes, which takes more of the host's time."""
+    if not os.path.exists(os.path.join(PYTHON_INCLUDE, "Python.h")):
+        sys.stderr.write(f"no Python.h in {PYTHON_INCLUDE}: {os.path.basename(BINDING)} is not built, "
+                         "its calls go through ctypes\n")
+        if os.path.exists(BINDING):      # an earlier library's
+            os.remove(BINDING)
+        return
     tmp = BINDING + ".tmp"
-    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
-           "-I", sysconfig.get_paths()["include"], "-isystem", ROCM_INCLUDE, os.path.join(CSRC, "binding.cpp"),
+    # host code alone; the HIP runtime is the library's
+    cmd = [HIPCC, "-x", "c++", "-no-hip-rt", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           "-I", PYTHON_INCLUDE, "-isystem", ROCM_INCLUDE, os.path.join(CSRC, "binding.cpp"),
            "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
