@@ -493,8 +493,11 @@ int oidn_fp8_unpack(const void* packed, long m, long n, void* y, long ldy, int d
  *   z = [x] [w]^T + bias,  y = act(z) + residual,  [.] the packed form's values
  * w8: the packed weights (n x k).  x: m x k of dtype, packed inside, or with
  * OIDN_X_FP8 a packed matrix.  dtype: OIDN_F16 or OIDN_BF16.  The products of codes
- * are added eight at a time with 13 bits below the largest, those sums in fp32:
- * 1e-5 to 4e-5 of the result, far below the storage type's rounding.
+ * are added eight neighbours at a time, and what lies below 2^-13 of the largest one's
+ * power of two is cut off: each eight is off by less than 7 2^-13 of its largest product.
+ * Those sums are added in fp32.  Of normal data 1e-5 to 4e-5 of a result, far below the
+ * storage type's rounding; where large products cancel it may be all of what is left
+ * (oidn_linear adds in fp32 throughout).
  * k, n <= 2^23.  The rest is as for oidn_linear. */
 int oidn_linear_fp8_workspace_bytes(long m, int k, int n, int dtype, unsigned flags, size_t* bytes);
 int oidn_linear_fp8(const void* x, long ldx, const void* w8, const float* bias, const void* residual,
