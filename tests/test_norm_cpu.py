@@ -148,3 +148,23 @@ def test_no_rows_enqueue_nothing():
     norm_backward(m=0, dy=None, x=None, dweight=None, dshift=None, workspace=None)
     residual_backward(m=0, du=None, dv=None, o=None, u=None, dweight=None, dshift=None, dnext_weight=None,
                       dnext_shift=None, workspace=None)
+
+
+@pytest.mark.parametrize("m, n, gate_rows, most", [
+    (65536, 32, 65, 1024), (131072, 64, 65, 2048), (16384, 4096, 33, 512), (8192, 8192, 17, 512), (4096, 8256, 9, 512),
+    (130560, 32, 170, 768), (16384, 640, 17, 1024), (16384, 640, 40, 1536), (16384, 2048, 48, 768), (16384, 4096, 0, 512),
+    (16384, 1024, 0, 1024), (1 << 20, 64, 0, 768), (1 << 20, 4096, 1, 1024)])
+def test_sums_are_over_few_chunks(m, n, gate_rows, most):
+    """A chunk of rows leaves four rows of partial sums, and one of a gate's where a group has several chunks."""
+    assert U.oidn_norm_residual_backward_workspace_bytes(m, n, gate_rows, U.OIDN_F16) - (m * 32 if n > 8192 else 0) <= (
+        most * 4 * n * 4 + (most * n * 4 if gate_rows > m // most else 0) + 512)
+
+
+@pytest.mark.parametrize("groups, rows, n, lanes", [(1024, 8, 32, False), (1024, 16, 32, False), (1536, 8, 32, True),
+                                                    (512, 16, 32, False), (1024, 4, 96, True), (768, 4, 96, False),
+                                                    (512, 1, 32, True), (2800, 16, 32, True)])
+def test_gate_groups_of_few_rows(groups, rows, n, lanes):
+    """A workgroup each, or a row lane each, of 64 (up to 32 columns) or 16 (96)."""
+    at_once = 64 if n <= 32 else 16
+    chunks = -(-groups // at_once) if lanes else groups
+    assert U.oidn_norm_residual_backward_workspace_bytes(groups * rows, n, rows, U.OIDN_F16) == -(-chunks * 16 * n // 256) * 256

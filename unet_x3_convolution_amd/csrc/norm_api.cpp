@@ -50,7 +50,7 @@ BackSpace back_space(long m, int n, long gate_rows, void* ws) {
   auto floats = [&](size_t count) { return static_cast<float*>(r.take(align256(count * sizeof(float)))); };
   if (!norm_lanes(n)) b.rows = floats((size_t)m * kRowFloats);
   if (b.chunks.count > 1) b.part = floats((size_t)b.chunks.count * kNormSums * n);
-  if (gate_rows && b.chunks.per_group > 1) b.gate_part = floats((size_t)b.chunks.count * n);
+  if (gate_rows && b.chunks.per_group) b.gate_part = floats((size_t)b.chunks.count * n);
   b.bytes = r.used;
   return b;
 }

@@ -91,7 +91,7 @@ hipError_t launch_type(const NormBackArgs& a, hipStream_t stream) {
     }
   }
   const hipError_t e = hipGetLastError();
-  const long groups = a.dgate && a.chunks.per_group > 1 ? a.chunks.count / a.chunks.per_group : 0;
+  const long groups = a.dgate && a.chunks.per_group ? a.chunks.count / a.chunks.per_group : 0;
   if (e != hipSuccess || !columns || (a.chunks.count == 1 && !groups)) return e;
   const int across = finish_columns(a.n);
   const dim3 grid((unsigned)((a.n + across - 1l) / across), (unsigned)(kNormSums + groups)), block(kFinishThreads);
@@ -102,31 +102,50 @@ hipError_t launch_type(const NormBackArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Chunks enough to fill the device, and few enough that the sums over them stay a short
-// pass: at most about 1024, half of that where a workgroup takes one row at a time.
+// Chunks enough to fill the device once, and few enough that the sums over them stay a
+// short pass.  us, both norms, gate and dropout, at 512, 768 and 1024 chunks: 65536 rows of
+// 400 fp16 columns 98, 90 and 103 (so 768 up to 512 columns), 16384 bf16 rows of 1024 84, 64 and
+// 59 (1024 up to there), of 2048 95, 97 and 96, of 4096 183, 186 and 198 (512 from there on;
+// 1032 columns alone would gain by more, 86, 79 and 75).
+//
+// A gate's groups of more rows than such a chunk are parted only while all their chunks
+// fit the device together (1.5 times as many of 128 and 256 lanes), as one that runs after the
+// others costs a chunk's whole time, and parts' sums a workgroup for every group and 16
+// or 32 columns.  us, in one part and in as many as the rows ask for: 65536 rows of 32 fp16
+// columns, groups of 65 24.6 and 29.7; 16384 x 4096, of 33 186 and 295, of 200 in 3 parts and 7
+// 203 and 249; 16384 x 600, of 40 in 2 parts and 3 98 and 82; 16384 x 2048, of 48 149 and 135.
+// Groups of fewer rows come several to a chunk, as many as it holds: less than twice the
+// chunks named.
 NormChunks norm_chunks(long m, int n, long gate_rows) {
   NormChunks c{};
-  const long at_once = norm_row_lanes(n), target = at_once > 1 ? 1024 : 512;
+  const int lanes = norm_lanes(n);
+  const long step = norm_chunk_step(n), target = lanes && lanes <= 64 ? 768 : lanes == 128 ? 1024 : 512,
+             together = lanes == 128 || lanes == 256 ? target * 3 / 2 : target;
   long most = (m + target - 1) / target;
-  if (most < at_once) most = at_once;
+  if (most < step) most = step;
   c.group_rows = gate_rows && gate_rows < m ? gate_rows : m;
-  if (c.group_rows <= most) {
-    // A group of so few rows leaves most of a workgroup's row lanes without one: where there
-    // are many such groups, row lanes take one each, whose rows they add one after another;
-    // where there are few, a workgroup takes one (us, lanes and workgroups: 512 groups of 16
-    // rows of 32 fp16 columns 35.7 and 12.9, 1024 of 8 rows 21.9 and 19.7, 1024 of 4 rows of 96
-    // columns 16.3 and 19.1).
-    const bool few_rows = c.group_rows * 4 <= at_once, few = (m + c.group_rows - 1) / c.group_rows <= 512;
-    c.lane_groups = few_rows && !few;
-    const long least = c.lane_groups ? at_once * c.group_rows : 0, rows = most > least ? most : least;
-    c.rows = few_rows && few ? c.group_rows : rows / c.group_rows * c.group_rows;
-    c.count = (m + c.rows - 1) / c.rows;
-  } else {
-    const long parts = (c.group_rows + most - 1) / most;
-    c.rows = ((c.group_rows + parts - 1) / parts + at_once - 1) / at_once * at_once;
+  const long groups = (m + c.group_rows - 1) / c.group_rows, asked = (c.group_rows + most - 1) / most;
+  const long parts = asked * groups <= together ? asked : together / groups;
+  if (parts > 1) {
+    c.rows = ((c.group_rows + parts - 1) / parts + step - 1) / step * step;
     c.per_group = (c.group_rows + c.rows - 1) / c.rows;
-    c.count = (m + c.group_rows - 1) / c.group_rows * c.per_group;
+    c.count = groups * c.per_group;
+    return c;
   }
+  // A group of so few rows leaves most of a workgroup's row lanes without one.  Either row
+  // lanes take a group each, whose rows they add one after another (about 7 us and 1.6 for
+  // each row), or a workgroup takes one (6 us and one for each 100 groups).  us, lanes and
+  // workgroups, 32 fp16 columns: 1 row, 256 groups 8.8 and 9.7; 2 rows, 256 groups 10.3 and 9.6,
+  // 512 10.4 and 10.9; 4 rows, 768 groups 13.8 and 13.5, 1024 13.7 and 16.4; 8 rows, 1024 groups
+  // 21.7 and 19.1, 1536 22.1 and 23.8; 16 rows, 1024 groups 35.2 and 19.4.  96 columns: 4 rows,
+  // 768 groups 15.7 and 14.9, 1024 15.8 and 18.8.
+  const bool few_rows = c.group_rows * 4 <= step;
+  c.lane_groups = few_rows && groups > 160 * (c.group_rows + 1);
+  long held = few_rows && !c.lane_groups ? 1 : most / c.group_rows;
+  if (c.lane_groups && held < step) held = step;
+  if (held < 1) held = 1;
+  c.rows = held * c.group_rows;
+  c.count = (m + c.rows - 1) / c.rows;
   return c;
 }
 

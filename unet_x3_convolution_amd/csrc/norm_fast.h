@@ -397,8 +397,7 @@ __global__ __launch_bounds__(norm_threads<LANES>(), LANES >= 128 && !SHIFTS ? 4 
     }
     for (long r = begin; r < end; r += lanes, i += lanes) row(i, i < end, r + lanes < end ? i + lanes : -1);
     if (BRANCH && a.dgate) {
-      float* const out = c.per_group > 1 ? a.gate_part + chunk * n
-                                         : a.dgate + (c.per_group ? group : begin / c.group_rows) * a.lddg;
+      float* const out = c.per_group ? a.gate_part + chunk * n : a.dgate + begin / c.group_rows * a.lddg;
       if (alone || LANES > 64) {
         if (begin < end || !alone) put8<OIDN_F32, WHOLE>(out, j, gate_sum, left);
       } else {

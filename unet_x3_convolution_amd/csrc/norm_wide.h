@@ -258,8 +258,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_columns(NormBackArgs a) {
 #pragma unroll
   for (int k = 0; k < kNormSums; ++k)
     if (a.sums[k]) store8<OIDN_F32>(c.count > 1 ? a.part + (chunk * kNormSums + k) * n : a.sums[k], j, sums[k], n - j);
-  if (a.dgate && c.per_group)
-    store8<OIDN_F32>(c.per_group > 1 ? a.gate_part + chunk * n : a.dgate + chunk * a.lddg, j, gate_sum, n - j);
+  if (a.dgate && c.per_group) store8<OIDN_F32>(a.gate_part + chunk * n, j, gate_sum, n - j);
 }
 
 }  // namespace
