@@ -105,8 +105,13 @@ Forward forward(long m, int k, int n, int act, unsigned flags, void* ws) {
   f.pack = !x8 && !f.narrow && m > kCodedRows;
   Product8* one = &f.p;
   if (f.narrow) {
-    // one staged tile: 128 x 128 where they fill the units
-    const int tile = ((m + 127) / 128) * ((n + 127l) / 128) >= 512 ? 128 : 64;
+    // one staged tile: 128 x 128 where they fill the units and none is half empty (us, 64 x 64
+    // and 128 x 128: 16384 x 128 -> 512 with gelu 17.7 and 16.4, 32640 x 96 -> 1024 plain 34.4 and
+    // 31.8; 384 tiles, 16384 x 96 -> 384 with gelu 14.7 and 16.0; half empty ones, 65536 x 64 ->
+    // 64 11.4 and 15.7, 130560 x 96 -> 160 43 and 55, 65536 x 96 -> 448 53 and 57; from 1500
+    // tiles on they are even with an activation, and 0 to 8% ahead without)
+    const bool whole = (n + 63l) / 64 % 2 == 0;
+    const int tile = whole && ((m + 127) / 128) * ((n + 127l) / 128) >= 512 ? 128 : 64;
     f.p.plan = GemmPlan{tile, tile, false, true, 1, 4};
   } else if (f.few) f.p.plan = GemmPlan{64, 64, true, true, 1, 0};
   else plan_together(&one, 1);
