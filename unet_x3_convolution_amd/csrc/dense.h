@@ -95,7 +95,7 @@ constexpr int kDenseKF32 = 32;   // the same in fp32
 struct PlanShape {
   long rows, cols, len;
   int epi;
-  double extra;            // us that an activation adds to a 256 x 256 tile's epilogue, if that is to count
+  double extra;            // us of a 256 x 256 tile's epilogue beyond the table's (plan_products)
 };
 constexpr int kMaxGroup = 3;
 void plan_products(GemmPlan* const* plans, const PlanShape* shapes, int count, int dtype, bool direct);

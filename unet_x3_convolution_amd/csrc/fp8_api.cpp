@@ -44,11 +44,15 @@ void plan_together(Product8* const* p, int count) {
   PlanShape shapes[kMaxGroup8];
   for (int k = 0; k < count; ++k) {
     plans[k] = &p[k]->plan;
-    // A 256 x 256 tile's activation stands beside a loop half as long as a 16-bit product's
-    // (us, 256 x 256 against 128 x 128: 8192 x 1024 -> 4096 plain 49 and 49, gelu 68 and 61; 8192
-    // x 4096 -> 4096 gelu 132 and 140).
-    const double extra[] = {0, 2, 5, 10};      // none, relu, silu, gelu
-    shapes[k] = {p[k]->rows, p[k]->cols, p[k]->len / 2, kEpiStore, extra[p[k]->act]};
+    // A 256 x 256 tile's epilogue stands beside a loop half as long as a 16-bit product's: fitted
+    // to 8192 x 512 to 4096 -> 4096 (us, 256 x 256 against 128 x 128, none, relu, silu, gelu: 512
+    // 40 and 37, 43 and 37, 47 and 40, 58 and 48; 1024 52 and 51, 56 and 53, 62 and 56, 72 and 64;
+    // 2048 75 and 78, 79 and 79, 84 and 83, 94 and 89; 4096 119 and 131, 123 and 132, 129 and 136,
+    // 136 and 139).  Of 200 layers (2048 to 32640 rows, 256 to 4096 inputs, 448 to 8192 outputs)
+    // four got a tile that is over 3% slower than with 0, 2, 5, 10 (32640 x 4096 -> 448 with gelu 90
+    // for 80), 60 a faster one (32640 x 1024 -> 448 28 for 44).
+    const double extra[] = {7.5, 11.5, 14, 18.5};      // none, relu, silu, gelu
+    shapes[k] = {p[k]->rows, p[k]->cols, p[k]->len / 2, kEpiStore, count == 1 ? extra[p[k]->act] : 0};
   }
   plan_products(plans, shapes, count, OIDN_F16, true);
   for (int k = 0; k < count; ++k) {
