@@ -498,6 +498,9 @@ int oidn_fp8_unpack(const void* packed, long m, long n, void* y, long ldy, int d
  * Those sums are added in fp32.  Of normal data 1e-5 to 4e-5 of a result, far below the
  * storage type's rounding; where large products cancel it may be all of what is left
  * (oidn_linear adds in fp32 throughout).
+ * Faster than oidn_linear where a layer is large (8192 -> 8192 at any rows, 4096 -> 4096
+ * from 512 rows on) or x is packed already; no faster up to 1024 -> 1024 with x not packed,
+ * and slower with at most 128 inputs.
  * k, n <= 2^23.  The rest is as for oidn_linear. */
 int oidn_linear_fp8_workspace_bytes(long m, int k, int n, int dtype, unsigned flags, size_t* bytes);
 int oidn_linear_fp8(const void* x, long ldx, const void* w8, const float* bias, const void* residual,
@@ -523,8 +526,9 @@ int oidn_linear_fp8_backward(const void* dy, long lddy, const void* x, long ldx,
  * Matrices, pitches and types are as above; weights, shifts, gates and their
  * gradients are float32.  Statistics and sums are fp32; every output is rounded
  * once.  Rows of n columns, each by itself: a NaN or an infinity stays in its row.
- * A row whose sum of squares passes the range of float32 becomes zeros or NaN; so
- * does a row of equal values (of zeros, with OIDN_NORM_RMS) where eps is 0.
+ * A row whose sum of squares passes the range of float32 becomes zeros or NaN; so,
+ * where eps is 0, does one whose sum falls below it, as of equal values (of zeros, with
+ * OIDN_NORM_RMS).
  * In place: y of oidn_norm may be x, u may be x or o, y of oidn_dropout may be x
  * or the residual, add may be dx (same pitch).
  * ======================================================================== */

@@ -11,7 +11,9 @@
 //
 // Bound by the weights' bytes and a launch's latency: bf16 4096 -> 4096 (17 MB, 3.3 us at a
 // copy's rate) 7.0 us for one row, 8.4 to 8.8 for 2 to 4, 11.0 for 8 and 14.2 for 32 with
-// their packing; 8192 -> 8192 (67 MB) 17 us, 3.9 TB/s, where 16-bit weights take 24.8.
+// their packing; 8192 -> 8192 (67 MB) 17 us, 3.9 TB/s.  16-bit weights take 7.0, 8.2 (4 rows),
+// 9.3 (8), 13.9 (32) and 24.8: 4096 -> 4096 gains only where x is packed already (8 rows 8.2, 32
+// 10.0 to 11.0), smaller layers nothing (1024 -> 1024, one row 5.6 for 3.1).
 #include "dense_few.h"
 #include "fp8_code.h"
 #include "fp8_gemm.h"

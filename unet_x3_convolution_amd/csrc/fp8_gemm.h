@@ -80,10 +80,12 @@ __device__ __forceinline__ void copy4(const void* base, unsigned off, unsigned l
 // read or a copy, then a multiplication, under whose 32 cycles the next one issues.
 //
 // Bound by the matrix cores (64% of the cycles busy, at the clock that random data leaves):
-// bf16, 8192 cubed 2520 TFLOP/s, 8192 x 4096 -> 4096 109 us (2520), with gelu and residual
-// 135, as 256 x 256 tiles leave one wave a SIMD and the epilogue stands alone.  All of a
-// tile's fragments held in registers spilled (1030 us against 186 for the last with
-// packing); reads and copies grouped instead of spread reached 2440 TFLOP/s.
+// bf16, by card and pace 8192 cubed 2430 to 2690 TFLOP/s (a library product with one scale a
+// matrix 3200 beside the last), 8192 x 4096 -> 4096 112 to 127 us (94 to 108); gelu adds 18 us to
+// that, a residual 10, both 25, as 256 x 256 tiles leave one wave a SIMD and the epilogue stands
+// alone.  All of a tile's fragments held in registers spilled (1030 us against 186 for the
+// layer with both and packing); reads and copies grouped instead of spread reached 2440
+// TFLOP/s where these reached 2520.
 template <bool BF, int EPI, int T, Caching WHERE>
 __device__ __forceinline__ void gemm8(const Gemm8Args& a8, int block, char* lds) {
   const GemmArgs& a = a8.g;

@@ -201,9 +201,15 @@ __global__ __launch_bounds__(norm_threads<LANES>()) void norm_rows(NormArgs a) {
 // but what the forward pass returns is kept.  16384 x 4096 bf16, both norms, gate and
 // dropout (805 MB): 185 us, 4.4 TB/s, of which the sums over chunks take 10 (norm_finish).
 // The registers decide: five column sums, three of a row's matrices and the next row's
-// loads.  Weights from LDS instead of registers 254 -> 197 us, four waves a unit for rows of
-// more than a wave 199 -> 187; held to 128 registers everywhere it spills (236).  All sums
-// are added in a fixed order: results do not depend on timing.
+// loads.  Weights from LDS instead of registers 254 -> 197 us.  Without the shifts' sums rows of
+// more than a wave are held to 128 registers, four waves a unit, 199 -> 187, though 8 spill (fp32
+// 17); with them that spills more than it gains (236 us), except that a workgroup of 1024
+// threads has no more registers: there 41 and 66 spill, 53 and 143 at odd widths (4000 x 6091
+// fp32 376 us).  All sums are added in a fixed order: results do not depend on timing.
+//
+// A norm's gradients by themselves, without a branch: 16384 x 4096 bf16 91 us (403 MB, 4.4 TB/s),
+// with another gradient added 120 (537 MB, 4.5); 4096 x 8192 58, 4000 x 6091 59 (fp32 76); few
+// rows by latency, 130560 x 32 fp16 13, 8160 x 96 fp32 8.2, one row of 4096 4.1.
 //
 // A row lane is the LANES threads of a row.  Column sums stay in registers over a
 // chunk's rows and are added over the row lanes at its end; a gate's, where chunks hold
