@@ -10,6 +10,14 @@ import unet_x3_convolution_amd as U
 from unet_x3_convolution_amd import build
 
 
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not os.path.exists(U.LIB_PATH):
+        build.build(verbose=False)
+    elif not os.path.exists(U.BINDING_PATH):
+        build._binding()
+
+
 @pytest.fixture
 def absent(monkeypatch, tmp_path):
     U.lib()
@@ -92,5 +100,6 @@ def test_unsigned_and_sizes(absent):
 
 def test_both_ways_refuse_alike():
     """The same wrong numbers by the C++ calls, where they are built."""
-    assert os.path.exists(U.BINDING_PATH)
+    if not os.path.exists(U.BINDING_PATH):
+        pytest.skip("Python's headers are missing")
     test_unsigned_and_sizes(None)

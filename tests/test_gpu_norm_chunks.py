@@ -51,7 +51,7 @@ def test_gradients_over_several_rows(m, n, gate_rows):
 
 
 @pytest.mark.parametrize("m, n, gate_rows", [(1020, 4096, 5), (1020, 4099, 5), (1020, 8200, 5), (44000, 30, 16),
-                                             (12003, 30, 8), (900, 56, 1), (3001, 120, 2), (5003, 24, 4)])
+                                             (12003, 30, 8), (900, 56, 1), (3001, 120, 2), (5003, 24, 4), (66000, 24, 1)])
 def test_gradients_of_parted_and_shared_groups(m, n, gate_rows):
     """Groups in fewer parts than their rows ask for; groups of few rows, one a row lane and one a workgroup."""
     test_gradients_over_several_rows(m, n, gate_rows)
